@@ -240,11 +240,131 @@ nf4_status nf4_linear_host_noalloc(const uint16_t* x, const uint8_t* codes, cons
                                    int64_t M, int64_t N, int64_t K, cudaStream_t stream);
 
 /*
+ * Operators around the linears of a decoder layer: rotary positions, a paged key-value cache that
+ * quantises what it is given, the attention of one new token over it, and the residual norm.  With
+ * nf4_linear_grouped (q|k|v, gate|up) and nf4_linear (o, down) they make one decode step of a
+ * layer: norm, q|k|v, rope, append, attention, o, norm, gate|up, down.  The pages describe such a
+ * layer's linears only; the formulas below define the rest.  The common rules above hold.
+ */
+
+/*
+ * nf4_kv_cache - a paged key-value cache in the caller's memory (a description passed by pointer and
+ * read before the call returns; the library keeps nothing of it).  K and V are each
+ * [pages][kv_heads][page_size] vectors of head_dim values; place `slot` = page * page_size + offset
+ * holds one token's vectors of every kv head.  Formats, x being a vector of head_dim bf16 values:
+ *   NF4_KV_BF16  the values (2 head_dim bytes); no scales
+ *   NF4_KV_FP8   e4m3 codes (head_dim bytes), code = e4m3_rn(fp32(x / s)) saturated at +-448, and one
+ *                fp32 scale s = fp32(max |x| / 448) a vector; value = code * s; s = 0: code 0
+ *   NF4_KV_NF4   the library's NF4 format along head_dim: head_dim/2 bytes of codes and head_dim/64
+ *                fp16 scales, bit for bit what nf4_quantize gives for the same values
+ */
+typedef enum nf4_kv_format { NF4_KV_BF16 = 0, NF4_KV_FP8 = 1, NF4_KV_NF4 = 2 } nf4_kv_format;
+
+typedef struct nf4_kv_cache {
+    void* k;        /* device, [pages][kv_heads][page_size][bytes of a vector] */
+    void* v;        /* the same for the values */
+    void* k_scales; /* device: NULL (BF16), float [pages][kv_heads][page_size] (FP8) or
+                       fp16 bits [pages][kv_heads][page_size][head_dim/64] (NF4) */
+    void* v_scales;
+    int64_t pages;     /* 0 .. 2^31-1 */
+    int32_t kv_heads;  /* 1 .. 65535 */
+    int32_t page_size; /* tokens a page: a multiple of 16, up to 65536 */
+    int32_t head_dim;  /* 64, 128 or 256 */
+    int32_t format;    /* an nf4_kv_format */
+} nf4_kv_cache;
+
+/*
+ * nf4_kv_append - write T tokens' keys and values into the cache, quantised to its format.
+ *   cache  k, v and the scales are written at the given places only
+ *   k, v   in   bf16 bits [T][kv_heads][head_dim]
+ *   slots  in   int64 [T]: the place of each token; a negative slot skips its token (a padded row of
+ *               a batch); a slot >= pages * page_size is skipped and records code 42 in the device
+ *               error word.  The slots that are not skipped must be distinct: two tokens written to
+ *               one place leave an unspecified mix.
+ * Errors: NF4_ERR_SHAPE also for a format, head_dim, page_size or kv_heads outside the lists above.
+ */
+nf4_status nf4_kv_append(const nf4_kv_cache* cache, const uint16_t* k, const uint16_t* v, const int64_t* slots,
+                         int64_t T, cudaStream_t stream);
+
+/*
+ * nf4_kv_read - read T tokens' keys and values back as bf16, bf16_rn(fp32(code value * scale)).
+ *   slots  in   int64 [T], in any order, repeats allowed; a negative slot gives zeros; a slot
+ *               >= pages * page_size gives zeros and records code 42
+ *   k, v   out  bf16 bits [T][kv_heads][head_dim]; either may be NULL (not read then)
+ */
+nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v,
+                       cudaStream_t stream);
+
+/*
+ * nf4_attention_decode - attention of one new token a sequence over the cache:
+ *   out[b][h] = sum_j p_j v_j,  p = softmax_j(scale * q[b][h] . k_j),
+ * j over places max(0, lengths[b] - window) .. lengths[b] - 1 of sequence b (window = 0: from 0),
+ * k_j and v_j the cache's values (not rounded to bf16) of kv head h / (q_heads / kv_heads); place j
+ * is in page page_table[b][j / page_size].  A sequence with nothing to attend to gives zeros.  The
+ * new token's own key and value are in the cache before the call.
+ *   q           in   bf16 bits [B][q_heads][head_dim]; q_heads a multiple of kv_heads
+ *   page_table  in   int32 [B][max_pages]; entries past a sequence's length are not read
+ *   lengths     in   int32 [B]; a negative length counts as 0.  A length past max_pages * page_size is
+ *                    cut there, and a needed page outside [0, pages) is left out of the sum; both
+ *                    record code 43 in the device error word.
+ *   out         out  bf16 bits [B][q_heads][head_dim]
+ *   workspace   nf4_attention_workspace_bytes(cache, B, q_heads) bytes on the device, for the partial
+ *               results of sequences that are split.  It must be zero before its first use; every
+ *               call leaves it fit for the next one.  Calls that may overlap on the GPU need a
+ *               workspace each; one workspace serves calls of different sizes as long as it is large
+ *               enough for each.
+ * Values in places that are not attended to (past a length, before the window) do not matter, NaN
+ * and infinities included.  Memory of workspace_bytes below the need: NF4_ERR_SHAPE.
+ */
+int64_t nf4_attention_workspace_bytes(const nf4_kv_cache* cache, int64_t B, int64_t q_heads);
+nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, const int32_t* page_table,
+                                int64_t max_pages, const int32_t* lengths, int64_t B, int64_t q_heads, float scale,
+                                int64_t window, uint16_t* out, void* workspace, int64_t workspace_bytes,
+                                cudaStream_t stream);
+
+/*
+ * nf4_rope - rotary positions with up to four axes (one for text; time, height and width for images
+ * and video) on q and k in one launch.  Pair i < rotary_dim / 2 of a head is elements (i, i +
+ * rotary_dim/2), or (2i, 2i + 1) when `interleaved`; its angle is positions[a][t] * inv_freq[i] as a
+ * real product (reduced exactly, at any position), a being the axis of the run of `sections` that
+ * i falls in.  (x, y) becomes (x cos - y sin, y cos + x sin) * magnitude in fp32, rounded once to
+ * bf16; elements past rotary_dim are copied.
+ *   q, k           in   bf16 bits [T][q_heads][head_dim], [T][k_heads][head_dim]; either head count may
+ *                       be 0 (its pointers are not used)
+ *   positions      in   int32 [axes][T]
+ *   sections       in   host array of `axes` (1..4) counts of pairs, each >= 0, sum rotary_dim / 2
+ *   inv_freq       in   float [rotary_dim / 2] (finite)
+ *   rotary_dim     a multiple of 16, at most head_dim and 256; head_dim a multiple of 16, and
+ *                  (q_heads + k_heads) * head_dim at most 2^24
+ *   q_out, k_out   out  the same shapes; each may be its own input (in place), no other overlap
+ */
+nf4_status nf4_rope(const uint16_t* q, int64_t q_heads, const uint16_t* k, int64_t k_heads, int64_t T, int64_t head_dim,
+                    const int32_t* positions, int axes, const int32_t* sections, const float* inv_freq,
+                    int64_t rotary_dim, int interleaved, float magnitude, uint16_t* q_out, uint16_t* k_out,
+                    cudaStream_t stream);
+
+/*
+ * nf4_rmsnorm - root-mean-square norm with the residual's addition: h = x + residual in fp32 (h = x
+ * without one), residual_out = bf16_rn(h), y = h * rsqrt(mean(h^2) + eps) * weight in fp32, written as
+ * bf16 (y, what nf4_linear reads) and / or in 8 bits: y8 = e4m3_rn(y / s) saturated at +-448 with one
+ * fp32 scale s = max |y| / 448 a row (an all-zero row: s = 0, codes 0).
+ *   x, residual    in   bf16 bits [T][H], H a positive multiple of 8; residual may be NULL
+ *   weight         in   bf16 bits [H]
+ *   residual_out   out  bf16 bits [T][H] or NULL; may be residual or x itself
+ *   y              out  bf16 bits [T][H] or NULL; may be x itself
+ *   y8, y8_scales  out  e4m3 codes [T][H] and float [T], or both NULL; y or y8 must be given
+ */
+nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int64_t H,
+                       float eps, uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y8_scales,
+                       cudaStream_t stream);
+
+/*
  * nf4_check_device_error - diagnostics: read and clear the device-side error words of the current
  * device.  The linear kernels bound every pipeline wait (one second of wall-clock time per wait,
  * see nf4_diag_set_wait_limit); a wait that runs out records a nonzero code (1..39; 39 is
  * nf4_diag_bounded_wait's), and the kernel drains and exits instead of hanging, leaving its outputs
- * unspecified.  nf4_embed records 41 for an id outside the table.  *code receives the first
+ * unspecified.  nf4_embed records 41 for an id outside the table, the cache calls 42 for a slot
+ * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds.  *code receives the first
  * recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
  */
 nf4_status nf4_check_device_error(int* code);

@@ -24,7 +24,8 @@ STATUS_NAMES = {0: "NF4_OK", 1: "NF4_ERR_NULL", 2: "NF4_ERR_SHAPE", 3: "NF4_ERR_
 
 # Every symbol include/nf4.h declares.
 EXPORTED = ("nf4_quantize", "nf4_dequant", "nf4_linear", "nf4_linear_grouped", "nf4_embed",
-            "nf4_ring_create", "nf4_ring_run", "nf4_ring_destroy", "nf4_linear_host_noalloc",
+            "nf4_kv_append", "nf4_kv_read", "nf4_attention_workspace_bytes", "nf4_attention_decode", "nf4_rope",
+            "nf4_rmsnorm", "nf4_ring_create", "nf4_ring_run", "nf4_ring_destroy", "nf4_linear_host_noalloc",
             "nf4_check_device_error", "nf4_diag_bounded_wait", "nf4_diag_set_wait_limit", "nf4_status_str",
             "nf4_abi_version", "nf4_noalloc_slot_bytes", "nf4_last_cuda_error")
 
@@ -65,6 +66,19 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nf4_linear_grouped.restype = ci
     lib.nf4_embed.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp]
     lib.nf4_embed.restype = ci
+    cf = ctypes.c_float
+    lib.nf4_kv_append.argtypes = [vp, vp, vp, vp, i64, vp]
+    lib.nf4_kv_append.restype = ci
+    lib.nf4_kv_read.argtypes = [vp, vp, i64, vp, vp, vp]
+    lib.nf4_kv_read.restype = ci
+    lib.nf4_attention_workspace_bytes.argtypes = [vp, i64, i64]
+    lib.nf4_attention_workspace_bytes.restype = i64
+    lib.nf4_attention_decode.argtypes = [vp, vp, vp, i64, vp, i64, i64, cf, i64, vp, vp, i64, vp]
+    lib.nf4_attention_decode.restype = ci
+    lib.nf4_rope.argtypes = [vp, i64, vp, i64, i64, i64, vp, ci, vp, vp, i64, ci, cf, vp, vp, vp]
+    lib.nf4_rope.restype = ci
+    lib.nf4_rmsnorm.argtypes = [vp, vp, vp, i64, i64, cf, vp, vp, vp, vp, vp]
+    lib.nf4_rmsnorm.restype = ci
     lib.nf4_ring_create.argtypes = [i64, ctypes.POINTER(ctypes.c_void_p)]
     lib.nf4_ring_create.restype = ci
     lib.nf4_ring_run.argtypes = [vp, vp, i64, vp]
@@ -245,7 +259,216 @@ def nf4_check_device_error() -> int:
     return code.value
 
 
+# ---------------------------------------------------------------------------------------------
+# Operators around the linears of a decoder layer
+# ---------------------------------------------------------------------------------------------
+KV_FORMATS = {"bf16": 0, "fp8": 1, "nf4": 2}
+
+
+class _KvCacheStruct(ctypes.Structure):
+    """nf4_kv_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+def _expect(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """The address of a contiguous CUDA tensor of exactly this type and shape (or ValueError)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: want a CUDA tensor")
+    return t.data_ptr()
+
+
+def _current(stream) -> int:
+    """The raw handle of `stream`, or of the current device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+class KVCache:
+    """A paged key-value cache over the caller's tensors (include/nf4.h, nf4_kv_cache).
+
+    format "bf16": k, v bf16 [pages, kv_heads, page_size, head_dim]; no scales.
+    format "fp8":  k, v float8_e4m3fn of that shape; scales fp32 [pages, kv_heads, page_size].
+    format "nf4":  k, v uint8 [pages, kv_heads, page_size, head_dim/2]; scales fp16 [..., head_dim/64].
+    """
+
+    def __init__(self, format: str, k: torch.Tensor, v: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None):
+        if format not in KV_FORMATS:
+            raise ValueError(f"format {format!r}: want one of {sorted(KV_FORMATS)}")
+        if k.dim() != 4:
+            raise ValueError("k: want [pages, kv_heads, page_size, head_dim]")
+        pages, kv_heads, page_size, width = k.shape
+        head_dim = 2 * width if format == "nf4" else width
+        dtype = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "nf4": torch.uint8}[format]
+        places = (pages, kv_heads, page_size)
+        pk, pv = _expect(k, "k", dtype, k.shape), _expect(v, "v", dtype, k.shape)
+        pks = pvs = 0
+        if format == "bf16":
+            if k_scales is not None or v_scales is not None:
+                raise ValueError("a bf16 cache has no scales")
+        else:
+            if k_scales is None or v_scales is None:
+                raise ValueError(f"a cache in {format} needs k_scales and v_scales")
+            sdtype, sshape = ((torch.float32, places) if format == "fp8" else
+                              (torch.float16, (*places, head_dim // GROUP)))
+            pks, pvs = _expect(k_scales, "k_scales", sdtype, sshape), _expect(v_scales, "v_scales", sdtype, sshape)
+        self.format, self.pages, self.kv_heads = format, pages, kv_heads
+        self.page_size, self.head_dim = page_size, head_dim
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.device = k.device
+        self._c = _KvCacheStruct(pk, pv, pks, pvs, pages, kv_heads, page_size, head_dim, KV_FORMATS[format])
+        self._address = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, format: str, pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KVCache":
+        """A cache with its own tensors, zeroed."""
+        places = (pages, kv_heads, page_size)
+
+        def zeros(width, dtype):
+            return torch.zeros((*places, width), dtype=dtype, device=device)
+
+        if format == "bf16":
+            return cls(format, zeros(head_dim, torch.bfloat16), zeros(head_dim, torch.bfloat16))
+        if format == "fp8":
+            side = [zeros(head_dim, torch.uint8).view(torch.float8_e4m3fn) for _ in range(2)]
+            return cls(format, *side, *(torch.zeros(places, dtype=torch.float32, device=device) for _ in range(2)))
+        if format == "nf4":
+            return cls(format, zeros(head_dim // 2, torch.uint8), zeros(head_dim // 2, torch.uint8),
+                       zeros(head_dim // GROUP, torch.float16), zeros(head_dim // GROUP, torch.float16))
+        raise ValueError(f"format {format!r}: want one of {sorted(KV_FORMATS)}")
+
+
+def nf4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Write k, v bf16 [T, kv_heads, head_dim] at int64 slots [T] (page * page_size + offset; < 0: skip)."""
+    t = slots.shape[0]
+    shape = (t, cache.kv_heads, cache.head_dim)
+    _check(load().nf4_kv_append(cache._address, _expect(k, "k", torch.bfloat16, shape),
+                                _expect(v, "v", torch.bfloat16, shape), _expect(slots, "slots", torch.int64, (t,)), t,
+                                _current(stream)), "nf4_kv_append")
+
+
+def nf4_kv_read(cache: KVCache, slots: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                stream=None) -> None:
+    """Read int64 slots [T] back into k and / or v bf16 [T, kv_heads, head_dim]."""
+    t = slots.shape[0]
+    shape = (t, cache.kv_heads, cache.head_dim)
+    _check(load().nf4_kv_read(cache._address, _expect(slots, "slots", torch.int64, (t,)), t,
+                              None if k is None else _expect(k, "k", torch.bfloat16, shape),
+                              None if v is None else _expect(v, "v", torch.bfloat16, shape), _current(stream)),
+           "nf4_kv_read")
+
+
+def nf4_attention_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> int:
+    n = load().nf4_attention_workspace_bytes(cache._address, batch, q_heads)
+    if n < 0:
+        raise NF4Error(2, "nf4_attention_workspace_bytes")
+    return n
+
+
+def attention_workspace(cache: KVCache, batch: int, q_heads: int) -> torch.Tensor:
+    """A zeroed workspace for nf4_attention_decode with this cache, up to this batch and these heads."""
+    return torch.zeros(nf4_attention_workspace_bytes(cache, batch, q_heads), dtype=torch.uint8, device=cache.device)
+
+
+def nf4_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                         out: torch.Tensor, workspace: torch.Tensor, scale: Optional[float] = None, window: int = 0,
+                         stream=None) -> None:
+    """out[b, h] = attention of q bf16 [B, q_heads, head_dim] over the cache's places of each sequence:
+    page_table int32 [B, max_pages], lengths int32 [B]; scale defaults to head_dim ** -0.5."""
+    b, q_heads, d = q.shape
+    if d != cache.head_dim:
+        raise ValueError(f"q: head_dim {d}, the cache has {cache.head_dim}")
+    shape, max_pages = q.shape, page_table.shape[-1]
+    _check(load().nf4_attention_decode(
+        cache._address, _expect(q, "q", torch.bfloat16, shape),
+        _expect(page_table, "page_table", torch.int32, (b, max_pages)), max_pages,
+        _expect(lengths, "lengths", torch.int32, (b,)), b, q_heads, d ** -0.5 if scale is None else scale, window,
+        _expect(out, "out", torch.bfloat16, shape), _expect(workspace, "workspace", torch.uint8, workspace.shape),
+        workspace.numel(), _current(stream)), "nf4_attention_decode")
+
+
+def nf4_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor,
+             q_out: Optional[torch.Tensor], k_out: Optional[torch.Tensor], sections=None, interleaved: bool = False,
+             magnitude: float = 1.0, stream=None) -> None:
+    """Rotary positions on q [T, q_heads, D] and k [T, k_heads, D] (bf16; either may be None; the outputs
+    may be the inputs): positions int32 [axes, T], inv_freq fp32 [rotary_dim / 2], `sections` the pairs of
+    each axis (default: one axis)."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q and k are both None")
+    t, _, d = one.shape
+    axes, pairs = positions.shape[0], inv_freq.shape[0]
+    sections = [pairs] if sections is None else sections
+    if len(sections) != axes:
+        raise ValueError(f"sections: want one count for each of the {axes} axes")
+    side = []
+    for name, x, o in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            side.append((0, 0, 0))
+        else:
+            shape = (t, x.shape[1], d)
+            side.append((_expect(x, name, torch.bfloat16, shape), x.shape[1],
+                         _expect(o, name + "_out", torch.bfloat16, shape)))
+    (pq, hq, pqo), (pk, hk, pko) = side
+    _check(load().nf4_rope(pq, hq, pk, hk, t, d, _expect(positions, "positions", torch.int32, (axes, t)), axes,
+                           (ctypes.c_int32 * axes)(*sections), _expect(inv_freq, "inv_freq", torch.float32, (pairs,)),
+                           2 * pairs, int(interleaved), magnitude, pqo, pko, _current(stream)), "nf4_rope")
+
+
+def nf4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                residual_out: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                y8: Optional[torch.Tensor] = None, y8_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Norm of x (+ residual) bf16 [T, H] into y bf16 and / or y8 float8_e4m3fn with y8_scales fp32 [T];
+    residual_out receives the sum."""
+    t, h = x.shape
+    bf16, shape = torch.bfloat16, x.shape
+
+    def at(v, name, dtype, want):
+        return None if v is None else _expect(v, name, dtype, want)
+
+    _check(load().nf4_rmsnorm(_expect(x, "x", bf16, shape), at(residual, "residual", bf16, shape),
+                              _expect(weight, "weight", bf16, (h,)), t, h, eps,
+                              at(residual_out, "residual_out", bf16, shape), at(y, "y", bf16, shape),
+                              at(y8, "y8", torch.float8_e4m3fn, shape), at(y8_scales, "y8_scales", torch.float32, (t,)),
+                              _current(stream)), "nf4_rmsnorm")
+
+
 # Convenience wrappers that allocate the outputs with torch.
+def kv_read(cache: KVCache, slots: torch.Tensor, stream=None):
+    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
+    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=slots.device) for _ in range(2))
+    nf4_kv_read(cache, slots, k, v, stream)
+    return k, v
+
+
+def attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                     workspace: torch.Tensor, scale: Optional[float] = None, window: int = 0, stream=None):
+    out = torch.empty_like(q)
+    nf4_attention_decode(cache, q, page_table, lengths, out, workspace, scale, window, stream)
+    return out
+
+
+def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, sections=None,
+         interleaved: bool = False, magnitude: float = 1.0, stream=None):
+    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+    nf4_rope(q, k, positions, inv_freq, q_out, k_out, sections, interleaved, magnitude, stream)
+    return q_out, k_out
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None, stream=None):
+    """y, or (y, x + residual) with a residual."""
+    y = torch.empty_like(x)
+    r = None if residual is None else torch.empty_like(x)
+    nf4_rmsnorm(x, weight, eps, residual=residual, residual_out=r, y=y, stream=stream)
+    return y if residual is None else (y, r)
+
+
 def quantize(w: torch.Tensor, stream=None):
     n, k = w.shape
     codes = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)

@@ -66,6 +66,43 @@ nf4_status from_cuda(cudaError_t e) {
     return NF4_ERR_CUDA;
 }
 
+// A cache description: sizes first, then (for a cache that holds anything) its pointers.
+nf4_status check_cache(const nf4_kv_cache* c) {
+    if (!c) return NF4_ERR_NULL;
+    if (c->format < NF4_KV_BF16 || c->format > NF4_KV_NF4) return NF4_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NF4_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16 != 0) return NF4_ERR_SHAPE;
+    if (c->kv_heads < 1 || c->kv_heads > 65535 || c->pages < 0 || c->pages > kMaxDim) return NF4_ERR_SHAPE;
+    if (c->pages == 0) return NF4_OK;
+    const bool scaled = c->format != NF4_KV_BF16;
+    if (!c->k || !c->v || (scaled && (!c->k_scales || !c->v_scales))) return NF4_ERR_NULL;
+    if (!aligned16(c->k) || !aligned16(c->v)) return NF4_ERR_ALIGN;
+    if (scaled && (!aligned16(c->k_scales) || !aligned16(c->v_scales))) return NF4_ERR_ALIGN;
+    return NF4_OK;
+}
+
+// The byte ranges of a cache: k, v, k_scales, v_scales (unused ones empty).
+struct Ranges {
+    const void* p[4];
+    int64_t n[4];
+};
+Ranges cache_ranges(const nf4_kv_cache* c) {
+    const int64_t places = c->pages * c->kv_heads * c->page_size;
+    const int64_t vec = c->format == NF4_KV_BF16 ? 2 * c->head_dim : c->format == NF4_KV_FP8 ? c->head_dim : c->head_dim / 2;
+    const int64_t sc = c->format == NF4_KV_BF16 ? 0 : c->format == NF4_KV_FP8 ? 4 : c->head_dim / NF4_GROUP_SIZE * 2;
+    return {{c->k, c->v, c->k_scales, c->v_scales}, {places * vec, places * vec, places * sc, places * sc}};
+}
+bool overlaps_cache(const Ranges& r, const void* p, int64_t bytes) {
+    for (int i = 0; i < 4; i++)
+        if (overlap(r.p[i], r.n[i], p, bytes)) return true;
+    return false;
+}
+
+nf4::KvCache device_cache(const nf4_kv_cache* c) {
+    return {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), static_cast<uint8_t*>(c->k_scales),
+            static_cast<uint8_t*>(c->v_scales), c->pages, c->kv_heads, c->page_size, c->head_dim, c->format};
+}
+
 }  // namespace
 
 namespace nf4 {
@@ -158,10 +195,12 @@ nf4_status nf4_check_device_error(int* code) {
     int dev = 0, sms = 0;
     nf4_status st = current_device(&dev, &sms);
     if (st != NF4_OK) return st;
-    int linear = 0, embed = 0;
+    int linear = 0, embed = 0, kv = 0, attention = 0;
     if ((st = from_cuda(nf4::read_and_clear_error(&linear))) != NF4_OK) return st;
     if ((st = from_cuda(nf4::read_and_clear_embed_error(&embed))) != NF4_OK) return st;
-    *code = linear ? linear : embed;
+    if ((st = from_cuda(nf4::read_and_clear_kv_error(&kv))) != NF4_OK) return st;
+    if ((st = from_cuda(nf4::read_and_clear_attention_error(&attention))) != NF4_OK) return st;
+    *code = linear ? linear : embed ? embed : kv ? kv : attention;
     return NF4_OK;
 }
 
@@ -243,6 +282,143 @@ nf4_status nf4_linear(const uint16_t* x, const uint8_t* codes, const uint16_t* s
     if (M <= nf4::kGemvMaxTokens && K <= nf4::gemv_max_k(M))
         return from_cuda(nf4::launch_gemv(x, codes, scales, y, M, N, K, sms, stream));
     return from_cuda(nf4::launch_stream(x, 1, &codes, &scales, &y, &N, M, K, sms, stream));
+}
+
+nf4_status nf4_kv_append(const nf4_kv_cache* cache, const uint16_t* k, const uint16_t* v, const int64_t* slots,
+                         int64_t T, cudaStream_t stream) {
+    nf4_status st = check_cache(cache);
+    if (st != NF4_OK) return st;
+    if (T < 0 || T > kMaxDim) return NF4_ERR_SHAPE;
+    if (T == 0) return NF4_OK;
+    if (!k || !v || !slots) return NF4_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return NF4_ERR_ALIGN;
+    const Ranges r = cache_ranges(cache);
+    const int64_t in = T * cache->kv_heads * cache->head_dim * 2;
+    if (overlaps_cache(r, k, in) || overlaps_cache(r, v, in) || overlaps_cache(r, slots, T * 8)) return NF4_ERR_ALIAS;
+    for (int i = 0; i < 4; i++)
+        for (int j = i + 1; j < 4; j++)
+            if (overlap(r.p[i], r.n[i], r.p[j], r.n[j])) return NF4_ERR_ALIAS;
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != NF4_OK) return st;
+    return from_cuda(nf4::launch_kv_append(device_cache(cache), k, v, slots, T, sms, stream));
+}
+
+nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v,
+                       cudaStream_t stream) {
+    nf4_status st = check_cache(cache);
+    if (st != NF4_OK) return st;
+    if (T < 0 || T > kMaxDim) return NF4_ERR_SHAPE;
+    if (T == 0 || (!k && !v)) return NF4_OK;
+    if (!slots) return NF4_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(slots)) return NF4_ERR_ALIGN;
+    const Ranges r = cache_ranges(cache);
+    const int64_t ob = T * cache->kv_heads * cache->head_dim * 2;
+    if ((k && (overlaps_cache(r, k, ob) || overlap(k, ob, slots, T * 8))) ||
+        (v && (overlaps_cache(r, v, ob) || overlap(v, ob, slots, T * 8))) || (k && v && overlap(k, ob, v, ob)))
+        return NF4_ERR_ALIAS;
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != NF4_OK) return st;
+    return from_cuda(nf4::launch_kv_read(device_cache(cache), slots, T, k, v, sms, stream));
+}
+
+int64_t nf4_attention_workspace_bytes(const nf4_kv_cache* cache, int64_t B, int64_t q_heads) {
+    if (!cache || check_cache(cache) == NF4_ERR_SHAPE || B < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0) return -1;
+    return nf4::attention_workspace_bytes(cache->kv_heads, cache->head_dim, B, q_heads);
+}
+
+nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, const int32_t* page_table,
+                                int64_t max_pages, const int32_t* lengths, int64_t B, int64_t q_heads, float scale,
+                                int64_t window, uint16_t* out, void* workspace, int64_t workspace_bytes,
+                                cudaStream_t stream) {
+    nf4_status st = check_cache(cache);
+    if (st != NF4_OK) return st;
+    if (B < 0 || B > 65535 || q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads != 0) return NF4_ERR_SHAPE;
+    if (max_pages < 0 || max_pages * cache->page_size > kMaxDim || window < 0) return NF4_ERR_SHAPE;
+    if (B == 0) return NF4_OK;
+    if (!q || !lengths || !out || !workspace || (max_pages > 0 && !page_table)) return NF4_ERR_NULL;
+    if (!aligned16(q) || !aligned16(lengths) || !aligned16(out) || !aligned16(workspace) || !aligned16(page_table))
+        return NF4_ERR_ALIGN;
+    const int64_t need = nf4::attention_workspace_bytes(cache->kv_heads, cache->head_dim, B, q_heads);
+    if (workspace_bytes < need) return NF4_ERR_SHAPE;
+    const Ranges r = cache_ranges(cache);
+    const int64_t qb = B * q_heads * cache->head_dim * 2, tb = B * max_pages * 4;
+    const void* outs[2] = {out, workspace};
+    const int64_t ons[2] = {qb, need};
+    for (int i = 0; i < 2; i++)
+        if (overlaps_cache(r, outs[i], ons[i]) || overlap(outs[i], ons[i], q, qb) ||
+            overlap(outs[i], ons[i], page_table, tb) || overlap(outs[i], ons[i], lengths, B * 4))
+            return NF4_ERR_ALIAS;
+    if (overlap(out, qb, workspace, need)) return NF4_ERR_ALIAS;
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != NF4_OK) return st;
+    return from_cuda(nf4::launch_attention(device_cache(cache), q, page_table, max_pages, lengths, B, q_heads, scale,
+                                           window, out, workspace, sms, stream));
+}
+
+nf4_status nf4_rope(const uint16_t* q, int64_t q_heads, const uint16_t* k, int64_t k_heads, int64_t T, int64_t head_dim,
+                    const int32_t* positions, int axes, const int32_t* sections, const float* inv_freq,
+                    int64_t rotary_dim, int interleaved, float magnitude, uint16_t* q_out, uint16_t* k_out,
+                    cudaStream_t stream) {
+    if (T < 0 || T > kMaxDim || q_heads < 0 || q_heads > 65535 || k_heads < 0 || k_heads > 65535) return NF4_ERR_SHAPE;
+    if (head_dim < 16 || head_dim % 16 != 0 || head_dim > (1 << 24) || (q_heads + k_heads) * head_dim > (1 << 24))
+        return NF4_ERR_SHAPE;
+    if (rotary_dim < 16 || rotary_dim > head_dim || rotary_dim > 256 || rotary_dim % 16 != 0) return NF4_ERR_SHAPE;
+    if (axes < 1 || axes > 4) return NF4_ERR_SHAPE;
+    if (!sections) return NF4_ERR_NULL;
+    nf4::RopeArgs a{};
+    int64_t pairs = 0;
+    for (int i = 0; i < 4; i++) {
+        if (i < axes) {
+            if (sections[i] < 0) return NF4_ERR_SHAPE;
+            pairs += sections[i];
+        }
+        a.section_end[i] = static_cast<int>(pairs > kMaxDim ? kMaxDim : pairs);
+    }
+    if (pairs != rotary_dim / 2) return NF4_ERR_SHAPE;
+    if (T == 0 || q_heads + k_heads == 0) return NF4_OK;
+    if (!positions || !inv_freq || (q_heads && (!q || !q_out)) || (k_heads && (!k || !k_out))) return NF4_ERR_NULL;
+    const void* ins[4] = {positions, inv_freq, q_heads ? q : nullptr, k_heads ? k : nullptr};
+    const void* outs[2] = {q_heads ? q_out : nullptr, k_heads ? k_out : nullptr};
+    const int64_t in_bytes[4] = {axes * T * 4, rotary_dim * 2, T * q_heads * head_dim * 2, T * k_heads * head_dim * 2};
+    for (const void* p : ins)
+        if (!aligned16(p)) return NF4_ERR_ALIGN;
+    for (const void* p : outs)
+        if (!aligned16(p)) return NF4_ERR_ALIGN;
+    for (int o = 0; o < 2; o++)
+        for (int i = 0; i < 4; i++)
+            if (!(i == o + 2 && outs[o] == ins[i]) && overlap(outs[o], in_bytes[o + 2], ins[i], in_bytes[i]))
+                return NF4_ERR_ALIAS;
+    if (overlap(outs[0], in_bytes[2], outs[1], in_bytes[3])) return NF4_ERR_ALIAS;
+    int dev = 0, sms = 0;
+    nf4_status st = current_device(&dev, &sms);
+    if (st != NF4_OK) return st;
+    a.q = q, a.k = k, a.q_out = q_out, a.k_out = k_out, a.positions = positions, a.inv_freq = inv_freq;
+    a.T = T, a.q_heads = static_cast<int>(q_heads), a.k_heads = static_cast<int>(k_heads);
+    a.head_dim = static_cast<int>(head_dim), a.rotary_dim = static_cast<int>(rotary_dim), a.axes = axes;
+    a.interleaved = interleaved != 0, a.magnitude = magnitude;
+    return from_cuda(nf4::launch_rope(a, sms, stream));
+}
+
+nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int64_t H,
+                       float eps, uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y8_scales,
+                       cudaStream_t stream) {
+    if (T < 0 || T > kMaxDim || H <= 0 || H > kMaxDim || H % 8 != 0) return NF4_ERR_SHAPE;
+    if (T == 0) return NF4_OK;
+    if (!x || !weight || (!y && !y8) || (y8 != nullptr) != (y8_scales != nullptr)) return NF4_ERR_NULL;
+    const void* all[7] = {x, residual, weight, residual_out, y, y8, y8_scales};
+    const int64_t n[7] = {T * H * 2, T * H * 2, H * 2, T * H * 2, T * H * 2, T * H, T * 4};
+    for (const void* p : all)
+        if (!aligned16(p)) return NF4_ERR_ALIGN;
+    for (int o = 3; o < 7; o++)
+        for (int i = 0; i < 7; i++) {
+            if (i == o || !all[o] || !all[i]) continue;
+            const bool same = all[o] == all[i] && ((o == 3 && i <= 1) || (o == 4 && i == 0));  // in place
+            if (!same && overlap(all[o], n[o], all[i], n[i])) return NF4_ERR_ALIAS;
+        }
+    int dev = 0, sms = 0;
+    nf4_status st = current_device(&dev, &sms);
+    if (st != NF4_OK) return st;
+    return from_cuda(nf4::launch_rmsnorm(x, residual, weight, T, H, eps, residual_out, y, y8, y8_scales, sms, stream));
 }
 
 }  // extern "C"

@@ -40,6 +40,44 @@ cudaError_t launch_embed(const int32_t* ids, int64_t n_ids, const uint8_t* codes
                          int64_t K, uint16_t* out, int num_sms, cudaStream_t stream);
 cudaError_t read_and_clear_embed_error(int* code);
 
+// Key-value cache formats (nf4_kv_format) and the checked description of a cache.
+constexpr int kKvBf16 = 0, kKvFp8 = 1, kKvNf4 = 2;
+struct KvCache {
+    uint8_t *k, *v;              // [pages][kv_heads][page_size] vectors
+    uint8_t *k_scales, *v_scales;
+    int64_t pages;
+    int kv_heads, page_size, head_dim, format;
+};
+cudaError_t launch_kv_append(const KvCache& c, const uint16_t* k, const uint16_t* v, const int64_t* slots, int64_t T,
+                             int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvCache& c, const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v, int num_sms,
+                           cudaStream_t stream);
+// Error word of the cache calls (42: a slot outside the cache) and of the attention (43: a page or a
+// length outside its bounds).
+cudaError_t read_and_clear_kv_error(int* code);
+cudaError_t read_and_clear_attention_error(int* code);
+
+// One new token a sequence over the cache; the workspace is described in nf4_attn.cu.
+int64_t attention_workspace_bytes(int kv_heads, int head_dim, int64_t B, int64_t q_heads);
+cudaError_t launch_attention(const KvCache& c, const uint16_t* q, const int32_t* page_table, int64_t max_pages,
+                             const int32_t* lengths, int64_t B, int64_t q_heads, float scale, int64_t window,
+                             uint16_t* out, void* workspace, int num_sms, cudaStream_t stream);
+
+struct RopeArgs {
+    const uint16_t *q, *k;
+    uint16_t *q_out, *k_out;
+    const int32_t* positions;  // [axes][T]
+    const float* inv_freq;
+    int64_t T;
+    int q_heads, k_heads, head_dim, rotary_dim, axes, interleaved;
+    int section_end[4];  // first pair past axis a's run
+    float magnitude;
+};
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int64_t H,
+                           float eps, uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y8_scales, int num_sms,
+                           cudaStream_t stream);
+
 // The C-ABI layer's device check (an nf4_status value): the current device and its SM count.
 int abi_current_device(int* device, int* sms);
 // Records a CUDA error for nf4_last_cuda_error (no-op for cudaSuccess).

@@ -1,0 +1,316 @@
+// Rotary positions and the residual RMS norm: elementwise work over rows of activations, bound by the
+// bytes of their rows (long calls) or by the latency of one launch (decode).
+#include <cmath>
+
+#include "nf4_kv.cuh"
+
+namespace nf4 {
+namespace {
+
+// ---------------------------------------------------------------------------------------------
+// Rotary positions
+// ---------------------------------------------------------------------------------------------
+// A thread owns eight pairs of one token (16 values a head, two 16-byte pieces) and walks some of the
+// token's q and k heads with them, so the angles are computed once for all of these heads.
+//
+// Angle of a pair: positions * inv_freq radians, a real product, needed modulo 2 pi.  inv_freq / (2 pi)
+// is formed once in double and its fraction held as a 64-bit binary fraction F of a turn; F * position
+// modulo 2^64 is then the fraction of the product, exactly, by integer wrap-around (error: that of F,
+// 2^-53 relative, times the position: below 2^-22 turn at |position| < 2^31).  Its upper 32 bits, as a
+// signed number, are an angle in [-pi, pi), where the hardware sine and cosine have an absolute
+// error near 2^-21, far below the 2^-9 of the bf16 result.
+constexpr int kRopeThreads = 256;
+
+struct Turn {
+    float c[8], s[8];
+};
+
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int heads_step) {
+    pdl_launch_dependents();
+    const int chunks = a.head_dim / 16, rot = a.rotary_dim / 16;
+    const int per_token = chunks * heads_step;
+    int64_t t;
+    int id;
+    if (per_token <= kRopeThreads) {
+        const int per_block = kRopeThreads / per_token;
+        t = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / per_token;
+        id = threadIdx.x % per_token;
+        if (threadIdx.x / per_token >= per_block) t = a.T;
+    } else {
+        t = blockIdx.x;
+        id = blockIdx.y * kRopeThreads + threadIdx.x;
+    }
+    if (t >= a.T || id >= per_token) {
+        pdl_wait();
+        return;
+    }
+    const int c = id % chunks, h0 = id / chunks;
+    pdl_wait();
+    // elements of this thread's two pieces inside a head
+    int e0, e1;
+    Turn r;
+    if (c < rot) {
+        e0 = a.interleaved ? 16 * c : 8 * c;
+        e1 = a.interleaved ? 16 * c + 8 : 8 * c + a.rotary_dim / 2;
+        int32_t pos[4];
+#pragma unroll
+        for (int x = 0; x < 4; x++) pos[x] = x < a.axes ? a.positions[x * a.T + t] : 0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int i = 8 * c + j;
+            const int32_t p = i < a.section_end[0] ? pos[0] : i < a.section_end[1] ? pos[1] : i < a.section_end[2] ? pos[2] : pos[3];
+            const double turns = static_cast<double>(a.inv_freq[i]) * 0.15915494309189533577;
+            const uint64_t frac = __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+            const uint64_t at = frac * static_cast<uint64_t>(static_cast<int64_t>(p));
+            const float angle = static_cast<float>(static_cast<int32_t>(at >> 32)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+            r.s[j] = __sinf(angle) * a.magnitude;
+            r.c[j] = __cosf(angle) * a.magnitude;
+        }
+    } else {
+        e0 = 16 * c;
+        e1 = 16 * c + 8;
+    }
+    for (int h = h0; h < a.q_heads + a.k_heads; h += heads_step) {
+        const bool is_q = h < a.q_heads;
+        const uint16_t* src = is_q ? a.q : a.k;
+        uint16_t* dst = is_q ? a.q_out : a.k_out;
+        const int64_t row = (is_q ? t * a.q_heads + h : t * a.k_heads + (h - a.q_heads)) * a.head_dim;
+        uint4 u = *reinterpret_cast<const uint4*>(src + row + e0), v = *reinterpret_cast<const uint4*>(src + row + e1);
+        if (c < rot) {
+            uint32_t in0[4] = {u.x, u.y, u.z, u.w}, in1[4] = {v.x, v.y, v.z, v.w}, o0[4], o1[4];
+            if (a.interleaved) {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float2 p = bf16x2_to_f32x2(j < 4 ? in0[j] : in1[j - 4]);
+                    const uint32_t w = f32x2_to_bf16x2(p.x * r.c[j] - p.y * r.s[j], p.y * r.c[j] + p.x * r.s[j]);
+                    if (j < 4)
+                        o0[j] = w;
+                    else
+                        o1[j - 4] = w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float2 p = bf16x2_to_f32x2(in0[j]), q = bf16x2_to_f32x2(in1[j]);
+                    const float c0 = r.c[2 * j], c1 = r.c[2 * j + 1], s0 = r.s[2 * j], s1 = r.s[2 * j + 1];
+                    o0[j] = f32x2_to_bf16x2(p.x * c0 - q.x * s0, p.y * c1 - q.y * s1);
+                    o1[j] = f32x2_to_bf16x2(q.x * c0 + p.x * s0, q.y * c1 + p.y * s1);
+                }
+            }
+            u = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            v = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+        }
+        *reinterpret_cast<uint4*>(dst + row + e0) = u;
+        *reinterpret_cast<uint4*>(dst + row + e1) = v;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Residual RMS norm
+// ---------------------------------------------------------------------------------------------
+// One CTA a row.  h = x + residual stays in registers (CH pieces of eight values a thread; CH = 0, for
+// rows too wide for that, reads the row again), one block reduction gives sum(h^2) and max |h w| at once:
+// max |y| = rsqrt(...) * max |h w|, so the 8-bit scale needs no second one.
+__device__ __forceinline__ float2 block_sum_max(float2 v, float2* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+        v.y = fmaxf(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, o));
+    }
+    const int warps = blockDim.x / 32;
+    if (warps == 1) return v;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    float2 r = part[0];
+    for (int w = 1; w < warps; w++) {
+        const float2 p = part[w];
+        r.x += p.x;
+        r.y = fmaxf(r.y, p.y);
+    }
+    return r;
+}
+
+struct NormArgs {
+    const uint4 *x, *residual, *weight;
+    uint4 *residual_out, *y;
+    uint2* y8;
+    float* y8_scales;
+    int vecs;  // 16-byte pieces a row
+    float inv_h, eps;
+};
+
+__device__ __forceinline__ void load_h(const NormArgs& a, int64_t at, float (&h)[8]) {
+    const uint4 x = a.x[at];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 f = bf16x2_to_f32x2(xs[j]);
+        h[2 * j] = f.x, h[2 * j + 1] = f.y;
+    }
+    if (a.residual) {
+        const uint4 r = a.residual[at];
+        const uint32_t rs[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 f = bf16x2_to_f32x2(rs[j]);
+            h[2 * j] += f.x, h[2 * j + 1] += f.y;
+        }
+    }
+}
+
+__device__ __forceinline__ void load_w(const NormArgs& a, int i, float (&w)[8]) {
+    const uint4 x = a.weight[i];
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 f = bf16x2_to_f32x2(xs[j]);
+        w[2 * j] = f.x, w[2 * j + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float (&v)[8]) {
+    return make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                      f32x2_to_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void store_out(const NormArgs& a, int64_t at, const float (&h)[8], const float (&w)[8],
+                                          float rstd, float inv_scale) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = h[j] * rstd * w[j];
+    if (a.residual_out) a.residual_out[at] = pack_bf16(h);
+    if (a.y) a.y[at] = pack_bf16(y);
+    if (a.y8) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) y[j] *= inv_scale;
+        a.y8[at] = make_uint2(f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16),
+                              f32x2_to_e4m3x2(y[4], y[5]) | (f32x2_to_e4m3x2(y[6], y[7]) << 16));
+    }
+}
+
+template <int CH>
+__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
+    __shared__ float2 part[32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * a.vecs;
+    constexpr int N = CH ? CH : 1;
+    float h[N][8];
+    float2 acc = make_float2(0.0f, 0.0f);
+    auto add = [&](const float (&v)[8], int i) {
+        float w[8];
+        if (a.y8) load_w(a, i, w);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            acc.x = fmaf(v[j], v[j], acc.x);
+            if (a.y8) acc.y = fmaxf(acc.y, fabsf(v[j] * w[j]));
+        }
+    };
+    if (CH) {
+#pragma unroll
+        for (int c = 0; c < N; c++) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i < a.vecs) load_h(a, row + i, h[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < N; c++) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i < a.vecs) add(h[c], i);
+        }
+    } else {
+        for (int i = threadIdx.x; i < a.vecs; i += blockDim.x) {
+            load_h(a, row + i, h[0]);
+            add(h[0], i);
+        }
+    }
+    acc = block_sum_max(acc, part);
+    const float rstd = 1.0f / sqrtf(acc.x * a.inv_h + a.eps);
+    const float top = acc.y * rstd, scale = top / kFp8Max;
+    const float inv_scale = scale > 0.0f ? 1.0f / scale : 0.0f;
+    if (a.y8 && threadIdx.x == 0) a.y8_scales[blockIdx.x] = scale;
+    if (CH) {
+#pragma unroll
+        for (int c = 0; c < N; c++) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i < a.vecs) {
+                float w[8];
+                load_w(a, i, w);
+                store_out(a, row + i, h[c], w, rstd, inv_scale);
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i < a.vecs; i += blockDim.x) {
+            float w[8];
+            load_h(a, row + i, h[0]);
+            load_w(a, i, w);
+            store_out(a, row + i, h[0], w, rstd, inv_scale);
+        }
+    }
+}
+
+cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
+    const int heads = a.q_heads + a.k_heads, chunks = a.head_dim / 16;
+    // Heads a thread walks: as many (up to eight) as leave every SM a thousand threads.
+    const int64_t threads = a.T * heads * chunks;
+    int64_t walk = threads / (static_cast<int64_t>(num_sms) * 1024);
+    if (walk > 8) walk = 8;
+    if (walk < 1) walk = 1;
+    const int step = static_cast<int>((heads + walk - 1) / walk), per_token = chunks * step;
+    dim3 grid(static_cast<unsigned>(a.T), (per_token + kRopeThreads - 1) / kRopeThreads);
+    if (per_token <= kRopeThreads) {
+        const int per_block = kRopeThreads / per_token;
+        grid = dim3(static_cast<unsigned>((a.T + per_block - 1) / per_block));
+    }
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config(grid, kRopeThreads, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, rope_kernel, a, step);
+}
+
+cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int64_t H,
+                           float eps, uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y8_scales, int num_sms,
+                           cudaStream_t stream) {
+    NormArgs a{};
+    a.x = reinterpret_cast<const uint4*>(x);
+    a.residual = reinterpret_cast<const uint4*>(residual);
+    a.weight = reinterpret_cast<const uint4*>(weight);
+    a.residual_out = reinterpret_cast<uint4*>(residual_out);
+    a.y = reinterpret_cast<uint4*>(y);
+    a.y8 = reinterpret_cast<uint2*>(y8);
+    a.y8_scales = y8_scales;
+    a.vecs = static_cast<int>(H / 8);
+    a.inv_h = static_cast<float>(1.0 / static_cast<double>(H));
+    a.eps = eps;
+    // Few rows: as many threads as the row has pieces.  Many rows: up to four pieces a thread, which
+    // leaves room for more rows an SM.
+    const int want = T <= 2 * num_sms ? 1024 : 256;
+    const int64_t pieces = (a.vecs + want - 1) / want;
+    const int ch = pieces <= 1 ? 1 : pieces <= 2 ? 2 : 4;
+    int64_t threads = ((a.vecs + ch - 1) / ch + 31) / 32 * 32;
+    const bool wide = threads > 1024;
+    if (wide) threads = 1024;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg =
+        pdl_config(dim3(static_cast<unsigned>(T)), static_cast<int>(threads), stream, &attr);
+    if (wide) return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<0>, a);
+    switch (ch) {
+        case 1: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<1>, a);
+        case 2: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<2>, a);
+        default: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<4>, a);
+    }
+}
+
+}  // namespace nf4
