@@ -364,7 +364,8 @@ nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
  * see nf4_diag_set_wait_limit); a wait that runs out records a nonzero code (1..39; 39 is
  * nf4_diag_bounded_wait's), and the kernel drains and exits instead of hanging, leaving its outputs
  * unspecified.  nf4_embed records 41 for an id outside the table, the cache calls 42 for a slot
- * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds.  *code receives the first
+ * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds (44: a shared-memory layout that its
+ * kernel does not know).  *code receives the first
  * recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
  */
 nf4_status nf4_check_device_error(int* code);

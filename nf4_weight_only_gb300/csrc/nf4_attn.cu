@@ -1,131 +1,906 @@
 // Attention of one new token a sequence over the paged key-value cache.
 //
-// The plainest form: one CTA of four warps for each (sequence, query head); a warp takes every
-// fourth key, its lanes a slice of head_dim each, with the running maximum and sum of a softmax;
-// the warps' results are joined in shared memory.
+// Mathematics.  For one sequence and kv head, the G query heads that share it give
+//   S = K q^T [keys x heads],  p = 2^(S c - m),  O^T = V^T p^T [dims x heads],  l = sum p,
+// one pass over the cache with a running maximum m a head (c = scale log2 e); O / l at the end.  Both
+// products go through mma.sync m16n8k16 with the cache as the 16-row operand and the heads as the
+// eight columns: 128 bytes of bf16 cache feed one instruction, so the tensor work is far below what
+// the cache's bytes cost, and the fragments are read in an order that needs no rearrangement of the
+// cache: the dims of a product's k axis may be permuted at will (q is permuted alike), and so may the
+// keys.  tcgen05 wants 64 or 128 rows from shared memory in canonical tiles; here the rows are in
+// pages of 16 and more, quantised, and a tile would be used once, for eight columns.
+//
+// Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte
+// (two codes) indexes a table of fp16 pairs in shared memory (T rounded to fp16, 2^-12 relative).  The
+// scales are applied in fp32: K's to S, V's to p.  q in fp16 is scaled by a power of two a head (exact
+// except for elements below 2^-28 of the head's largest); p * scale in fp16 (2^-12) by a power of two a
+// warp that follows the largest scale.  With a bf16 cache p is rounded to bf16 (2^-9).  S, m, l and O are
+// fp32 throughout.
+//
+// Work.  A unit is 16 keys of one sequence and kv head (or of one group of at most 16 of its query
+// heads).  The units of all sequences are laid end to end and every CTA takes an equal run of them, so
+// ragged batches, one long sequence and thousands of short ones load the SMs alike; the CTAs work the
+// runs out from the lengths, with no plan from the host.  Inside a run the warps of a CTA take units in
+// turn, each with its own ring of cp.async stages and no block barrier, and join their results in shared
+// memory where a sequence's part of the run ends.  A sequence that crosses runs leaves one partial result
+// a CTA in the workspace; the CTA that finishes last joins them in order, so results do not depend
+// on timing.
+#include <mutex>
+
 #include "nf4_kv.cuh"
 
 namespace nf4 {
 namespace {
 
+// Error word of the attention (43: a page or a length outside its bounds).
 __device__ int g_attention_error;
 
-template <int FMT, int D>
-__device__ __forceinline__ void load_values(const uint8_t* base, const uint8_t* scales, int64_t at, int lane,
-                                            float (&x)[D / 32]) {
-    constexpr int E = D / 32;
+constexpr int kMaxGrid = 320;         // CTAs a launch has at most (workspace slots)
+constexpr int kCounters = 1024;       // ticket counters at the start of the workspace
+constexpr int kMinUnits = 8;          // smallest run worth a CTA
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.0f;         // p may reach 2^8 before the running maximum moves
+
+struct AttnArgs {
+    KvCache c;
+    const uint16_t* q;
+    const int32_t* page_table;
+    const int32_t* lengths;
+    uint16_t* out;
+    uint32_t* counters;
+    float* partials;
+    int64_t max_pages, window;
+    uint64_t page_magic;  // ceil(2^64 / (page_size / 16))
+    int B, q_heads, group;
+    int chunks, chunk_heads;  // query heads of a kv head: `chunks` groups of at most chunk_heads
+    int slot_floats;          // floats of one partial result
+    float scale;
+};
+
+// ---------------------------------------------------------------------------------------------
+// Fragments
+// ---------------------------------------------------------------------------------------------
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit elements across the warp: lane (g, t) gives row g, columns 2t and 2t + 1, and
+// gets rows 2t and 2t + 1 of column g.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128a(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+// The table is never written after the first barrier: its loads may move.
+__device__ __forceinline__ uint32_t lds_table(uint32_t a) {
+    uint32_t v;
+    asm("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+// B bytes (4, 8 or 16) global -> shared; B source bytes are read, or none and zeros written.
+template <int B>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+    const uint32_t n = live ? B : 0;
+    if (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(B) : "memory");
+}
+
+// Shared memory of a CTA.  NF4 keeps its pair table at shared address 64 KB, entry v (a code byte) at
+// 256 v and lane l's copy 4 l into it, so one byte permute of a code word and the lane's constant is a
+// lookup's whole address and the 32 lanes never conflict.  The warps' rings lie on both sides of it.
+constexpr uint32_t kTableAt = 65536, kTableEnd = 131072;
+
+template <int FMT, int D, int NT>
+struct Shape {
+    static constexpr bool kBf = FMT == kKvBf16;
+    static constexpr int VB = kv_vector_bytes(FMT, D);           // bytes of a vector
+    static constexpr int SB = 16 * kv_scale_bytes(FMT, D);       // bytes of 16 keys' scales of one side
+    static constexpr int GR = FMT == kKvNf4 ? D / 64 : 1;        // scale groups of a vector
+    static constexpr int kStage = 32 * VB + 2 * SB;              // 16 keys, K and V
+    // Warps and stages: enough warps to issue the decoding (16 for the quantised formats where their
+    // registers allow it), and about 100 KB in flight an SM.
+    static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : (NT == 2 || D == 256) ? 8 : 16;
+    static constexpr int kRingMost = FMT == kKvNf4 ? (W == 16 ? 10240 : 20480) : 204800 / W;
+    static constexpr int kStagesFit = kRingMost / kStage;
+    static constexpr int NST = kStagesFit > 6 ? 6 : kStagesFit;
+    static constexpr int kRing = NST * kStage;
+    static constexpr int kResult = NT * 8 * (D + 2) * 4;         // bytes of a warp's result
+    static constexpr int kSmem = 226 * 1024;                     // dynamic; with 1 KB of static, all there is
+    static constexpr int kArea = kRing > kResult ? kRing : kResult;
+    // dynamic shared memory starts 1 to 4 KB into the window
+    static constexpr int kBelow = FMT == kKvNf4 ? static_cast<int>(kTableAt - 4096) / kArea : W;
+    static_assert(NST >= 2, "a ring has at least two stages");
+    static_assert(FMT == kKvNf4 ? (W - kBelow) * kArea <= kSmem + 1024 - static_cast<int>(kTableEnd)
+                                : W * kArea <= kSmem, "the areas fit");
+};
+
+// Dynamic shared memory cut into areas of `bytes`, the NF4 table left out: address of area w.  Used for
+// the warps' rings and, once these are drained, for their results.
+template <int FMT>
+__device__ __forceinline__ uint32_t area_of(uint32_t base, int w, uint32_t bytes) {
+    if (FMT != kKvNf4) return base + w * bytes;
+    const int below = (kTableAt - base) / bytes;
+    return w < below ? base + w * bytes : kTableEnd + (w - below) * bytes;
+}
+
+// Key of fragment row r (0..7; row r + 8 holds the key 8 later).  Chosen so that rows r = 0..3 and 4..7,
+// and rows 2t and 2t + 1 over t, are distinct modulo 4: the bank groups of the NF4 reads then differ.
+__device__ __forceinline__ int key_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
+
+// NF4 vectors in a stage: the 32-byte piece that holds group r of key row `k`.
+template <int D>
+__device__ __forceinline__ uint32_t nf4_piece(int k, int r) {
+    if (D == 64) return k * 32;
+    if (D == 128) return k * 64 + ((r ^ ((k >> 1) & 1)) * 32);
+    return k * 128 + ((r ^ (k & 3)) * 32);
+}
+
+// ---------------------------------------------------------------------------------------------
+// One unit into a stage
+// ---------------------------------------------------------------------------------------------
+// place: vector index of the unit's first key, or -1 (a page outside the cache: zeros).  lo and hi: the
+// live keys of the unit; dead ones are filled with zeros so that nothing non-finite meets a weight of 0.
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void issue_unit(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+    using S = Shape<FMT, D, NT>;
+    const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
+    if (place < 0) {
+        for (int i = lane * 4; i < S::kStage; i += 128)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + i), "r"(0) : "memory");
+        return;
+    }
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* k = c.k + place * S::VB;
+    const uint8_t* v = c.v + place * S::VB;
+    auto live = [&](int key) { return key >= lo && key < hi; };
+    if (FMT == kKvNf4) {
+        constexpr int P = S::VB / 16;  // 16-byte pieces of a vector
 #pragma unroll
-    for (int e = 0; e < E; e++) {
-        const int d = lane * E + e;
-        if (FMT == kKvBf16) {
-            x[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(base)[at * D + d]);
-        } else if (FMT == kKvFp8) {
-            const uint32_t h = e4m3x2_to_f16x2(base[at * D + d]);
-            x[e] = __half2float(__ushort_as_half(static_cast<uint16_t>(h & 0xFFFFu))) *
-                   reinterpret_cast<const float*>(scales)[at];
-        } else {
-            const uint32_t b = base[at * (D / 2) + d / 2];
-            x[e] = kNF4[(d & 1) ? b >> 4 : b & 15u] *
-                   __half2float(__ushort_as_half(reinterpret_cast<const uint16_t*>(scales)[at * (D / 64) + d / 64]));
+        for (int j = 0; j < P / 2; j++) {
+            const int piece = j * 32 + lane, key = piece / P, p = piece % P;
+            const uint32_t at = nf4_piece<D>(key, p / 2) + (p & 1) * 16;
+            const bool on = live(key);
+            cp_async<16>(kb + at, k + piece * 16, on);
+            cp_async<16>(vb + at, v + piece * 16, on);
+        }
+    } else {
+        // each lane copies what it will read itself, in the order in which it will read it
+        constexpr int CK = S::VB / 4 < 16 ? S::VB / 4 : 16, NK = S::VB / 4 / CK;
+        const int key = key_of_row(g);
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+#pragma unroll
+            for (int i = 0; i < NK; i++)
+                cp_async<CK>(kb + ((r * NK + i) * 32 + lane) * CK, k + (key + 8 * r) * S::VB + (i * 4 + t) * CK,
+                             live(key + 8 * r));
+        constexpr int CV = S::VB / 8 < 16 ? S::VB / 8 : 16, NV = S::VB / 8 / CV;
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const int kr = key_of_row(2 * t + (r & 1)) + 8 * (r >> 1);
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                cp_async<CV>(vb + ((r * NV + i) * 32 + lane) * CV, v + kr * S::VB + (i * 8 + g) * CV, live(kr));
+        }
+    }
+    if (S::SB) {
+        constexpr int SK = S::SB ? S::SB / 16 : 1;  // scale bytes of a key
+        const uint8_t* ks = c.k_scales + place * SK;
+        const uint8_t* vs = c.v_scales + place * SK;
+#pragma unroll
+        for (int i = 0; i < 2 * S::SB; i += 128) {
+            const int o = i + lane * 4;
+            if (o < 2 * S::SB) {
+                const int at = o < S::SB ? o : o - S::SB;
+                const bool on = live(at / SK) || live((at + 3) / SK);
+                cp_async<4>(sb + o, (o < S::SB ? ks : vs) + at, on);
+            }
         }
     }
 }
 
+// ---------------------------------------------------------------------------------------------
+// The running softmax and output of a warp
+// ---------------------------------------------------------------------------------------------
+template <int FMT, int D, int NT>
+struct WarpState {
+    uint32_t q[NT][D / 16][2];  // fragments of q^T
+    float mul[NT][2];           // S -> base-2 logit, heads 2t and 2t + 1
+    float m[NT][2], l[NT][2];
+    float o[NT][D / 16][4];
+    float vn, vlim;             // V scales are multiplied by vn; they stay below vlim
+};
+
+// First dim of a lane's run of consecutive dims: K side (t) and V side (g).
 template <int FMT, int D>
-__global__ void __launch_bounds__(128) attention_kernel(KvCache c, const uint16_t* __restrict__ q,
-                                                        const int32_t* __restrict__ page_table, int64_t max_pages,
-                                                        const int32_t* __restrict__ lengths, int q_heads, float scale,
-                                                        int64_t window, uint16_t* __restrict__ out) {
-    constexpr int E = D / 32;
-    __shared__ float part[4][D + 2];
+__device__ __forceinline__ int k_dim(int i, int t) {  // i-th run of the lane; runs of 8 (bf16) or 16
+    if (FMT == kKvBf16) return (i * 4 + t) * 8;
+    return (i * 4 + t) * 16;
+}
+template <int FMT, int D>
+__device__ __forceinline__ constexpr int v_run() {  // dims of a run on the V side
+    return FMT == kKvFp8 ? (D / 8 < 16 ? D / 8 : 16) : 8;
+}
+
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void load_q(const AttnArgs& a, WarpState<FMT, D, NT>& s, const uint16_t* q, int heads,
+                                       int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int RUN = FMT == kKvBf16 ? 8 : 16;  // consecutive dims of a lane
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        const int h = nt * 8 + g;
+        uint32_t w[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 4 / RUN; i++)
+#pragma unroll
+            for (int j = 0; j < RUN / 8; j++) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (h < heads) x = *reinterpret_cast<const uint4*>(q + h * D + k_dim<FMT, D>(i, t) + 8 * j);
+                const int at = (i * RUN + 8 * j) / 2;
+                w[at] = x.x, w[at + 1] = x.y, w[at + 2] = x.z, w[at + 3] = x.w;
+            }
+        float mul = a.scale * kLog2e;
+        if (FMT != kKvBf16) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; i++) {
+                const float2 f = bf16x2_to_f32x2(w[i]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // the head's largest element to [2^14, 2^15)
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
+            const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+            mul *= __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; i++) {
+                const float2 f = bf16x2_to_f32x2(w[i]);
+                w[i] = pack_f16(f.x * up, f.y * up);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; i++) s.q[nt][i][0] = w[2 * i], s.q[nt][i][1] = w[2 * i + 1];
+        s.mul[nt][0] = __shfl_sync(0xFFFFFFFFu, mul, 8 * t);
+        s.mul[nt][1] = __shfl_sync(0xFFFFFFFFu, mul, 8 * t + 4);
+        s.m[nt][0] = s.m[nt][1] = -3e38f;
+        s.l[nt][0] = s.l[nt][1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) s.o[nt][i][j] = 0.0f;
+    }
+    s.vn = 1.0f;
+    s.vlim = -1.0f;
+}
+
+// One unit of 16 keys from its stage.  lo, hi: its live keys (full: all of them).
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t buf, bool full, int lo, int hi,
+                                            int lane) {
+    using S = Shape<FMT, D, NT>;
+    constexpr bool BF = S::kBf;
+    constexpr int GR = S::GR;
+    const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
+    const int g = lane >> 2, t = lane & 3, key = key_of_row(g);
+    // the lane's constant in a table lookup's address: 64 KB and 4 * lane around the code byte
+    const uint32_t column = (kTableAt >> 8) | static_cast<uint32_t>(4 * lane);
+    auto pair_of = [&](uint32_t word, int byte) {  // fp16 pair of byte `byte` of a code word
+        return lds_table(prmt(word, column, 0x6504u + 16u * static_cast<uint32_t>(byte)));
+    };
+
+    // S = K q^T: two chains a product (a chain for each scale group with NF4)
+    constexpr int CH = FMT == kKvNf4 ? GR : 2;
+    float sc[NT][CH][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int c = 0; c < CH; c++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) sc[nt][c][j] = 0.0f;
+    if (FMT == kKvNf4) {
+#pragma unroll
+        for (int r = 0; r < GR; r++) {
+            const uint2 u = lds64(kb + nf4_piece<D>(key, r) + t * 8);
+            const uint2 w = lds64(kb + nf4_piece<D>(key + 8, r) + t * 8);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {  // four dims a row each
+                const uint32_t x = i < 2 ? u.x : u.y, y = i < 2 ? w.x : w.y;
+                const int b = 2 * (i & 1);
+                const uint32_t f[4] = {pair_of(x, b), pair_of(y, b), pair_of(x, b + 1), pair_of(y, b + 1)};
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+                    mma16816<false>(sc[nt][r], f, s.q[nt][r * 4 + i][0], s.q[nt][r * 4 + i][1]);
+            }
+        }
+    } else {
+        constexpr int CK = S::VB / 4 < 16 ? S::VB / 4 : 16, NK = S::VB / 4 / CK, WK = CK / 4;
+#pragma unroll
+        for (int i = 0; i < NK; i++) {
+            uint32_t x[WK], y[WK];
+            const uint4 u = lds128a(kb + (i * 32 + lane) * CK), w = lds128a(kb + ((NK + i) * 32 + lane) * CK);
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+            y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
+            if (BF) {
+#pragma unroll
+                for (int j = 0; j < WK / 2; j++) {
+                    const uint32_t f[4] = {x[2 * j], y[2 * j], x[2 * j + 1], y[2 * j + 1]};
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+                        mma16816<true>(sc[nt][j & 1], f, s.q[nt][i * 2 + j][0], s.q[nt][i * 2 + j][1]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < WK; j++) {
+                    const uint32_t f[4] = {e4m3x2_to_f16x2(x[j] & 0xFFFFu), e4m3x2_to_f16x2(y[j] & 0xFFFFu),
+                                           e4m3x2_to_f16x2(x[j] >> 16), e4m3x2_to_f16x2(y[j] >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+                        mma16816<false>(sc[nt][j & 1], f, s.q[nt][i * 4 + j][0], s.q[nt][i * 4 + j][1]);
+                }
+            }
+        }
+    }
+
+    // scales of keys `key` (row g) and key + 8
+    float ks[2][GR], vs[2][GR];
+    if (FMT != kKvBf16) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            const int k = key + 8 * r;
+            if (FMT == kKvFp8) {
+                ks[r][0] = __uint_as_float(lds32(sb + 4 * k));
+                vs[r][0] = __uint_as_float(lds32(sb + S::SB + 4 * k));
+            } else if (GR == 1) {
+                ks[r][0] = __half2float(__ushort_as_half(lds_u16(sb + 2 * k)));
+                vs[r][0] = __half2float(__ushort_as_half(lds_u16(sb + S::SB + 2 * k)));
+            } else {
+#pragma unroll
+                for (int p = 0; p < GR / 2; p++) {
+                    const uint32_t kw = lds32(sb + (k * GR + 2 * p) * 2), vw = lds32(sb + S::SB + (k * GR + 2 * p) * 2);
+                    const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw));
+                    const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vw));
+                    ks[r][2 * p] = kf.x, ks[r][2 * p + (GR > 1)] = kf.y;
+                    vs[r][2 * p] = vf.x, vs[r][2 * p + (GR > 1)] = vf.y;
+                }
+            }
+        }
+    }
+    const bool on[2] = {full || (key >= lo && key < hi), full || (key + 8 >= lo && key + 8 < hi)};
+    if (FMT != kKvBf16) {
+        if (!full) {
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+#pragma unroll
+                for (int c = 0; c < GR; c++)
+                    if (!on[r]) vs[r][c] = 0.0f;
+        }
+        // V scales in fp16 range: the largest times vn stays below 2^7
+        float top = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+#pragma unroll
+            for (int c = 0; c < GR; c++) top = fmaxf(top, vs[r][c]);
+        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+        if (top > s.vlim) {
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 7), 254);
+            const float vn = __uint_as_float(static_cast<uint32_t>(260 - e) << 23), f = vn / s.vn;
+            s.vn = vn;
+            s.vlim = __uint_as_float(static_cast<uint32_t>(min(e + 1, 254)) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int i = 0; i < D / 16; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) s.o[nt][i][j] *= f;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; r++)
+#pragma unroll
+            for (int c = 0; c < GR; c++) vs[r][c] *= s.vn;
+    }
+
+    // base-2 logits of keys (row g: 0, 1; row g + 8: 2, 3) and heads 2t, 2t + 1; weights; p^T fragments
+    float x[NT][4];
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int r = j >> 1;
+            float y;
+            if (FMT == kKvBf16) {
+                y = (sc[nt][0][j] + sc[nt][CH > 1][j]) * s.mul[nt][j & 1];
+            } else if (FMT == kKvFp8) {
+                y = (sc[nt][0][j] + sc[nt][CH > 1][j]) * (ks[r][0] * s.mul[nt][j & 1]);
+            } else {
+                y = sc[nt][0][j] * ks[r][0];
+#pragma unroll
+                for (int c = 1; c < GR; c++) y = fmaf(sc[nt][c][j], ks[r][c], y);
+                y *= s.mul[nt][j & 1];
+            }
+            x[nt][j] = on[r] ? y : -INFINITY;
+            over |= x[nt][j] > s.m[nt][j & 1] + kLazy;
+        }
+    if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                float top = fmaxf(x[nt][j], x[nt][j + 2]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                top = fmaxf(top, s.m[nt][j]);
+                const float f = exp2_approx(s.m[nt][j] - top);
+                s.m[nt][j] = top;
+                s.l[nt][j] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; i++) s.o[nt][i][j] *= f, s.o[nt][i][j + 2] *= f;
+            }
+    }
+    uint32_t pb[NT][GR][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) p[j] = exp2_approx(x[nt][j] - s.m[nt][j & 1]);
+        s.l[nt][0] += p[0] + p[2];
+        s.l[nt][1] += p[1] + p[3];
+        if (FMT == kKvBf16) {
+            pb[nt][0][0] = transpose8x8(f32x2_to_bf16x2(p[0], p[1]));
+            pb[nt][0][1] = transpose8x8(f32x2_to_bf16x2(p[2], p[3]));
+        } else {
+#pragma unroll
+            for (int c = 0; c < GR; c++) {
+                pb[nt][c][0] = transpose8x8(pack_f16(p[0] * vs[0][c], p[1] * vs[0][c]));
+                pb[nt][c][1] = transpose8x8(pack_f16(p[2] * vs[1][c], p[3] * vs[1][c]));
+            }
+        }
+    }
+
+    // O^T += V^T p^T: fragment column pairs are keys of rows (2t, 2t + 1) and (2t + 8, 2t + 9)
+    if (FMT == kKvNf4) {
+        const int ka = key_of_row(2 * t), kc = key_of_row(2 * t + 1);
+#pragma unroll
+        for (int r = 0; r < GR; r++) {
+            const uint32_t wa = lds32(vb + nf4_piece<D>(ka, r) + g * 4), wb = lds32(vb + nf4_piece<D>(kc, r) + g * 4);
+            const uint32_t wc = lds32(vb + nf4_piece<D>(ka + 8, r) + g * 4),
+                           wd = lds32(vb + nf4_piece<D>(kc + 8, r) + g * 4);
+            // code bytes (first key low, second key high) of the even and of the odd dims
+            const uint32_t lo4 = 0x0F0F0F0Fu;
+            const uint32_t e0 = (wa & lo4) | ((wb << 4) & ~lo4), o0 = ((wa >> 4) & lo4) | (wb & ~lo4);
+            const uint32_t e1 = (wc & lo4) | ((wd << 4) & ~lo4), o1 = ((wc >> 4) & lo4) | (wd & ~lo4);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t f[4] = {pair_of(e0, i), pair_of(o0, i), pair_of(e1, i), pair_of(o1, i)};
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) mma16816<false>(s.o[nt][r * 4 + i], f, pb[nt][r][0], pb[nt][r][1]);
+            }
+        }
+    } else {
+        constexpr int CV = S::VB / 8 < 16 ? S::VB / 8 : 16, NV = S::VB / 8 / CV, WV = CV / 4;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const uint32_t at = vb + ((r * NV + i) * 32 + lane) * CV;
+                if (CV == 16) {
+                    const uint4 u = lds128a(at);
+                    w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
+                } else {
+                    const uint2 u = lds64(at);
+                    w[r][0] = u.x, w[r][1] = u.y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < WV; j++) {
+                if (BF) {
+                    const uint32_t f[4] = {prmt(w[0][j], w[1][j], 0x5410), prmt(w[0][j], w[1][j], 0x7632),
+                                           prmt(w[2][j], w[3][j], 0x5410), prmt(w[2][j], w[3][j], 0x7632)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) mma16816<true>(s.o[nt][i * WV + j], f, pb[nt][0][0], pb[nt][0][1]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {  // dims 0, 1 and 2, 3 of the word
+                        const uint32_t u = prmt(w[0][j], w[1][j], h ? 0x7362 : 0x5140);
+                        const uint32_t z = prmt(w[2][j], w[3][j], h ? 0x7362 : 0x5140);
+                        const uint32_t f[4] = {e4m3x2_to_f16x2(u & 0xFFFFu), e4m3x2_to_f16x2(u >> 16),
+                                               e4m3x2_to_f16x2(z & 0xFFFFu), e4m3x2_to_f16x2(z >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+                            mma16816<false>(s.o[nt][(i * WV + j) * 2 + h], f, pb[nt][0][0], pb[nt][0][1]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// Lengths and runs
+// ---------------------------------------------------------------------------------------------
+struct Span {
+    int start, end;  // keys [start, end) of a sequence
+    __device__ int first_unit() const { return start >> 4; }
+    __device__ int units() const { return end > start ? ((end + 15) >> 4) - (start >> 4) : 0; }
+};
+
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+    const int64_t most = a.max_pages * a.c.page_size;
+    const int64_t n0 = a.lengths[b];
+    const int n = static_cast<int>(n0 < 0 ? 0 : n0 > most ? most : n0);
+    Span s;
+    s.end = n;
+    s.start = a.window > 0 && n > a.window ? n - static_cast<int>(a.window) : 0;
+    return s;
+}
+
+// Four dims of one head, joined over `n` results in their order: part(j) is result j, [heads][D] sums of
+// weighted values, [heads] maxima, [heads] sums of weights.
+struct Joined {
+    float4 o;
+    float top, l;
+};
+template <int D, bool GLOBAL, typename Part>
+__device__ __forceinline__ Joined join(const Part& part, int n, int heads, int i) {
+    auto ld = [](const float* p) { return GLOBAL ? __ldcg(p) : *p; };
+    const int h = i / (D / 4);
+    Joined r{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -3e38f, 0.0f};
+#pragma unroll 4
+    for (int j = 0; j < n; j++) r.top = fmaxf(r.top, ld(part(j) + heads * D + h));
+#pragma unroll 4
+    for (int j = 0; j < n; j++) {
+        const float* p = part(j);
+        const float f = exp2_approx(ld(p + heads * D + h) - r.top);
+        r.l = fmaf(f, ld(p + heads * D + heads + h), r.l);
+        const float4* q = reinterpret_cast<const float4*>(p) + i;
+        const float4 v = GLOBAL ? __ldcg(q) : *q;
+        r.o.x = fmaf(f, v.x, r.o.x), r.o.y = fmaf(f, v.y, r.o.y);
+        r.o.z = fmaf(f, v.z, r.o.z), r.o.w = fmaf(f, v.w, r.o.w);
+    }
+    return r;
+}
+__device__ __forceinline__ uint2 normalised(const Joined& r) {
+    const float f = r.l > 0.0f ? 1.0f / r.l : 0.0f;
+    return make_uint2(f32x2_to_bf16x2(r.o.x * f, r.o.y * f), f32x2_to_bf16x2(r.o.z * f, r.o.w * f));
+}
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel(const AttnArgs a) {
+    using S = Shape<FMT, D, NT>;
+    constexpr int W = S::W, NST = S::NST;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int s_last;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int h = blockIdx.x, kv = h / (q_heads / c.kv_heads);
-    const int64_t b = blockIdx.y;
+    const uint32_t base = smem_u32(smem);
+    if (FMT == kKvNf4) {
+        for (int i = threadIdx.x; i < 256 * 32; i += W * 32) {
+            const int v = i >> 5;
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(kTableAt + v * 256 + (i & 31) * 4),
+                         "r"(pack_f16(kNF4[v & 15], kNF4[v >> 4]))
+                         : "memory");
+        }
+        __syncthreads();
+    }
     pdl_launch_dependents();
     pdl_wait();
-    int64_t n = lengths[b];
-    if (n < 0) n = 0;
-    if (n > max_pages * c.page_size) {
-        n = max_pages * c.page_size;
-        if (threadIdx.x == 0) atomicCAS(&g_attention_error, 0, 43);
+    if (base > 4096) {  // not where the areas were laid out for: nothing is computed, and that is reported
+        if (threadIdx.x == 0) atomicCAS(&g_attention_error, 0, 44);
+        return;
     }
-    const int64_t first = window > 0 && n > window ? n - window : 0;
-    float qs[E], acc[E];
+
+    // total units, and (block 0) lengths out of bounds
+    const int segs = a.c.kv_heads * a.chunks;  // runs of units a sequence
+    int64_t total = 0;
+    {
+        int64_t mine = 0;
+        for (int b = lane; b < a.B; b += 32) {
+            mine += span_of(a, b).units();
+            if (blockIdx.x == 0 && warp == 0 && a.lengths[b] > a.max_pages * a.c.page_size)
+                atomicCAS(&g_attention_error, 0, 43);
+        }
 #pragma unroll
-    for (int e = 0; e < E; e++) {
-        qs[e] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(q)[(b * q_heads + h) * D + lane * E + e]) * scale;
-        acc[e] = 0.0f;
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+        total = mine * segs;
     }
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = first + warp; j < n; j += 4) {
-        const int64_t page = page_table[b * max_pages + j / c.page_size];
-        if (page < 0 || page >= c.pages) {
-            if (lane == 0) atomicCAS(&g_attention_error, 0, 43);
+    // sequences with nothing to attend to
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+        if (span_of(a, b).units() == 0)
+            for (int i = threadIdx.x; i < a.q_heads * D / 8; i += W * 32)
+                reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * D / 8) + i] = make_uint4(0, 0, 0, 0);
+
+    int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    if (share < kMinUnits) share = kMinUnits;
+    int64_t at = blockIdx.x * share;
+    const int64_t stop = at + share < total ? at + share : total;
+    if (at >= stop) return;
+
+    // the sequence that unit `at` belongs to, and the units before it
+    int b = 0;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+        int64_t u = b0 + lane < a.B ? static_cast<int64_t>(span_of(a, b0 + lane).units()) * segs : 0, sum = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + sum > at);
+        if (past) {
+            const int f = __ffs(past) - 1;
+            b = b0 + f;
+            before += __shfl_sync(0xFFFFFFFFu, sum - u, f);
+            break;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+
+    const uint32_t ring = area_of<FMT>(base, warp, S::kArea);
+    const int units_per_page = a.c.page_size >> 4;
+    WarpState<FMT, D, NT> s;
+    while (at < stop) {
+        // the piece of this run in one segment: units [u0, u1) of its n
+        const Span span = span_of(a, b);
+        const int n = span.units();
+        if (n == 0) {
+            b++;
             continue;
         }
-        const int64_t at = (page * c.kv_heads + kv) * c.page_size + j % c.page_size;
-        float x[E], s = 0.0f;
-        load_values<FMT, D>(c.k, c.k_scales, at, lane, x);
+        const int seg = static_cast<int>((at - before) / n);
+        const int64_t seg_at = before + static_cast<int64_t>(seg) * n;
+        const int u0 = static_cast<int>(at - seg_at);
+        const int u1 = static_cast<int>(stop - seg_at < n ? stop - seg_at : n);
+        const int kv = seg / a.chunks, chunk = seg % a.chunks;
+        const int head0 = chunk * a.chunk_heads;
+        const int heads = min(a.chunk_heads, a.group - head0);
+        const int64_t row0 = static_cast<int64_t>(b) * a.q_heads + static_cast<int64_t>(kv) * a.group + head0;
+
+        // this warp's units: u0 + warp + W j, j < mine; lane j holds where unit 32 * batch + j lies
+        const int mine = u1 - u0 > warp ? (u1 - u0 - warp + W - 1) / W : 0;
+        auto place_of = [&](int j) -> int64_t {
+            if (j >= mine) return -1;
+            const uint32_t unit = span.first_unit() + u0 + warp + j * W;
+            const uint32_t p = units_per_page == 1 ? unit : static_cast<uint32_t>(__umul64hi(unit, a.page_magic));
+            const int64_t page = a.page_table[b * a.max_pages + p];
+            if (page < 0 || page >= a.c.pages) {
+                atomicCAS(&g_attention_error, 0, 43);
+                return -1;
+            }
+            return (page * a.c.kv_heads + kv) * a.c.page_size + (unit - p * units_per_page) * 16;
+        };
+        int64_t places = place_of(lane), next_places = place_of(32 + lane);
+        load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);
+
+        uint32_t bad = 0;  // bit i: the unit issued i units ago has no page
+        int issued = 0;
+        uint32_t in_buf = ring, out_buf = ring;
+        auto issue = [&]() {
+            if (issued < mine) {
+                if (issued > 0 && (issued & 31) == 0) {
+                    places = next_places;
+                    next_places = place_of(issued + 32 + lane);
+                }
+                const int64_t place = __shfl_sync(0xFFFFFFFFu, places, issued & 31);
+                bad = (bad << 1) | (place < 0 ? 1u : 0u);
+                const int first = (span.first_unit() + u0 + warp + issued * W) * 16;
+                issue_unit<FMT, D, NT>(a.c, in_buf, place, span.start - first, span.end - first, lane);
+            } else {
+                bad <<= 1;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            issued++;
+            in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
+        };
 #pragma unroll
-        for (int e = 0; e < E; e++) s = fmaf(qs[e], x[e], s);
+        for (int i = 0; i < NST - 1; i++) issue();
+        for (int j = 0; j < mine; j++) {
+            cp_async_wait<NST - 2>();
+            __syncwarp();  // the stage is complete for every lane, and the one before it is free
+            issue();
+            const int first = (span.first_unit() + u0 + warp + j * W) * 16;
+            int lo = span.start - first, hi = span.end - first;
+            if ((bad >> (NST - 1)) & 1) lo = hi = 0;
+            attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= 16, lo, hi, lane);
+            out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
+        }
+        cp_async_wait<0>();
+        __syncthreads();  // every ring is free: the joins use its memory
+
+        const int joiners = min(W, u1 - u0);  // warps that had a unit
+        auto result_of = [&](int w) {
+            return reinterpret_cast<float*>(smem + (area_of<FMT>(base, w, S::kArea) - base));
+        };
+        if (warp < joiners) {
+            float* dst = result_of(warp);
+            const int g = lane >> 2, t = lane & 3;
+            const float back = FMT == kKvBf16 ? 1.0f : 1.0f / s.vn;
+            constexpr int RUN = v_run<FMT, D>();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        const float top = fmaxf(m, s), f = expf(m - top), p = expf(s - top);
-        m = top;
-        l = l * f + p;
-        load_values<FMT, D>(c.v, c.v_scales, at, lane, x);
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = fmaf(p, x[e], acc[e] * f);
-    }
+                for (int j = 0; j < 2; j++) {
+                    const int h = nt * 8 + 2 * t + j;
+                    float l = s.l[nt][j];
 #pragma unroll
-    for (int e = 0; e < E; e++) part[warp][lane * E + e] = acc[e];
-    if (lane == 0) part[warp][D] = m, part[warp][D + 1] = l;
-    __syncthreads();
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < 4; w++) top = fmaxf(top, part[w][D]);
-    float f[4];
-    for (int w = 0; w < 4; w++) {
-        f[w] = top == -INFINITY ? 0.0f : expf(part[w][D] - top);
-        sum += f[w] * part[w][D + 1];
-    }
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float o = 0.0f;
-        for (int w = 0; w < 4; w++) o += f[w] * part[w][d];
-        out[(b * q_heads + h) * D + d] = bf16_bits(sum > 0.0f ? o / sum : 0.0f);
+                    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                    if (h < heads) {
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) {
+                            const int dim = (2 * i) / RUN * (8 * RUN) + g * RUN + (2 * i) % RUN;
+                            *reinterpret_cast<float2*>(dst + h * D + dim) =
+                                make_float2(s.o[nt][i][j] * back, s.o[nt][i][j + 2] * back);
+                        }
+                        if (g == 0) {
+                            dst[heads * D + h] = s.m[nt][j];
+                            dst[heads * D + heads + h] = l;
+                        }
+                    }
+                }
+        }
+        __syncthreads();
+        uint2* out = reinterpret_cast<uint2*>(a.out + row0 * D);
+        const bool whole = u0 == 0 && u1 == n;
+        float* slot = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (u0 == 0 ? 1 : 0)) * a.slot_floats;
+        for (int i = threadIdx.x; i < heads * (D / 4); i += W * 32) {
+            const Joined r = join<D, false>(result_of, joiners, heads, i);
+            if (whole) {
+                out[i] = normalised(r);
+            } else {
+                __stcg(reinterpret_cast<float4*>(slot) + i, r.o);
+                if (i % (D / 4) == 0) {
+                    __stcg(slot + heads * D + i / (D / 4), r.top);
+                    __stcg(slot + heads * D + heads + i / (D / 4), r.l);
+                }
+            }
+        }
+        if (!whole) {
+            // the segment's pieces lie in consecutive CTAs; the last to finish joins them
+            __threadfence();
+            __syncthreads();
+            const int64_t c0 = seg_at / share, c1 = (seg_at + n - 1) / share;
+            const unsigned pieces = static_cast<unsigned>(c1 - c0) + 1;
+            if (threadIdx.x == 0) s_last = atomicInc(a.counters + c0, pieces - 1) == pieces - 1;
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                auto piece = [&](int j) -> const float* {
+                    return a.partials + ((c0 + j) * 2 + (j == 0 ? 1 : 0)) * a.slot_floats;
+                };
+                for (int i = threadIdx.x; i < heads * (D / 4); i += W * 32)
+                    out[i] = normalised(join<D, true>(piece, static_cast<int>(pieces), heads, i));
+            }
+        }
+        __syncthreads();  // the joins' memory becomes rings again
+        at = seg_at + u1;
+        if (seg + 1 == segs && u1 == n) {
+            before += static_cast<int64_t>(n) * segs;
+            b++;
+        }
     }
 }
 
-template <int FMT, int D>
-cudaError_t attend(const KvCache& c, const uint16_t* q, const int32_t* page_table, int64_t max_pages,
-                   const int32_t* lengths, int64_t B, int64_t q_heads, float scale, int64_t window, uint16_t* out,
-                   cudaStream_t stream) {
+int slot_floats(int chunk_heads, int D) { return (chunk_heads * (D + 2) + 3) / 4 * 4; }
+
+template <int FMT, int D, int NT>
+cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    using S = Shape<FMT, D, NT>;
+    static std::once_flag attr_once[64];  // once per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t attr_err = cudaSuccess;
+    std::call_once(attr_once[dev & 63], [&] {
+        attr_err = cudaFuncSetAttribute(attention_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        S::kSmem);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    // as many CTAs as SMs, or fewer where the longest possible sequences leave less than that to do
+    const int64_t most = a.B * static_cast<int64_t>(a.c.kv_heads) * a.chunks * ((a.max_pages * a.c.page_size + 15) / 16);
+    int64_t grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
+    if (grid > (most + kMinUnits - 1) / kMinUnits) grid = (most + kMinUnits - 1) / kMinUnits;
+    if (grid < 1) grid = 1;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(q_heads), static_cast<unsigned>(B));
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(S::W * 32);
+    cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_kernel<FMT, D>, c, q, page_table, max_pages, lengths,
-                              static_cast<int>(q_heads), scale, window, out);
+    return cudaLaunchKernelEx(&cfg, attention_kernel<FMT, D, NT>, a);
+}
+
+// Query heads of a kv head in groups of at most 16, as even as they come.
+void head_chunks(int group, int* chunks, int* chunk_heads) {
+    *chunks = (group + 15) / 16;
+    *chunk_heads = (group + *chunks - 1) / *chunks;
+}
+
+template <int FMT, int D>
+cudaError_t launch_nt(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    return a.chunk_heads > 8 ? launch<FMT, D, 2>(a, num_sms, stream) : launch<FMT, D, 1>(a, num_sms, stream);
+}
+
+template <int FMT>
+cudaError_t launch_d(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+    return a.c.head_dim == 64    ? launch_nt<FMT, 64>(a, num_sms, stream)
+           : a.c.head_dim == 128 ? launch_nt<FMT, 128>(a, num_sms, stream)
+                                 : launch_nt<FMT, 256>(a, num_sms, stream);
 }
 
 }  // namespace
 
-int64_t attention_workspace_bytes(int, int, int64_t, int64_t) { return 16; }
+// Workspace: kCounters tickets (zero before the first use, and again after each call), then two partial
+// results a CTA.
+int64_t attention_workspace_bytes(int kv_heads, int head_dim, int64_t, int64_t q_heads) {
+    int chunks, chunk_heads;
+    head_chunks(static_cast<int>(q_heads / kv_heads), &chunks, &chunk_heads);
+    return kCounters * 4 + static_cast<int64_t>(kMaxGrid) * 2 * slot_floats(chunk_heads, head_dim) * 4;
+}
 
 cudaError_t launch_attention(const KvCache& c, const uint16_t* q, const int32_t* page_table, int64_t max_pages,
                              const int32_t* lengths, int64_t B, int64_t q_heads, float scale, int64_t window,
-                             uint16_t* out, void*, int, cudaStream_t stream) {
-#define NF4_CALL(F, D) attend<F, D>(c, q, page_table, max_pages, lengths, B, q_heads, scale, window, out, stream)
-    if (c.format == kKvBf16)
-        return c.head_dim == 64 ? NF4_CALL(kKvBf16, 64) : c.head_dim == 128 ? NF4_CALL(kKvBf16, 128) : NF4_CALL(kKvBf16, 256);
-    if (c.format == kKvFp8)
-        return c.head_dim == 64 ? NF4_CALL(kKvFp8, 64) : c.head_dim == 128 ? NF4_CALL(kKvFp8, 128) : NF4_CALL(kKvFp8, 256);
-    return c.head_dim == 64 ? NF4_CALL(kKvNf4, 64) : c.head_dim == 128 ? NF4_CALL(kKvNf4, 128) : NF4_CALL(kKvNf4, 256);
-#undef NF4_CALL
+                             uint16_t* out, void* workspace, int num_sms, cudaStream_t stream) {
+    AttnArgs a{};
+    a.c = c;
+    a.q = q, a.page_table = page_table, a.lengths = lengths, a.out = out;
+    a.counters = static_cast<uint32_t*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounters * 4);
+    a.max_pages = max_pages, a.window = window;
+    const uint64_t upp = static_cast<uint64_t>(c.page_size / 16);
+    a.page_magic = upp > 1 ? ~uint64_t{0} / upp + 1 : 0;
+    a.B = static_cast<int>(B), a.q_heads = static_cast<int>(q_heads);
+    a.group = static_cast<int>(q_heads / c.kv_heads);
+    head_chunks(a.group, &a.chunks, &a.chunk_heads);
+    a.slot_floats = slot_floats(a.chunk_heads, c.head_dim);
+    a.scale = scale;
+    switch (c.format) {
+        case kKvBf16: return launch_d<kKvBf16>(a, num_sms, stream);
+        case kKvFp8: return launch_d<kKvFp8>(a, num_sms, stream);
+        default: return launch_d<kKvNf4>(a, num_sms, stream);
+    }
 }
 
 cudaError_t read_and_clear_attention_error(int* code) {
