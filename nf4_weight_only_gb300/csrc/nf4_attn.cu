@@ -18,13 +18,14 @@
 // 2^-8, would cost as much as the output's own rounding).  S, m, l and O are fp32 throughout.
 //
 // Work.  A unit is 16 keys of one sequence and kv head (or of one group of at most 16 of its query
-// heads).  The units of all sequences are laid end to end and every CTA takes an equal run of them, so
-// ragged batches, one long sequence and thousands of short ones load the SMs alike; the CTAs work the
-// runs out from the lengths, with no plan from the host.  Inside a run the warps of a CTA take units in
-// turn, each with its own ring of cp.async stages and no block barrier, and join their results in shared
-// memory where a sequence's part of the run ends.  A sequence that crosses runs leaves one partial result
-// a CTA in the workspace; the CTA that finishes last joins them in order, so results do not depend
-// on timing.
+// heads): a segment.  Segments are cut into pieces of about equal size by a rule on the lengths alone, which
+// the kernel works out for itself (no plan from the host), so ragged batches, one long sequence and
+// thousands of short ones load the SMs alike.  A worker is a group of warps, two to a CTA and SM, so that
+// one streams while the other starts or joins a piece.  It takes its first piece by its number and
+// further ones by a ticket.  Inside a piece its warps take units in turn, each with its own ring of
+// cp.async stages and no barrier; their results are joined in shared memory.  The pieces of a segment leave
+// partial results in the workspace; the worker that finishes the last of them joins them in their
+// order (16 at a time, then the joined ones), so results do not depend on timing.
 #include <mutex>
 
 #include "nf4_kv.cuh"
@@ -35,9 +36,12 @@ namespace {
 // Error word of the attention (43: a page or a length outside its bounds).
 __device__ int g_attention_error;
 
-constexpr int kMaxGrid = 320;         // CTAs a launch has at most (workspace slots)
-constexpr int kCounters = 1024;       // ticket counters at the start of the workspace
-constexpr int kMinUnits = 8;          // smallest run worth a CTA
+constexpr int kMaxWorkers = 320;
+constexpr int kPiecesPerWorker = 4;   // where the work allows it: evens out the SMs' different speeds
+constexpr int kLongUnits = 16;        // units a warp in the smallest piece worth a ticket of its own
+constexpr int kFanIn = 16;            // partial results joined at a time
+constexpr int kMostBatches = (kMaxWorkers * kPiecesPerWorker + kFanIn) / kFanIn + 1;
+constexpr int kSlots = 2 * kMaxWorkers * kPiecesPerWorker + 2;  // partial results (see slot0 in the kernel)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;         // p may reach 2^8 before the running maximum moves
 
@@ -47,8 +51,9 @@ struct AttnArgs {
     const int32_t* page_table;
     const int32_t* lengths;
     uint16_t* out;
-    uint32_t* counters;
-    float* partials;
+    uint32_t* tickets;  // [0] pieces handed out, [1] workers done
+    uint32_t* joins;    // [2][kSlots] partial results of a batch, batches of a segment
+    float* partials;    // [kSlots][slot_floats]
     int64_t max_pages, window;
     uint64_t page_magic;  // ceil(2^64 / (page_size / 16))
     int B, q_heads, group;
@@ -152,17 +157,19 @@ struct Shape {
     // Warps and stages: enough warps to issue the decoding (16 for the quantised formats where their
     // registers allow it), and about 100 KB in flight an SM.
     static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : (NT == 2 || D == 256) ? 8 : 16;
+    static constexpr int NG = 2, WG = W / NG;                    // workers a CTA, warps a worker
     static constexpr int kRingMost = FMT == kKvNf4 ? (W == 16 ? 10240 : 20480) : 204800 / W;
     static constexpr int kStagesFit = kRingMost / kStage;
-    static constexpr int NST = kStagesFit > 6 ? 6 : kStagesFit;
+    static constexpr int NST = kStagesFit > 10 ? 10 : kStagesFit;
     static constexpr int kRing = NST * kStage;
     static constexpr int kResult = NT * 8 * (D + 2) * 4;         // bytes of a warp's result
-    static constexpr int kSmem = 226 * 1024;                     // dynamic; with 1 KB of static, all there is
+    static constexpr int kSmem = 225 * 1024;                     // dynamic; with 2 KB of static, all there is
     static constexpr int kArea = kRing > kResult ? kRing : kResult;
-    // dynamic shared memory starts 1 to 4 KB into the window
+    static_assert(kArea >= kMostBatches * 2 * NT * 8 * 4, "an area holds the maxima and sums of the last join");
+    // dynamic shared memory starts 2 to 4 KB into the window
     static constexpr int kBelow = FMT == kKvNf4 ? static_cast<int>(kTableAt - 4096) / kArea : W;
     static_assert(NST >= 2, "a ring has at least two stages");
-    static_assert(FMT == kKvNf4 ? (W - kBelow) * kArea <= kSmem + 1024 - static_cast<int>(kTableEnd)
+    static_assert(FMT == kKvNf4 ? (W - kBelow) * kArea <= kSmem + 2048 - static_cast<int>(kTableEnd)
                                 : W * kArea <= kSmem, "the areas fit");
 };
 
@@ -190,21 +197,16 @@ __device__ __forceinline__ uint32_t nf4_piece(int k, int r) {
 // ---------------------------------------------------------------------------------------------
 // One unit into a stage
 // ---------------------------------------------------------------------------------------------
-// place: vector index of the unit's first key, or -1 (a page outside the cache: zeros).  lo and hi: the
-// live keys of the unit; dead ones are filled with zeros so that nothing non-finite meets a weight of 0.
-template <int FMT, int D, int NT>
-__device__ __forceinline__ void issue_unit(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+// place: vector index of the unit's first key.  lo and hi: the live keys of the unit (ALL: every one);
+// dead ones are filled with zeros so that nothing non-finite meets a weight of 0.
+template <int FMT, int D, int NT, bool ALL>
+__device__ __forceinline__ void copy_unit(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
     using S = Shape<FMT, D, NT>;
     const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
-    if (place < 0) {
-        for (int i = lane * 4; i < S::kStage; i += 128)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + i), "r"(0) : "memory");
-        return;
-    }
     const int g = lane >> 2, t = lane & 3;
     const uint8_t* k = c.k + place * S::VB;
     const uint8_t* v = c.v + place * S::VB;
-    auto live = [&](int key) { return key >= lo && key < hi; };
+    auto live = [&](int key) { return ALL || (key >= lo && key < hi); };
     if (FMT == kKvNf4) {
         constexpr int P = S::VB / 16;  // 16-byte pieces of a vector
 #pragma unroll
@@ -247,6 +249,19 @@ __device__ __forceinline__ void issue_unit(const KvCache& c, uint32_t buf, int64
                 cp_async<4>(sb + o, (o < S::SB ? ks : vs) + at, on);
             }
         }
+    }
+}
+
+// The same for a place that may be -1 (a page outside the cache: zeros).
+template <int FMT, int D, int NT>
+__device__ __forceinline__ void issue_unit(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+    if (place < 0) {
+        for (int i = lane * 4; i < Shape<FMT, D, NT>::kStage; i += 128)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + i), "r"(0) : "memory");
+    } else if (lo <= 0 && hi >= 16) {
+        copy_unit<FMT, D, NT, true>(c, buf, place, lo, hi, lane);
+    } else {
+        copy_unit<FMT, D, NT, false>(c, buf, place, lo, hi, lane);
     }
 }
 
@@ -598,25 +613,23 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 }
 
 // Four dims of one head, joined over `n` results in their order: part(j) is result j, [heads][D] sums of
-// weighted values, [heads] maxima, [heads] sums of weights.
+// weighted values, [heads] maxima, [heads] sums of weights.  ml: the maxima and sums of all results,
+// [n][2 heads], in shared memory.
 struct Joined {
     float4 o;
     float top, l;
 };
 template <int D, bool GLOBAL, typename Part>
-__device__ __forceinline__ Joined join(const Part& part, int n, int heads, int i) {
-    auto ld = [](const float* p) { return GLOBAL ? __ldcg(p) : *p; };
+__device__ __forceinline__ Joined join(const Part& part, const float* ml, int n, int heads, int i) {
     const int h = i / (D / 4);
     Joined r{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -3e38f, 0.0f};
-#pragma unroll 4
-    for (int j = 0; j < n; j++) r.top = fmaxf(r.top, ld(part(j) + heads * D + h));
-#pragma unroll 4
+    for (int j = 0; j < n; j++) r.top = fmaxf(r.top, ml[j * 2 * heads + h]);
+#pragma unroll 8
     for (int j = 0; j < n; j++) {
-        const float* p = part(j);
-        const float f = exp2_approx(ld(p + heads * D + h) - r.top);
-        r.l = fmaf(f, ld(p + heads * D + heads + h), r.l);
-        const float4* q = reinterpret_cast<const float4*>(p) + i;
-        const float4 v = GLOBAL ? __ldcg(q) : *q;
+        const float4* p = reinterpret_cast<const float4*>(part(j)) + i;
+        const float4 v = GLOBAL ? __ldcg(p) : *p;
+        const float f = exp2_approx(ml[j * 2 * heads + h] - r.top);
+        r.l = fmaf(f, ml[j * 2 * heads + heads + h], r.l);
         r.o.x = fmaf(f, v.x, r.o.x), r.o.y = fmaf(f, v.y, r.o.y);
         r.o.z = fmaf(f, v.z, r.o.z), r.o.w = fmaf(f, v.w, r.o.w);
     }
@@ -626,17 +639,71 @@ __device__ __forceinline__ uint2 normalised(const Joined& r) {
     const float f = r.l > 0.0f ? 1.0f / r.l : 0.0f;
     return make_uint2(f32x2_to_bf16x2(r.o.x * f, r.o.y * f), f32x2_to_bf16x2(r.o.z * f, r.o.w * f));
 }
+template <int D>
+__device__ __forceinline__ void store_partial(float* slot, const Joined& r, int heads, int i) {
+    __stcg(reinterpret_cast<float4*>(slot) + i, r.o);
+    if (i % (D / 4) == 0) {
+        __stcg(slot + heads * D + i / (D / 4), r.top);
+        __stcg(slot + heads * D + heads + i / (D / 4), r.l);
+    }
+}
+
+template <int THREADS>
+__device__ __forceinline__ void worker_barrier(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(THREADS) : "memory");
+}
+
+// A sequence among the others: its span, and what precedes it.
+struct Place {
+    int b;
+    int64_t units_before;  // units of the sequences before it, all segments
+    uint32_t pieces_before;
+};
+
+// The sequence whose pieces include number `id`, searched from `at` on (b = B: none).  Every segment of
+// a sequence of n units has ceil(n / cut) pieces.  The whole warp calls it.
+__device__ __forceinline__ Place locate(const AttnArgs& a, Place at, uint32_t id, int cut, int segs, int lane) {
+    while (at.b < a.B) {
+        const int b = at.b + lane;
+        const int n = b < a.B ? span_of(a, b).units() : 0;
+        const uint32_t p = static_cast<uint32_t>((n + cut - 1) / cut) * segs;
+        uint32_t sum = p;
+        int64_t units = static_cast<int64_t>(n) * segs;
+        const int64_t own = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            const int64_t up_units = __shfl_up_sync(0xFFFFFFFFu, units, o);
+            if (lane >= o) sum += up, units += up_units;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, at.pieces_before + sum > id);
+        if (past) {
+            const int f = __ffs(past) - 1;
+            at.b += f;
+            at.units_before += __shfl_sync(0xFFFFFFFFu, units - own, f);
+            at.pieces_before += __shfl_sync(0xFFFFFFFFu, sum - p, f);
+            return at;
+        }
+        at.b += 32;
+        at.units_before += __shfl_sync(0xFFFFFFFFu, units, 31);
+        at.pieces_before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+    }
+    at.b = a.B;
+    return at;
+}
 
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel(const AttnArgs a) {
     using S = Shape<FMT, D, NT>;
-    constexpr int W = S::W, NST = S::NST;
+    constexpr int WG = S::WG, NST = S::NST, THREADS = WG * 32;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ int s_last;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    __shared__ uint32_t s_word[S::NG][2];            // a worker's next piece; whether it joins
+    __shared__ float s_ml[S::NG][WG * 2 * NT * 8];   // the maxima and sums of its warps
+    const int lane = threadIdx.x % 32, group = threadIdx.x / THREADS;
+    const int tid = threadIdx.x % THREADS, warp = tid / 32;  // in the worker
     const uint32_t base = smem_u32(smem);
     if (FMT == kKvNf4) {
-        for (int i = threadIdx.x; i < 256 * 32; i += W * 32) {
+        for (int i = threadIdx.x; i < 256 * 32; i += S::W * 32) {
             const int v = i >> 5;
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(kTableAt + v * 256 + (i & 31) * 4),
                          "r"(pack_f16(kTableF16[v & 15], kTableF16[v >> 4]))
@@ -651,129 +718,100 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         return;
     }
 
-    // total units, and (block 0) lengths out of bounds
-    const int segs = a.c.kv_heads * a.chunks;  // runs of units a sequence
+    // all units, and with them the size that segments are cut to
+    const int segs = a.c.kv_heads * a.chunks;  // segments of a sequence
+    const uint32_t worker = blockIdx.x * S::NG + group, workers = gridDim.x * S::NG;
     int64_t total = 0;
+    for (int b = lane; b < a.B; b += 32) total += span_of(a, b).units();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    total *= segs;
+    int cut;
     {
-        int64_t mine = 0;
-        for (int b = lane; b < a.B; b += 32) {
-            mine += span_of(a, b).units();
-            if (blockIdx.x == 0 && warp == 0 && a.lengths[b] > a.max_pages * a.c.page_size)
-                atomicCAS(&g_attention_error, 0, 43);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-        total = mine * segs;
-    }
-    // sequences with nothing to attend to
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)
-        if (span_of(a, b).units() == 0)
-            for (int i = threadIdx.x; i < a.q_heads * D / 8; i += W * 32)
-                reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * D / 8) + i] = make_uint4(0, 0, 0, 0);
-
-    int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    if (share < kMinUnits) share = kMinUnits;
-    int64_t at = blockIdx.x * share;
-    const int64_t stop = at + share < total ? at + share : total;
-    if (at >= stop) return;
-
-    // the sequence that unit `at` belongs to, and the units before it
-    int b = 0;
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += 32) {
-        int64_t u = b0 + lane < a.B ? static_cast<int64_t>(span_of(a, b0 + lane).units()) * segs : 0, sum = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += up;
-        }
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + sum > at);
-        if (past) {
-            const int f = __ffs(past) - 1;
-            b = b0 + f;
-            before += __shfl_sync(0xFFFFFFFFu, sum - u, f);
-            break;
-        }
-        before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        const int64_t one = (total + workers - 1) / workers;  // a piece for each worker
+        const int64_t some = (total + workers * kPiecesPerWorker - 1) / (workers * kPiecesPerWorker);
+        int64_t c = one <= kLongUnits * WG ? one : some > kLongUnits * WG ? some : kLongUnits * WG;
+        if (c < WG) c = WG;
+        cut = static_cast<int>(c < (1 << 30) ? c : (1 << 30));
     }
 
-    const uint32_t ring = area_of<FMT>(base, warp, S::kArea);
+    const uint32_t ring = area_of<FMT>(base, group * WG + warp, S::kArea);
+    auto area = [&](int w) {  // of warp w of this worker, once its ring is drained
+        return reinterpret_cast<float*>(smem + (area_of<FMT>(base, group * WG + w, S::kArea) - base));
+    };
     const int units_per_page = a.c.page_size >> 4;
     WarpState<FMT, D, NT> s;
-    while (at < stop) {
-        // the piece of this run in one segment: units [u0, u1) of its n
-        const Span span = span_of(a, b);
+    Place at{0, 0, 0};
+    for (uint32_t id = worker;;) {
+        at = locate(a, at, id, cut, segs, lane);
+        if (at.b == a.B) break;
+        uint32_t next = 0;
+        if (tid == 0) next = atomicAdd(a.tickets, 1u) + workers;  // arrives while the piece is worked on
+        // piece `part` of `parts` of segment `seg`: units [u0, u1) of its n
+        const Span span = span_of(a, at.b);
         const int n = span.units();
-        if (n == 0) {
-            b++;
-            continue;
-        }
-        const int seg = static_cast<int>((at - before) / n);
-        const int64_t seg_at = before + static_cast<int64_t>(seg) * n;
-        const int u0 = static_cast<int>(at - seg_at);
-        const int u1 = static_cast<int>(stop - seg_at < n ? stop - seg_at : n);
-        const int kv = seg / a.chunks, chunk = seg % a.chunks;
-        const int head0 = chunk * a.chunk_heads;
+        const uint32_t parts = static_cast<uint32_t>((n + cut - 1) / cut);
+        const uint32_t in_seq = id - at.pieces_before;
+        const int seg = static_cast<int>(in_seq / parts);
+        const uint32_t part = in_seq - seg * parts;
+        const int len = static_cast<int>((n + parts - 1) / parts);
+        const int u0 = min(n, static_cast<int>(part) * len), u1 = min(n, u0 + len);
+        const int kv = seg / a.chunks, head0 = (seg - kv * a.chunks) * a.chunk_heads;
         const int heads = min(a.chunk_heads, a.group - head0);
-        const int64_t row0 = static_cast<int64_t>(b) * a.q_heads + static_cast<int64_t>(kv) * a.group + head0;
+        const int64_t row0 = static_cast<int64_t>(at.b) * a.q_heads + static_cast<int64_t>(kv) * a.group + head0;
 
-        // this warp's units: u0 + warp + W j, j < mine; lane j holds where unit 32 * batch + j lies
-        const int mine = u1 - u0 > warp ? (u1 - u0 - warp + W - 1) / W : 0;
+        // this warp's units: u0 + warp + WG j, j < mine; lane j holds where unit 32 * batch + j lies
+        const int mine = u1 - u0 > warp ? (u1 - u0 - warp + WG - 1) / WG : 0;
+        const int first = span.first_unit() + u0 + warp;
         auto place_of = [&](int j) -> int64_t {
             if (j >= mine) return -1;
-            const uint32_t unit = span.first_unit() + u0 + warp + j * W;
+            const uint32_t unit = first + j * WG;
             const uint32_t p = units_per_page == 1 ? unit : static_cast<uint32_t>(__umul64hi(unit, a.page_magic));
-            const int64_t page = a.page_table[b * a.max_pages + p];
+            const int64_t page = a.page_table[at.b * a.max_pages + p];
             if (page < 0 || page >= a.c.pages) {
                 atomicCAS(&g_attention_error, 0, 43);
                 return -1;
             }
             return (page * a.c.kv_heads + kv) * a.c.page_size + (unit - p * units_per_page) * 16;
         };
-        int64_t places = place_of(lane), next_places = place_of(32 + lane);
+        int64_t places = place_of(lane), next_places = mine > 32 ? place_of(32 + lane) : -1;
         load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);
 
         uint32_t bad = 0;  // bit i: the unit issued i units ago has no page
-        int issued = 0;
         uint32_t in_buf = ring, out_buf = ring;
-        auto issue = [&]() {
-            if (issued < mine) {
-                if (issued > 0 && (issued & 31) == 0) {
+        for (int j = 1 - NST; j < mine; j++) {
+            if (j >= 0) {
+                cp_async_wait<NST - 2>();
+                __syncwarp();  // the stage is complete for every lane, and the one before it is free
+            }
+            const int ahead = j + NST - 1;
+            bad <<= 1;
+            if (ahead < mine) {
+                if (ahead > 0 && (ahead & 31) == 0) {
                     places = next_places;
-                    next_places = place_of(issued + 32 + lane);
+                    next_places = place_of(ahead + 32 + lane);
                 }
-                const int64_t place = __shfl_sync(0xFFFFFFFFu, places, issued & 31);
-                bad = (bad << 1) | (place < 0 ? 1u : 0u);
-                const int first = (span.first_unit() + u0 + warp + issued * W) * 16;
-                issue_unit<FMT, D, NT>(a.c, in_buf, place, span.start - first, span.end - first, lane);
-            } else {
-                bad <<= 1;
+                const int64_t place = __shfl_sync(0xFFFFFFFFu, places, ahead & 31);
+                bad |= place < 0 ? 1u : 0u;
+                const int key0 = (first + ahead * WG) * 16;
+                issue_unit<FMT, D, NT>(a.c, in_buf, place, span.start - key0, span.end - key0, lane);
+                in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            issued++;
-            in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
-        };
-#pragma unroll
-        for (int i = 0; i < NST - 1; i++) issue();
-        for (int j = 0; j < mine; j++) {
-            cp_async_wait<NST - 2>();
-            __syncwarp();  // the stage is complete for every lane, and the one before it is free
-            issue();
-            const int first = (span.first_unit() + u0 + warp + j * W) * 16;
-            int lo = span.start - first, hi = span.end - first;
-            if ((bad >> (NST - 1)) & 1) lo = hi = 0;
-            attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= 16, lo, hi, lane);
-            out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
+            if (j >= 0) {
+                const int key0 = (first + j * WG) * 16;
+                int lo = span.start - key0, hi = span.end - key0;
+                if ((bad >> (NST - 1)) & 1) lo = hi = 0;
+                attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= 16, lo, hi, lane);
+                out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
+            }
         }
         cp_async_wait<0>();
-        __syncthreads();  // every ring is free: the joins use its memory
+        __syncwarp();  // the warp's ring is drained: its memory takes the warp's result
 
-        const int joiners = min(W, u1 - u0);  // warps that had a unit
-        auto result_of = [&](int w) {
-            return reinterpret_cast<float*>(smem + (area_of<FMT>(base, w, S::kArea) - base));
-        };
+        const int joiners = min(WG, u1 - u0);  // warps that had a unit
         if (warp < joiners) {
-            float* dst = result_of(warp);
+            float* dst = area(warp);
             const int g = lane >> 2, t = lane & 3;
             const float back = FMT == kKvBf16 ? 1.0f : (FMT == kKvNf4 ? 1.0f / kTableUnit : 1.0f) / s.vn;
             constexpr int RUN = v_run<FMT, D>();
@@ -793,52 +831,71 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                                 make_float2(s.o[nt][i][j] * back, s.o[nt][i][j + 2] * back);
                         }
                         if (g == 0) {
-                            dst[heads * D + h] = s.m[nt][j];
-                            dst[heads * D + heads + h] = l;
+                            s_ml[group][warp * 2 * heads + h] = s.m[nt][j];
+                            s_ml[group][warp * 2 * heads + heads + h] = l;
                         }
                     }
                 }
         }
-        __syncthreads();
+        if (tid == 0) s_word[group][0] = next;
+        worker_barrier<THREADS>(group);
+        id = s_word[group][0];
         uint2* out = reinterpret_cast<uint2*>(a.out + row0 * D);
-        const bool whole = u0 == 0 && u1 == n;
-        float* slot = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (u0 == 0 ? 1 : 0)) * a.slot_floats;
-        for (int i = threadIdx.x; i < heads * (D / 4); i += W * 32) {
-            const Joined r = join<D, false>(result_of, joiners, heads, i);
-            if (whole) {
+        const int columns = heads * (D / 4);
+        // slots of a segment's pieces: segments that are cut have more than `cut` units, so these runs are
+        // disjoint
+        const int64_t slot0 = parts > 1 ? 2 * ((at.units_before + static_cast<int64_t>(seg) * n) / cut) : 0;
+        auto slot = [&](int64_t i) { return a.partials + (slot0 + i) * a.slot_floats; };
+        for (int i = tid; i < columns; i += THREADS) {
+            const Joined r = join<D, false>(area, s_ml[group], joiners, heads, i);
+            if (parts == 1)
                 out[i] = normalised(r);
-            } else {
-                __stcg(reinterpret_cast<float4*>(slot) + i, r.o);
-                if (i % (D / 4) == 0) {
-                    __stcg(slot + heads * D + i / (D / 4), r.top);
-                    __stcg(slot + heads * D + heads + i / (D / 4), r.l);
-                }
-            }
+            else
+                store_partial<D>(slot(part), r, heads, i);
         }
-        if (!whole) {
-            // the segment's pieces lie in consecutive CTAs; the last to finish joins them
+        // joins `count` slots, `step` apart, once `tickets` says that all of them are there
+        auto join_slots = [&](uint32_t* ticket, int64_t from, int step, int count, bool last) {
             __threadfence();
-            __syncthreads();
-            const int64_t c0 = seg_at / share, c1 = (seg_at + n - 1) / share;
-            const unsigned pieces = static_cast<unsigned>(c1 - c0) + 1;
-            if (threadIdx.x == 0) s_last = atomicInc(a.counters + c0, pieces - 1) == pieces - 1;
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                auto piece = [&](int j) -> const float* {
-                    return a.partials + ((c0 + j) * 2 + (j == 0 ? 1 : 0)) * a.slot_floats;
-                };
-                for (int i = threadIdx.x; i < heads * (D / 4); i += W * 32)
-                    out[i] = normalised(join<D, true>(piece, static_cast<int>(pieces), heads, i));
+            worker_barrier<THREADS>(group);
+            if (tid == 0) s_word[group][1] = atomicInc(ticket, count - 1) == static_cast<unsigned>(count - 1);
+            worker_barrier<THREADS>(group);
+            if (!s_word[group][1]) return false;
+            __threadfence();
+            float* ml = area(0);
+            for (int i = tid; i < count * 2 * heads; i += THREADS) {
+                const int j = i / (2 * heads);
+                ml[i] = __ldcg(slot(from + static_cast<int64_t>(j) * step) + heads * D + (i - j * 2 * heads));
             }
+            worker_barrier<THREADS>(group);
+            auto piece = [&](int j) { return slot(from + static_cast<int64_t>(j) * step); };
+            for (int i = tid; i < columns; i += THREADS) {
+                const Joined r = join<D, true>(piece, ml, count, heads, i);
+                if (last)
+                    out[i] = normalised(r);
+                else
+                    store_partial<D>(slot(from), r, heads, i);
+            }
+            return true;
+        };
+        if (parts > 1) {
+            const int batch = part / kFanIn, batches = (parts + kFanIn - 1) / kFanIn;
+            const int64_t from = static_cast<int64_t>(batch) * kFanIn;
+            const int count = min(kFanIn, static_cast<int>(parts) - batch * kFanIn);
+            if (join_slots(a.joins + slot0 + from, from, 1, count, batches == 1) && batches > 1)
+                join_slots(a.joins + kSlots + slot0, 0, kFanIn, batches, true);
         }
-        __syncthreads();  // the joins' memory becomes rings again
-        at = seg_at + u1;
-        if (seg + 1 == segs && u1 == n) {
-            before += static_cast<int64_t>(n) * segs;
-            b++;
-        }
+        worker_barrier<THREADS>(group);  // the areas become rings again
     }
+
+    // sequences with nothing to attend to, and lengths past their tables
+    for (int b = blockIdx.x * S::W + threadIdx.x / 32; b < a.B; b += gridDim.x * S::W) {
+        if (lane == 0 && a.lengths[b] > a.max_pages * a.c.page_size) atomicCAS(&g_attention_error, 0, 43);
+        if (span_of(a, b).units() == 0)
+            for (int i = lane; i < a.q_heads * (D / 8); i += 32)
+                reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * (D / 8)) + i] = make_uint4(0, 0, 0, 0);
+    }
+    // the last worker leaves the tickets as it found them
+    if (tid == 0 && atomicInc(a.tickets + 1, workers - 1) == workers - 1) a.tickets[0] = 0;
 }
 
 int slot_floats(int chunk_heads, int D) { return (chunk_heads * (D + 2) + 3) / 4 * 4; }
@@ -857,8 +914,8 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
     if (attr_err != cudaSuccess) return attr_err;
     // as many CTAs as SMs, or fewer where the longest possible sequences leave less than that to do
     const int64_t most = a.B * static_cast<int64_t>(a.c.kv_heads) * a.chunks * ((a.max_pages * a.c.page_size + 15) / 16);
-    int64_t grid = num_sms < kMaxGrid ? num_sms : kMaxGrid;
-    if (grid > (most + kMinUnits - 1) / kMinUnits) grid = (most + kMinUnits - 1) / kMinUnits;
+    int64_t grid = num_sms < kMaxWorkers / S::NG ? num_sms : kMaxWorkers / S::NG;
+    if (grid > (most + S::W - 1) / S::W) grid = (most + S::W - 1) / S::W;
     if (grid < 1) grid = 1;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -893,12 +950,12 @@ cudaError_t launch_d(const AttnArgs& a, int num_sms, cudaStream_t stream) {
 
 }  // namespace
 
-// Workspace: kCounters tickets (zero before the first use, and again after each call), then two partial
-// results a CTA.
+// Workspace: the tickets (zero before the first use, and again after each call), then the partial results.
+constexpr int kControlBytes = (16 + 2 * kSlots * 4 + 255) / 256 * 256;
 int64_t attention_workspace_bytes(int kv_heads, int head_dim, int64_t, int64_t q_heads) {
     int chunks, chunk_heads;
     head_chunks(static_cast<int>(q_heads / kv_heads), &chunks, &chunk_heads);
-    return kCounters * 4 + static_cast<int64_t>(kMaxGrid) * 2 * slot_floats(chunk_heads, head_dim) * 4;
+    return kControlBytes + static_cast<int64_t>(kSlots) * slot_floats(chunk_heads, head_dim) * 4;
 }
 
 cudaError_t launch_attention(const KvCache& c, const uint16_t* q, const int32_t* page_table, int64_t max_pages,
@@ -907,8 +964,9 @@ cudaError_t launch_attention(const KvCache& c, const uint16_t* q, const int32_t*
     AttnArgs a{};
     a.c = c;
     a.q = q, a.page_table = page_table, a.lengths = lengths, a.out = out;
-    a.counters = static_cast<uint32_t*>(workspace);
-    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounters * 4);
+    a.tickets = static_cast<uint32_t*>(workspace);
+    a.joins = a.tickets + 4;
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kControlBytes);
     a.max_pages = max_pages, a.window = window;
     const uint64_t upp = static_cast<uint64_t>(c.page_size / 16);
     a.page_magic = upp > 1 ? ~uint64_t{0} / upp + 1 : 0;
