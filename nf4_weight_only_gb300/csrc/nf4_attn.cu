@@ -17,7 +17,7 @@
 // that follows the largest scale.  With a bf16 cache p goes in as the sum of two bf16 numbers (one alone,
 // 2^-8, would cost as much as the output's own rounding).  S, m, l and O are fp32 throughout.
 //
-// Work.  A unit is 16 keys of one sequence and kv head (or of one group of at most 16 of its query
+// Work.  A unit is 16 or 32 keys of one sequence and kv head (or of one group of at most 16 of its query
 // heads): a segment.  Segments are cut into pieces of about equal size by a rule on the lengths alone, which
 // the kernel works out for itself (no plan from the host), so ragged batches, one long sequence and
 // thousands of short ones load the SMs alike.  A worker is a group of warps, two to a CTA and SM, so that
@@ -142,6 +142,14 @@ __device__ __constant__ const float kTableF16[16] = {
     -0.058135986328125f, 0.0f,            0.050811767578125f, 0.10272216796875f, 0.1571044921875f, 0.2156982421875f,
     0.28125f,          0.359130859375f,   0.46142578125f,    0.63818359375f};
 
+// The four e4m3 codes of a word -> two fp16 pairs (bytes 0, 1 and bytes 2, 3), exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 // Shared memory of a CTA.  NF4 keeps its pair table at shared address 64 KB, entry v (a code byte) at
 // 256 v and lane l's copy 4 l into it, so one byte permute of a code word and the lane's constant is a
 // lookup's whole address and the 32 lanes never conflict.  The warps' rings lie on both sides of it.
@@ -153,12 +161,16 @@ struct Shape {
     static constexpr int VB = kv_vector_bytes(FMT, D);           // bytes of a vector
     static constexpr int SB = 16 * kv_scale_bytes(FMT, D);       // bytes of 16 keys' scales of one side
     static constexpr int GR = FMT == kKvNf4 ? D / 64 : 1;        // scale groups of a vector
-    static constexpr int kStage = 32 * VB + 2 * SB;              // 16 keys, K and V
+    // Blocks of 16 keys in a unit: two give the decoding formats two independent chains and halve the
+    // bookkeeping, where registers and shared memory allow it.
+    static constexpr int KS = FMT != kKvBf16 && NT == 1 && D <= 128 ? 2 : 1;
+    static constexpr int kBlock = 32 * VB + 2 * SB;              // 16 keys, K and V
+    static constexpr int kStage = KS * kBlock;
     // Warps and stages: enough warps to issue the decoding (16 for the quantised formats where their
     // registers allow it), and about 100 KB in flight an SM.
-    static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : (NT == 2 || D == 256) ? 8 : 16;
+    static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : (NT == 2 || D == 256) ? 8 : FMT == kKvFp8 ? 12 : 16;
     static constexpr int NG = 2, WG = W / NG;                    // workers a CTA, warps a worker
-    static constexpr int kRingMost = FMT == kKvNf4 ? (W == 16 ? 10240 : 20480) : 204800 / W;
+    static constexpr int kRingMost = FMT == kKvNf4 ? (W == 16 ? 10240 : 20480) : 230400 / W / 16 * 16;
     static constexpr int kStagesFit = kRingMost / kStage;
     static constexpr int NST = kStagesFit > 10 ? 10 : kStagesFit;
     static constexpr int kRing = NST * kStage;
@@ -195,12 +207,12 @@ __device__ __forceinline__ uint32_t nf4_piece(int k, int r) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// One unit into a stage
+// One block of 16 keys into its part of a stage
 // ---------------------------------------------------------------------------------------------
-// place: vector index of the unit's first key.  lo and hi: the live keys of the unit (ALL: every one);
+// place: vector index of the block's first key.  lo and hi: its live keys (ALL: every one);
 // dead ones are filled with zeros so that nothing non-finite meets a weight of 0.
 template <int FMT, int D, int NT, bool ALL>
-__device__ __forceinline__ void copy_unit(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+__device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
     using S = Shape<FMT, D, NT>;
     const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
     const int g = lane >> 2, t = lane & 3;
@@ -252,16 +264,16 @@ __device__ __forceinline__ void copy_unit(const KvCache& c, uint32_t buf, int64_
     }
 }
 
-// The same for a place that may be -1 (a page outside the cache: zeros).
+// The same for a place that may be negative (nothing to read: zeros).
 template <int FMT, int D, int NT>
-__device__ __forceinline__ void issue_unit(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+__device__ __forceinline__ void issue_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
     if (place < 0) {
-        for (int i = lane * 4; i < Shape<FMT, D, NT>::kStage; i += 128)
+        for (int i = lane * 4; i < Shape<FMT, D, NT>::kBlock; i += 128)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + i), "r"(0) : "memory");
     } else if (lo <= 0 && hi >= 16) {
-        copy_unit<FMT, D, NT, true>(c, buf, place, lo, hi, lane);
+        copy_block<FMT, D, NT, true>(c, buf, place, lo, hi, lane);
     } else {
-        copy_unit<FMT, D, NT, false>(c, buf, place, lo, hi, lane);
+        copy_block<FMT, D, NT, false>(c, buf, place, lo, hi, lane);
     }
 }
 
@@ -341,14 +353,15 @@ __device__ __forceinline__ void load_q(const AttnArgs& a, WarpState<FMT, D, NT>&
     s.vlim = -1.0f;
 }
 
-// One unit of 16 keys from its stage.  lo, hi: its live keys (full: all of them).
+// One unit from its stage.  full: every key is live; otherwise [lo, hi) are, without the blocks whose bit
+// is set in `bad`.
 template <int FMT, int D, int NT>
 __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t buf, bool full, int lo, int hi,
-                                            int lane) {
+                                            uint32_t bad, int lane) {
     using S = Shape<FMT, D, NT>;
     constexpr bool BF = S::kBf;
-    constexpr int GR = S::GR;
-    const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
+    constexpr int GR = S::GR, KS = S::KS;
+    constexpr uint32_t VOFF = 16 * S::VB, SOFF = 32 * S::VB;  // of a block's V and scales
     const int g = lane >> 2, t = lane & 3, key = key_of_row(g);
     // the lane's constant in a table lookup's address: 64 KB and 4 * lane around the code byte
     const uint32_t column = (kTableAt >> 8) | static_cast<uint32_t>(4 * lane);
@@ -356,100 +369,112 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
         return lds_table(prmt(word, column, 0x6504u + 16u * static_cast<uint32_t>(byte)));
     };
 
-    // S = K q^T: two chains a product (a chain for each scale group with NF4)
+    // S = K q^T: two chains a block (a chain for each scale group with NF4)
     constexpr int CH = FMT == kKvNf4 ? GR : 2;
-    float sc[NT][CH][4];
+    float sc[KS][NT][CH][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++)
+    for (int b = 0; b < KS; b++) {
 #pragma unroll
-        for (int c = 0; c < CH; c++)
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int j = 0; j < 4; j++) sc[nt][c][j] = 0.0f;
-    if (FMT == kKvNf4) {
+            for (int c = 0; c < CH; c++)
 #pragma unroll
-        for (int r = 0; r < GR; r++) {
-            const uint2 u = lds64(kb + nf4_piece<D>(key, r) + t * 8);
-            const uint2 w = lds64(kb + nf4_piece<D>(key + 8, r) + t * 8);
+                for (int j = 0; j < 4; j++) sc[b][nt][c][j] = 0.0f;
+        const uint32_t kb = buf + b * S::kBlock;
+        if (FMT == kKvNf4) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) {  // four dims a row each
-                const uint32_t x = i < 2 ? u.x : u.y, y = i < 2 ? w.x : w.y;
-                const int b = 2 * (i & 1);
-                const uint32_t f[4] = {pair_of(x, b), pair_of(y, b), pair_of(x, b + 1), pair_of(y, b + 1)};
+            for (int r = 0; r < GR; r++) {
+                const uint32_t at = kb + nf4_piece<D>(key, r) + t * 8;
+                const uint2 u = lds64(at), w = lds64(at + 8 * S::VB);
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-                    mma16816<false>(sc[nt][r], f, s.q[nt][r * 4 + i][0], s.q[nt][r * 4 + i][1]);
-            }
-        }
-    } else {
-        constexpr int CK = S::VB / 4 < 16 ? S::VB / 4 : 16, NK = S::VB / 4 / CK, WK = CK / 4;
-#pragma unroll
-        for (int i = 0; i < NK; i++) {
-            uint32_t x[WK], y[WK];
-            const uint4 u = lds128a(kb + (i * 32 + lane) * CK), w = lds128a(kb + ((NK + i) * 32 + lane) * CK);
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-            y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
-            if (BF) {
-#pragma unroll
-                for (int j = 0; j < WK / 2; j++) {
-                    const uint32_t f[4] = {x[2 * j], y[2 * j], x[2 * j + 1], y[2 * j + 1]};
+                for (int i = 0; i < 4; i++) {  // four dims a row each
+                    const uint32_t x = i < 2 ? u.x : u.y, y = i < 2 ? w.x : w.y;
+                    const int n = 2 * (i & 1);
+                    const uint32_t f[4] = {pair_of(x, n), pair_of(y, n), pair_of(x, n + 1), pair_of(y, n + 1)};
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
-                        mma16816<true>(sc[nt][j & 1], f, s.q[nt][i * 2 + j][0], s.q[nt][i * 2 + j][1]);
+                        mma16816<false>(sc[b][nt][r], f, s.q[nt][r * 4 + i][0], s.q[nt][r * 4 + i][1]);
                 }
-            } else {
+            }
+        } else {
+            constexpr int CK = S::VB / 4 < 16 ? S::VB / 4 : 16, NK = S::VB / 4 / CK, WK = CK / 4;
 #pragma unroll
-                for (int j = 0; j < WK; j++) {
-                    const uint32_t f[4] = {e4m3x2_to_f16x2(x[j] & 0xFFFFu), e4m3x2_to_f16x2(y[j] & 0xFFFFu),
-                                           e4m3x2_to_f16x2(x[j] >> 16), e4m3x2_to_f16x2(y[j] >> 16)};
+            for (int i = 0; i < NK; i++) {
+                uint32_t x[WK], y[WK];
+                const uint4 u = lds128a(kb + (i * 32 + lane) * CK), w = lds128a(kb + ((NK + i) * 32 + lane) * CK);
+                x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+                y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
+                if (BF) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-                        mma16816<false>(sc[nt][j & 1], f, s.q[nt][i * 4 + j][0], s.q[nt][i * 4 + j][1]);
+                    for (int j = 0; j < WK / 2; j++) {
+                        const uint32_t f[4] = {x[2 * j], y[2 * j], x[2 * j + 1], y[2 * j + 1]};
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+                            mma16816<true>(sc[b][nt][j & 1], f, s.q[nt][i * 2 + j][0], s.q[nt][i * 2 + j][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < WK; j++) {
+                        uint32_t f[4];
+                        e4m3x4_to_f16x4(x[j], f[0], f[2]);
+                        e4m3x4_to_f16x4(y[j], f[1], f[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++)
+                            mma16816<false>(sc[b][nt][j & 1], f, s.q[nt][i * 4 + j][0], s.q[nt][i * 4 + j][1]);
+                    }
                 }
             }
         }
     }
 
-    // scales of keys `key` (row g) and key + 8
-    float ks[2][GR], vs[2][GR];
+    // scales of keys `key` (row g) and key + 8 of each block
+    float ks[KS][2][GR], vs[KS][2][GR];
+    auto on = [&](int b, int r) {
+        const int k = 16 * b + 8 * r + key;
+        return k >= lo && k < hi && !((bad >> b) & 1);
+    };
     if (FMT != kKvBf16) {
 #pragma unroll
-        for (int r = 0; r < 2; r++) {
-            const int k = key + 8 * r;
-            if (FMT == kKvFp8) {
-                ks[r][0] = __uint_as_float(lds32(sb + 4 * k));
-                vs[r][0] = __uint_as_float(lds32(sb + S::SB + 4 * k));
-            } else if (GR == 1) {
-                ks[r][0] = __half2float(__ushort_as_half(lds_u16(sb + 2 * k)));
-                vs[r][0] = __half2float(__ushort_as_half(lds_u16(sb + S::SB + 2 * k)));
-            } else {
+        for (int b = 0; b < KS; b++)
 #pragma unroll
-                for (int p = 0; p < GR / 2; p++) {
-                    const uint32_t kw = lds32(sb + (k * GR + 2 * p) * 2), vw = lds32(sb + S::SB + (k * GR + 2 * p) * 2);
-                    const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw));
-                    const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vw));
-                    ks[r][2 * p] = kf.x, ks[r][2 * p + (GR > 1)] = kf.y;
-                    vs[r][2 * p] = vf.x, vs[r][2 * p + (GR > 1)] = vf.y;
+            for (int r = 0; r < 2; r++) {
+                const uint32_t at = buf + b * S::kBlock + SOFF + key * (S::SB / 16) + r * (S::SB / 2);
+                if (FMT == kKvFp8) {
+                    ks[b][r][0] = __uint_as_float(lds32(at));
+                    vs[b][r][0] = __uint_as_float(lds32(at + S::SB));
+                } else if (GR == 1) {
+                    ks[b][r][0] = __half2float(__ushort_as_half(lds_u16(at)));
+                    vs[b][r][0] = __half2float(__ushort_as_half(lds_u16(at + S::SB)));
+                } else {
+#pragma unroll
+                    for (int p = 0; p < GR / 2; p++) {
+                        const uint32_t kw = lds32(at + 4 * p), vw = lds32(at + S::SB + 4 * p);
+                        const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw));
+                        const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vw));
+                        ks[b][r][2 * p] = kf.x, ks[b][r][2 * p + (GR > 1)] = kf.y;
+                        vs[b][r][2 * p] = vf.x, vs[b][r][2 * p + (GR > 1)] = vf.y;
+                    }
                 }
             }
-        }
-    }
-    const bool on[2] = {full || (key >= lo && key < hi), full || (key + 8 >= lo && key + 8 < hi)};
-    if (FMT != kKvBf16) {
         if (!full) {
 #pragma unroll
-            for (int r = 0; r < 2; r++)
+            for (int b = 0; b < KS; b++)
 #pragma unroll
-                for (int c = 0; c < GR; c++)
-                    if (!on[r]) vs[r][c] = 0.0f;
+                for (int r = 0; r < 2; r++)
+#pragma unroll
+                    for (int c = 0; c < GR; c++)
+                        if (!on(b, r)) vs[b][r][c] = 0.0f;
         }
         // V scales in fp16 range: the largest times vn stays below 2^7
         float top = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 2; r++)
+        for (int b = 0; b < KS; b++)
 #pragma unroll
-            for (int c = 0; c < GR; c++) top = fmaxf(top, vs[r][c]);
-        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-        if (top > s.vlim) {
+            for (int r = 0; r < 2; r++)
+#pragma unroll
+                for (int c = 0; c < GR; c++) top = fmaxf(top, vs[b][r][c]);
+        if (__any_sync(0xFFFFFFFFu, top > s.vlim)) {
+            top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
             const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 7), 254);
             const float vn = __uint_as_float(static_cast<uint32_t>(260 - e) << 23), f = vn / s.vn;
             s.vn = vn;
@@ -461,131 +486,160 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
 #pragma unroll
                     for (int j = 0; j < 4; j++) s.o[nt][i][j] *= f;
         }
-#pragma unroll
-        for (int r = 0; r < 2; r++)
-#pragma unroll
-            for (int c = 0; c < GR; c++) vs[r][c] *= s.vn;
     }
 
-    // base-2 logits of keys (row g: 0, 1; row g + 8: 2, 3) and heads 2t, 2t + 1; weights; p^T fragments
-    float x[NT][4];
-    bool over = false;
+    // y: S with K's scales; x = y mul - m: base-2 logits of keys (row g: j = 0, 1; row g + 8: 2, 3) and heads
+    // 2t, 2t + 1, from the running maximum
+    float y[KS][NT][4], x[KS][NT][4];
+    float most = -INFINITY;
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++)
+    for (int b = 0; b < KS; b++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int r = j >> 1;
-            float y;
-            if (FMT == kKvBf16) {
-                y = (sc[nt][0][j] + sc[nt][CH > 1][j]) * s.mul[nt][j & 1];
-            } else if (FMT == kKvFp8) {
-                y = (sc[nt][0][j] + sc[nt][CH > 1][j]) * (ks[r][0] * s.mul[nt][j & 1]);
-            } else {
-                y = sc[nt][0][j] * ks[r][0];
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                for (int c = 1; c < GR; c++) y = fmaf(sc[nt][c][j], ks[r][c], y);
-                y *= s.mul[nt][j & 1];
+            for (int j = 0; j < 4; j++) {
+                const int r = j >> 1;
+                float v;
+                if (FMT == kKvNf4) {
+                    v = sc[b][nt][0][j] * ks[b][r][0];
+#pragma unroll
+                    for (int c = 1; c < GR; c++) v = fmaf(sc[b][nt][c][j], ks[b][r][c], v);
+                } else {
+                    v = sc[b][nt][0][j] + sc[b][nt][CH > 1][j];
+                    if (FMT == kKvFp8) v *= ks[b][r][0];
+                }
+                y[b][nt][j] = v;
+                x[b][nt][j] = fmaf(v, s.mul[nt][j & 1], -s.m[nt][j & 1]);
             }
-            x[nt][j] = on[r] ? y : -INFINITY;
-            over |= x[nt][j] > s.m[nt][j & 1] + kLazy;
-        }
-    if (__any_sync(0xFFFFFFFFu, over)) {
+    if (!full) {
+#pragma unroll
+        for (int b = 0; b < KS; b++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (!on(b, j >> 1)) x[b][nt][j] = -INFINITY;
+    }
+#pragma unroll
+    for (int b = 0; b < KS; b++)
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) most = fmaxf(most, x[b][nt][j]);
+    if (__any_sync(0xFFFFFFFFu, most > kLazy)) {
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int j = 0; j < 2; j++) {
-                float top = fmaxf(x[nt][j], x[nt][j + 2]);
+                float top = s.m[nt][j];
+#pragma unroll
+                for (int b = 0; b < KS; b++)
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        float& z = x[b][nt][j + 2 * r];
+                        z = z == -INFINITY ? z : y[b][nt][j + 2 * r] * s.mul[nt][j];
+                        top = fmaxf(top, z);
+                    }
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                top = fmaxf(top, s.m[nt][j]);
                 const float f = exp2_approx(s.m[nt][j] - top);
                 s.m[nt][j] = top;
                 s.l[nt][j] *= f;
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) s.o[nt][i][j] *= f, s.o[nt][i][j + 2] *= f;
+#pragma unroll
+                for (int b = 0; b < KS; b++) x[b][nt][j] -= top, x[b][nt][j + 2] -= top;
             }
     }
+    // weights, and p^T fragments
     constexpr int PB = FMT == kKvBf16 ? 2 : GR;  // bf16: p's high and low part; else one for each scale group
-    uint32_t pb[NT][PB][2];
+    uint32_t pb[KS][NT][PB][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++) {
-        float p[4];
+    for (int b = 0; b < KS; b++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) p[j] = exp2_approx(x[nt][j] - s.m[nt][j & 1]);
-        s.l[nt][0] += p[0] + p[2];
-        s.l[nt][1] += p[1] + p[3];
-        if (FMT == kKvBf16) {
+        for (int nt = 0; nt < NT; nt++) {
+            float p[4];
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const uint32_t hi = f32x2_to_bf16x2(p[2 * r], p[2 * r + 1]);
-                const float2 f = bf16x2_to_f32x2(hi);
-                pb[nt][0][r] = transpose8x8(hi);
-                pb[nt][PB - 1][r] = transpose8x8(f32x2_to_bf16x2(p[2 * r] - f.x, p[2 * r + 1] - f.y));
-            }
-        } else {
+            for (int j = 0; j < 4; j++) p[j] = exp2_approx(x[b][nt][j]);
+            s.l[nt][0] += p[0] + p[2];
+            s.l[nt][1] += p[1] + p[3];
+            if (FMT == kKvBf16) {
 #pragma unroll
-            for (int c = 0; c < GR; c++) {
-                pb[nt][c][0] = transpose8x8(pack_f16(p[0] * vs[0][c], p[1] * vs[0][c]));
-                pb[nt][c][1] = transpose8x8(pack_f16(p[2] * vs[1][c], p[3] * vs[1][c]));
-            }
-        }
-    }
-
-    // O^T += V^T p^T: fragment column pairs are keys of rows (2t, 2t + 1) and (2t + 8, 2t + 9)
-    if (FMT == kKvNf4) {
-        const int ka = key_of_row(2 * t), kc = key_of_row(2 * t + 1);
+                for (int r = 0; r < 2; r++) {
+                    const uint32_t hi16 = f32x2_to_bf16x2(p[2 * r], p[2 * r + 1]);
+                    const float2 f = bf16x2_to_f32x2(hi16);
+                    pb[b][nt][0][r] = transpose8x8(hi16);
+                    pb[b][nt][PB - 1][r] = transpose8x8(f32x2_to_bf16x2(p[2 * r] - f.x, p[2 * r + 1] - f.y));
+                }
+            } else {
 #pragma unroll
-        for (int r = 0; r < GR; r++) {
-            const uint32_t wa = lds32(vb + nf4_piece<D>(ka, r) + g * 4), wb = lds32(vb + nf4_piece<D>(kc, r) + g * 4);
-            const uint32_t wc = lds32(vb + nf4_piece<D>(ka + 8, r) + g * 4),
-                           wd = lds32(vb + nf4_piece<D>(kc + 8, r) + g * 4);
-            // code bytes (first key low, second key high) of the even and of the odd dims
-            const uint32_t lo4 = 0x0F0F0F0Fu;
-            const uint32_t e0 = (wa & lo4) | ((wb << 4) & ~lo4), o0 = ((wa >> 4) & lo4) | (wb & ~lo4);
-            const uint32_t e1 = (wc & lo4) | ((wd << 4) & ~lo4), o1 = ((wc >> 4) & lo4) | (wd & ~lo4);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t f[4] = {pair_of(e0, i), pair_of(o0, i), pair_of(e1, i), pair_of(o1, i)};
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++) mma16816<false>(s.o[nt][r * 4 + i], f, pb[nt][r][0], pb[nt][r][1]);
-            }
-        }
-    } else {
-        constexpr int CV = S::VB / 8 < 16 ? S::VB / 8 : 16, NV = S::VB / 8 / CV, WV = CV / 4;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            uint32_t w[4][4];
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const uint32_t at = vb + ((r * NV + i) * 32 + lane) * CV;
-                if (CV == 16) {
-                    const uint4 u = lds128a(at);
-                    w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
-                } else {
-                    const uint2 u = lds64(at);
-                    w[r][0] = u.x, w[r][1] = u.y;
+                for (int c = 0; c < GR; c++) {
+                    const float v0 = vs[b][0][c] * s.vn, v1 = vs[b][1][c] * s.vn;
+                    pb[b][nt][c][0] = transpose8x8(pack_f16(p[0] * v0, p[1] * v0));
+                    pb[b][nt][c][1] = transpose8x8(pack_f16(p[2] * v1, p[3] * v1));
                 }
             }
+        }
+
+    // O^T += V^T p^T: fragment column pairs are keys of rows (2t, 2t + 1) and (2t + 8, 2t + 9)
 #pragma unroll
-            for (int j = 0; j < WV; j++) {
-                if (BF) {
-                    const uint32_t f[4] = {prmt(w[0][j], w[1][j], 0x5410), prmt(w[0][j], w[1][j], 0x7632),
-                                           prmt(w[2][j], w[3][j], 0x5410), prmt(w[2][j], w[3][j], 0x7632)};
+    for (int b = 0; b < KS; b++) {
+        const uint32_t vb = buf + b * S::kBlock + VOFF;
+        if (FMT == kKvNf4) {
+            const int ka = key_of_row(2 * t), kc = key_of_row(2 * t + 1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++) {
-                        mma16816<true>(s.o[nt][i * WV + j], f, pb[nt][0][0], pb[nt][0][1]);
-                        mma16816<true>(s.o[nt][i * WV + j], f, pb[nt][PB - 1][0], pb[nt][PB - 1][1]);
+            for (int r = 0; r < GR; r++) {
+                const uint32_t at_a = vb + nf4_piece<D>(ka, r) + g * 4, at_c = vb + nf4_piece<D>(kc, r) + g * 4;
+                const uint32_t wa = lds32(at_a), wb = lds32(at_c);
+                const uint32_t wc = lds32(at_a + 8 * S::VB), wd = lds32(at_c + 8 * S::VB);
+                // code bytes (first key low, second key high) of the even and of the odd dims
+                const uint32_t lo4 = 0x0F0F0F0Fu;
+                const uint32_t e0 = (wa & lo4) | ((wb << 4) & ~lo4), o0 = ((wa >> 4) & lo4) | (wb & ~lo4);
+                const uint32_t e1 = (wc & lo4) | ((wd << 4) & ~lo4), o1 = ((wc >> 4) & lo4) | (wd & ~lo4);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t f[4] = {pair_of(e0, i), pair_of(o0, i), pair_of(e1, i), pair_of(o1, i)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+                        mma16816<false>(s.o[nt][r * 4 + i], f, pb[b][nt][r][0], pb[b][nt][r][1]);
+                }
+            }
+        } else {
+            constexpr int CV = S::VB / 8 < 16 ? S::VB / 8 : 16, NV = S::VB / 8 / CV, WV = CV / 4;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                uint32_t w[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const uint32_t at = vb + ((r * NV + i) * 32 + lane) * CV;
+                    if (CV == 16) {
+                        const uint4 u = lds128a(at);
+                        w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
+                    } else {
+                        const uint2 u = lds64(at);
+                        w[r][0] = u.x, w[r][1] = u.y;
                     }
-                } else {
+                }
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {  // dims 0, 1 and 2, 3 of the word
-                        const uint32_t u = prmt(w[0][j], w[1][j], h ? 0x7362 : 0x5140);
-                        const uint32_t z = prmt(w[2][j], w[3][j], h ? 0x7362 : 0x5140);
-                        const uint32_t f[4] = {e4m3x2_to_f16x2(u & 0xFFFFu), e4m3x2_to_f16x2(u >> 16),
-                                               e4m3x2_to_f16x2(z & 0xFFFFu), e4m3x2_to_f16x2(z >> 16)};
+                for (int j = 0; j < WV; j++) {
+                    if (BF) {
+                        const uint32_t f[4] = {prmt(w[0][j], w[1][j], 0x5410), prmt(w[0][j], w[1][j], 0x7632),
+                                               prmt(w[2][j], w[3][j], 0x5410), prmt(w[2][j], w[3][j], 0x7632)};
 #pragma unroll
-                        for (int nt = 0; nt < NT; nt++)
-                            mma16816<false>(s.o[nt][(i * WV + j) * 2 + h], f, pb[nt][0][0], pb[nt][0][1]);
+                        for (int nt = 0; nt < NT; nt++) {
+                            mma16816<true>(s.o[nt][i * WV + j], f, pb[b][nt][0][0], pb[b][nt][0][1]);
+                            mma16816<true>(s.o[nt][i * WV + j], f, pb[b][nt][PB - 1][0], pb[b][nt][PB - 1][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {  // dims 0, 1 and 2, 3 of the word
+                            uint32_t f[4];
+                            e4m3x4_to_f16x4(prmt(w[0][j], w[1][j], h ? 0x7362 : 0x5140), f[0], f[1]);
+                            e4m3x4_to_f16x4(prmt(w[2][j], w[3][j], h ? 0x7362 : 0x5140), f[2], f[3]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++)
+                                mma16816<false>(s.o[nt][(i * WV + j) * 2 + h], f, pb[b][nt][0][0], pb[b][nt][0][1]);
+                        }
                     }
                 }
             }
@@ -598,8 +652,10 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
 // ---------------------------------------------------------------------------------------------
 struct Span {
     int start, end;  // keys [start, end) of a sequence
-    __device__ int first_unit() const { return start >> 4; }
-    __device__ int units() const { return end > start ? ((end + 15) >> 4) - (start >> 4) : 0; }
+    template <int KEYS>
+    __device__ int units() const {  // of KEYS keys each, aligned
+        return end > start ? (end + KEYS - 1) / KEYS - start / KEYS : 0;
+    }
 };
 
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
@@ -662,10 +718,11 @@ struct Place {
 
 // The sequence whose pieces include number `id`, searched from `at` on (b = B: none).  Every segment of
 // a sequence of n units has ceil(n / cut) pieces.  The whole warp calls it.
+template <int KEYS>
 __device__ __forceinline__ Place locate(const AttnArgs& a, Place at, uint32_t id, int cut, int segs, int lane) {
     while (at.b < a.B) {
         const int b = at.b + lane;
-        const int n = b < a.B ? span_of(a, b).units() : 0;
+        const int n = b < a.B ? span_of(a, b).units<KEYS>() : 0;
         const uint32_t p = static_cast<uint32_t>((n + cut - 1) / cut) * segs;
         uint32_t sum = p;
         int64_t units = static_cast<int64_t>(n) * segs;
@@ -695,7 +752,7 @@ __device__ __forceinline__ Place locate(const AttnArgs& a, Place at, uint32_t id
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel(const AttnArgs a) {
     using S = Shape<FMT, D, NT>;
-    constexpr int WG = S::WG, NST = S::NST, THREADS = WG * 32;
+    constexpr int WG = S::WG, NST = S::NST, THREADS = WG * 32, KS = S::KS, KEYS = 16 * KS;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t s_word[S::NG][2];            // a worker's next piece; whether it joins
     __shared__ float s_ml[S::NG][WG * 2 * NT * 8];   // the maxima and sums of its warps
@@ -722,7 +779,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     const int segs = a.c.kv_heads * a.chunks;  // segments of a sequence
     const uint32_t worker = blockIdx.x * S::NG + group, workers = gridDim.x * S::NG;
     int64_t total = 0;
-    for (int b = lane; b < a.B; b += 32) total += span_of(a, b).units();
+    for (int b = lane; b < a.B; b += 32) total += span_of(a, b).units<KEYS>();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     total *= segs;
@@ -739,17 +796,17 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     auto area = [&](int w) {  // of warp w of this worker, once its ring is drained
         return reinterpret_cast<float*>(smem + (area_of<FMT>(base, group * WG + w, S::kArea) - base));
     };
-    const int units_per_page = a.c.page_size >> 4;
+    const int blocks_per_page = a.c.page_size >> 4;
     WarpState<FMT, D, NT> s;
     Place at{0, 0, 0};
     for (uint32_t id = worker;;) {
-        at = locate(a, at, id, cut, segs, lane);
+        at = locate<KEYS>(a, at, id, cut, segs, lane);
         if (at.b == a.B) break;
         uint32_t next = 0;
         if (tid == 0) next = atomicAdd(a.tickets, 1u) + workers;  // arrives while the piece is worked on
         // piece `part` of `parts` of segment `seg`: units [u0, u1) of its n
         const Span span = span_of(a, at.b);
-        const int n = span.units();
+        const int n = span.units<KEYS>();
         const uint32_t parts = static_cast<uint32_t>((n + cut - 1) / cut);
         const uint32_t in_seq = id - at.pieces_before;
         const int seg = static_cast<int>(in_seq / parts);
@@ -760,24 +817,27 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         const int heads = min(a.chunk_heads, a.group - head0);
         const int64_t row0 = static_cast<int64_t>(at.b) * a.q_heads + static_cast<int64_t>(kv) * a.group + head0;
 
-        // this warp's units: u0 + warp + WG j, j < mine; lane j holds where unit 32 * batch + j lies
+        // this warp's units: u0 + warp + WG j, j < mine; lane i holds where block 32 * batch + i of them lies
         const int mine = u1 - u0 > warp ? (u1 - u0 - warp + WG - 1) / WG : 0;
-        const int first = span.first_unit() + u0 + warp;
-        auto place_of = [&](int j) -> int64_t {
-            if (j >= mine) return -1;
-            const uint32_t unit = first + j * WG;
-            const uint32_t p = units_per_page == 1 ? unit : static_cast<uint32_t>(__umul64hi(unit, a.page_magic));
+        const int first = span.start / KEYS + u0 + warp;
+        auto place_of = [&](int i) -> int64_t {
+            const uint32_t block = (first + i / KS * WG) * KS + i % KS;
+            // past the warp's units, or nothing live in it: its page is not looked up
+            if (i >= mine * KS || block * 16 >= static_cast<uint32_t>(span.end) ||
+                block * 16 + 16 <= static_cast<uint32_t>(span.start))
+                return -2;
+            const uint32_t p = blocks_per_page == 1 ? block : static_cast<uint32_t>(__umul64hi(block, a.page_magic));
             const int64_t page = a.page_table[at.b * a.max_pages + p];
             if (page < 0 || page >= a.c.pages) {
                 atomicCAS(&g_attention_error, 0, 43);
                 return -1;
             }
-            return (page * a.c.kv_heads + kv) * a.c.page_size + (unit - p * units_per_page) * 16;
+            return (page * a.c.kv_heads + kv) * a.c.page_size + (block - p * blocks_per_page) * 16;
         };
-        int64_t places = place_of(lane), next_places = mine > 32 ? place_of(32 + lane) : -1;
+        int64_t places = place_of(lane), next_places = mine * KS > 32 ? place_of(32 + lane) : -2;
         load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);
 
-        uint32_t bad = 0;  // bit i: the unit issued i units ago has no page
+        uint32_t bad = 0;  // bits of the blocks issued last (the newest lowest): no page
         uint32_t in_buf = ring, out_buf = ring;
         for (int j = 1 - NST; j < mine; j++) {
             if (j >= 0) {
@@ -785,24 +845,27 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 __syncwarp();  // the stage is complete for every lane, and the one before it is free
             }
             const int ahead = j + NST - 1;
-            bad <<= 1;
+            bad <<= KS;
             if (ahead < mine) {
-                if (ahead > 0 && (ahead & 31) == 0) {
+                if (ahead > 0 && (ahead * KS & 31) == 0) {
                     places = next_places;
-                    next_places = place_of(ahead + 32 + lane);
+                    next_places = place_of(ahead * KS + 32 + lane);
                 }
-                const int64_t place = __shfl_sync(0xFFFFFFFFu, places, ahead & 31);
-                bad |= place < 0 ? 1u : 0u;
-                const int key0 = (first + ahead * WG) * 16;
-                issue_unit<FMT, D, NT>(a.c, in_buf, place, span.start - key0, span.end - key0, lane);
+                const int key0 = (first + ahead * WG) * KEYS;
+#pragma unroll
+                for (int b = 0; b < KS; b++) {
+                    const int64_t place = __shfl_sync(0xFFFFFFFFu, places, (ahead * KS + b) & 31);
+                    bad |= place == -1 ? 1u << b : 0u;
+                    issue_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, place, span.start - key0 - 16 * b,
+                                            span.end - key0 - 16 * b, lane);
+                }
                 in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (j >= 0) {
-                const int key0 = (first + j * WG) * 16;
-                int lo = span.start - key0, hi = span.end - key0;
-                if ((bad >> (NST - 1)) & 1) lo = hi = 0;
-                attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= 16, lo, hi, lane);
+                const int key0 = (first + j * WG) * KEYS, lo = span.start - key0, hi = span.end - key0;
+                const uint32_t gone = (bad >> (KS * (NST - 1))) & ((1u << KS) - 1);
+                attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= KEYS && gone == 0, lo, hi, gone, lane);
                 out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
             }
         }
@@ -890,7 +953,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     // sequences with nothing to attend to, and lengths past their tables
     for (int b = blockIdx.x * S::W + threadIdx.x / 32; b < a.B; b += gridDim.x * S::W) {
         if (lane == 0 && a.lengths[b] > a.max_pages * a.c.page_size) atomicCAS(&g_attention_error, 0, 43);
-        if (span_of(a, b).units() == 0)
+        if (span_of(a, b).units<KEYS>() == 0)
             for (int i = lane; i < a.q_heads * (D / 8); i += 32)
                 reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * (D / 8)) + i] = make_uint4(0, 0, 0, 0);
     }
@@ -913,7 +976,7 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
     });
     if (attr_err != cudaSuccess) return attr_err;
     // as many CTAs as SMs, or fewer where the longest possible sequences leave less than that to do
-    const int64_t most = a.B * static_cast<int64_t>(a.c.kv_heads) * a.chunks * ((a.max_pages * a.c.page_size + 15) / 16);
+    const int64_t most = a.B * static_cast<int64_t>(a.c.kv_heads) * a.chunks * ((a.max_pages * a.c.page_size + 16 * S::KS - 1) / (16 * S::KS));
     int64_t grid = num_sms < kMaxWorkers / S::NG ? num_sms : kMaxWorkers / S::NG;
     if (grid > (most + S::W - 1) / S::W) grid = (most + S::W - 1) / S::W;
     if (grid < 1) grid = 1;
