@@ -194,16 +194,30 @@ __device__ __forceinline__ uint32_t area_of(uint32_t base, int w, uint32_t bytes
     return w < below ? base + w * bytes : kTableEnd + (w - below) * bytes;
 }
 
-// Key of fragment row r (0..7; row r + 8 holds the key 8 later).  Chosen so that rows r = 0..3 and 4..7,
-// and rows 2t and 2t + 1 over t, are distinct modulo 4: the bank groups of the NF4 reads then differ.
+// Key of fragment row r (0..7; row r + 8 holds the key 8 later).  Rows r = 0..3 and 4..7, and rows 2t (or
+// 2t + 1) over t, are distinct modulo 4, and rows 2i and 2i + 1 differ in bit 2: the bank groups below.
 __device__ __forceinline__ int key_of_row(int r) { return (r & 1) ? 4 + (((r >> 1) + 2) & 3) : r >> 1; }
 
-// NF4 vectors in a stage: the 32-byte piece that holds group r of key row `k`.
-template <int D>
-__device__ __forceinline__ uint32_t nf4_piece(int k, int r) {
-    if (D == 64) return k * 32;
-    if (D == 128) return k * 64 + ((r ^ ((k >> 1) & 1)) * 32);
-    return k * 128 + ((r ^ (k & 3)) * 32);
+// Offset of 16-byte piece p of key row `row` inside a block's K or V.  The global side reads a block in order,
+// 512 contiguous bytes a warp instruction (segments of 64 or 128 bytes of several rows reach 5.4 TB/s in a
+// bare copy ring of this shape, whole lines in order 7.2); the pieces are permuted so that the fragment
+// reads do not conflict:
+//   16 bytes a lane, K: rows 2i, 2i + 1 by four pieces, told apart by bit 2 of the row
+//   16 bytes a lane, V: rows of four t by two pieces, told apart by the row modulo 4
+//   NF4 (8 bytes of a group, K; 4, V): four rows of 32 bytes, told apart by the row modulo 4
+template <int FMT, int D, bool IS_V>
+__device__ __forceinline__ uint32_t piece_at(int row, int p) {
+    constexpr int VB = kv_vector_bytes(FMT, D);
+    if (FMT == kKvNf4) {
+        if (D == 64) return row * 32 + p * 16;
+        if (D == 128) return row * 64 + (p ^ (((row >> 1) & 1) << 1)) * 16;
+        return row * 128 + (p ^ ((row & 3) << 1)) * 16;
+    }
+    if (VB == 64) {  // two rows a 128-byte line
+        if (IS_V) return row * 64 + (p ^ (((row >> 1) & 1) << 1)) * 16;
+        return ((row * 4 + p) ^ (((row >> 2) & 1) << 2)) * 16;
+    }
+    return row * VB + (IS_V ? p ^ ((row & 3) << 1) : p ^ (((row >> 2) & 1) << 2)) * 16;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -215,38 +229,15 @@ template <int FMT, int D, int NT, bool ALL>
 __device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
     using S = Shape<FMT, D, NT>;
     const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
-    const int g = lane >> 2, t = lane & 3;
     const uint8_t* k = c.k + place * S::VB;
     const uint8_t* v = c.v + place * S::VB;
     auto live = [&](int key) { return ALL || (key >= lo && key < hi); };
-    if (FMT == kKvNf4) {
-        constexpr int P = S::VB / 16;  // 16-byte pieces of a vector
+    constexpr int P = S::VB / 16;  // 16-byte pieces of a vector
 #pragma unroll
-        for (int j = 0; j < P / 2; j++) {
-            const int piece = j * 32 + lane, key = piece / P, p = piece % P;
-            const uint32_t at = nf4_piece<D>(key, p / 2) + (p & 1) * 16;
-            const bool on = live(key);
-            cp_async<16>(kb + at, k + piece * 16, on);
-            cp_async<16>(vb + at, v + piece * 16, on);
-        }
-    } else {
-        // each lane copies what it will read itself, in the order in which it will read it
-        constexpr int CK = S::VB / 4 < 16 ? S::VB / 4 : 16, NK = S::VB / 4 / CK;
-        const int key = key_of_row(g);
-#pragma unroll
-        for (int r = 0; r < 2; r++)
-#pragma unroll
-            for (int i = 0; i < NK; i++)
-                cp_async<CK>(kb + ((r * NK + i) * 32 + lane) * CK, k + (key + 8 * r) * S::VB + (i * 4 + t) * CK,
-                             live(key + 8 * r));
-        constexpr int CV = S::VB / 8 < 16 ? S::VB / 8 : 16, NV = S::VB / 8 / CV;
-#pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int kr = key_of_row(2 * t + (r & 1)) + 8 * (r >> 1);
-#pragma unroll
-            for (int i = 0; i < NV; i++)
-                cp_async<CV>(vb + ((r * NV + i) * 32 + lane) * CV, v + kr * S::VB + (i * 8 + g) * CV, live(kr));
-        }
+    for (int j = 0; j < P / 2; j++) {
+        const int n = j * 32 + lane, key = n / P, p = n % P;
+        cp_async<16>(kb + piece_at<FMT, D, false>(key, p), k + n * 16, live(key));
+        cp_async<16>(vb + piece_at<FMT, D, true>(key, p), v + n * 16, live(key));
     }
     if (S::SB) {
         constexpr int SK = S::SB ? S::SB / 16 : 1;  // scale bytes of a key
@@ -384,7 +375,7 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
         if (FMT == kKvNf4) {
 #pragma unroll
             for (int r = 0; r < GR; r++) {
-                const uint32_t at = kb + nf4_piece<D>(key, r) + t * 8;
+                const uint32_t at = kb + piece_at<FMT, D, false>(key, 2 * r) + t * 8;
                 const uint2 u = lds64(at), w = lds64(at + 8 * S::VB);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {  // four dims a row each
@@ -401,7 +392,8 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
 #pragma unroll
             for (int i = 0; i < NK; i++) {
                 uint32_t x[WK], y[WK];
-                const uint4 u = lds128a(kb + (i * 32 + lane) * CK), w = lds128a(kb + ((NK + i) * 32 + lane) * CK);
+                const uint32_t at = kb + piece_at<FMT, D, false>(key, i * 4 + t);
+                const uint4 u = lds128a(at), w = lds128a(at + 8 * S::VB);
                 x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
                 y[0] = w.x, y[1] = w.y, y[2] = w.z, y[3] = w.w;
                 if (BF) {
@@ -589,7 +581,8 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
             const int ka = key_of_row(2 * t), kc = key_of_row(2 * t + 1);
 #pragma unroll
             for (int r = 0; r < GR; r++) {
-                const uint32_t at_a = vb + nf4_piece<D>(ka, r) + g * 4, at_c = vb + nf4_piece<D>(kc, r) + g * 4;
+                const uint32_t at_a = vb + piece_at<FMT, D, true>(ka, 2 * r) + g * 4;
+                const uint32_t at_c = vb + piece_at<FMT, D, true>(kc, 2 * r) + g * 4;
                 const uint32_t wa = lds32(at_a), wb = lds32(at_c);
                 const uint32_t wc = lds32(at_a + 8 * S::VB), wd = lds32(at_c + 8 * S::VB);
                 // code bytes (first key low, second key high) of the even and of the odd dims
@@ -611,7 +604,10 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
                 uint32_t w[4][4];
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    const uint32_t at = vb + ((r * NV + i) * 32 + lane) * CV;
+                    const int row = key_of_row(2 * t + (r & 1));
+                    const uint32_t at = vb + (r >> 1) * 8 * S::VB +
+                                        (CV == 16 ? piece_at<FMT, D, true>(row, i * 8 + g)
+                                                  : piece_at<FMT, D, true>(row, g / 2) + (g & 1) * 8);
                     if (CV == 16) {
                         const uint4 u = lds128a(at);
                         w[r][0] = u.x, w[r][1] = u.y, w[r][2] = u.z, w[r][3] = u.w;
