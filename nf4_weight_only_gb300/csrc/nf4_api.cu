@@ -335,6 +335,7 @@ nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, co
     if (B < 0 || B > 65535 || q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads != 0) return NF4_ERR_SHAPE;
     if (B * q_heads > (int64_t{1} << 30)) return NF4_ERR_SHAPE;
     if (max_pages < 0 || max_pages > kMaxDim || max_pages * cache->page_size > kMaxDim || window < 0) return NF4_ERR_SHAPE;
+    if (max_pages > 0 && B > (int64_t{1} << 35) / (max_pages * cache->page_size)) return NF4_ERR_SHAPE;
     if (B == 0) return NF4_OK;
     if (!q || !lengths || !out || !workspace || (max_pages > 0 && !page_table)) return NF4_ERR_NULL;
     if (!aligned16(q) || !aligned16(lengths) || !aligned16(out) || !aligned16(workspace) || !aligned16(page_table))

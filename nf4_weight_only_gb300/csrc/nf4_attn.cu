@@ -36,12 +36,11 @@ namespace {
 // Error word of the attention (43: a page or a length outside its bounds).
 __device__ int g_attention_error;
 
-constexpr int kMaxWorkers = 320;
-constexpr int kPiecesPerWorker = 4;   // where the work allows it: evens out the SMs' different speeds
-constexpr int kLongUnits = 16;        // units a warp in the smallest piece worth a ticket of its own
+constexpr int kMaxWorkers = 320;      // of W / 2 warps
+constexpr int kPiecesPerWorker = 4;   // in long calls (see make_plan)
+constexpr int kLongUnits = 16;        // units a warp up to which a call is one piece a worker
 constexpr int kFanIn = 16;            // partial results joined at a time
-constexpr int kMostBatches = (kMaxWorkers * kPiecesPerWorker + kFanIn) / kFanIn + 1;
-constexpr int kSlots = 2 * kMaxWorkers * kPiecesPerWorker + 2;  // partial results (see slot0 in the kernel)
+constexpr int kSlots = 2 * kMaxWorkers * kPiecesPerWorker + 2;  // partial results (see slot0)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;         // p may reach 2^8 before the running maximum moves
 
@@ -169,7 +168,6 @@ struct Shape {
     // Warps and stages: enough warps to issue the decoding (16 for the quantised formats where their
     // registers allow it), and about 100 KB in flight an SM.
     static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : (NT == 2 || D == 256) ? 8 : FMT == kKvFp8 ? 12 : 16;
-    static constexpr int NG = 2, WG = W / NG;                    // workers a CTA, warps a worker
     static constexpr int kRingMost = FMT == kKvNf4 ? (W == 16 ? 10240 : 20480) : 230400 / W / 16 * 16;
     static constexpr int kStagesFit = kRingMost / kStage;
     static constexpr int NST = kStagesFit > 10 ? 10 : kStagesFit;
@@ -177,7 +175,7 @@ struct Shape {
     static constexpr int kResult = NT * 8 * (D + 2) * 4;         // bytes of a warp's result
     static constexpr int kSmem = 225 * 1024;                     // dynamic; with 2 KB of static, all there is
     static constexpr int kArea = kRing > kResult ? kRing : kResult;
-    static_assert(kArea >= kMostBatches * 2 * NT * 8 * 4, "an area holds the maxima and sums of the last join");
+    static_assert(kArea >= (kSlots / 2 / kFanIn + 2) * 2 * NT * 8 * 4, "an area holds the maxima and sums of a join");
     // dynamic shared memory starts 2 to 4 KB into the window
     static constexpr int kBelow = FMT == kKvNf4 ? static_cast<int>(kTableAt - 4096) / kArea : W;
     static_assert(NST >= 2, "a ring has at least two stages");
@@ -664,26 +662,44 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
     return s;
 }
 
-// Four dims of one head, joined over `n` results in their order: part(j) is result j, [heads][D] sums of
-// weighted values, [heads] maxima, [heads] sums of weights.  ml: the maxima and sums of all results,
-// [n][2 heads], in shared memory.
+// Four dims (column i) of one head, joined over `n` results in their order: part(j) is result j, [heads][D]
+// sums of weighted values, then [heads] maxima and [heads] sums of weights at ml(j).  Eight results are
+// loaded at a time, so the latency of the memory that holds them is met once for each eight.
 struct Joined {
     float4 o;
     float top, l;
 };
-template <int D, bool GLOBAL, typename Part>
-__device__ __forceinline__ Joined join(const Part& part, const float* ml, int n, int heads, int i) {
+template <int D, bool GLOBAL, bool ML_SHARED = !GLOBAL, typename Part, typename Ml>
+__device__ __forceinline__ Joined join(const Part& part, const Ml& ml, int n, int heads, int i) {
+    constexpr int N = GLOBAL ? 8 : 4;
     const int h = i / (D / 4);
     Joined r{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -3e38f, 0.0f};
-    for (int j = 0; j < n; j++) r.top = fmaxf(r.top, ml[j * 2 * heads + h]);
-#pragma unroll 8
-    for (int j = 0; j < n; j++) {
-        const float4* p = reinterpret_cast<const float4*>(part(j)) + i;
-        const float4 v = GLOBAL ? __ldcg(p) : *p;
-        const float f = exp2_approx(ml[j * 2 * heads + h] - r.top);
-        r.l = fmaf(f, ml[j * 2 * heads + heads + h], r.l);
-        r.o.x = fmaf(f, v.x, r.o.x), r.o.y = fmaf(f, v.y, r.o.y);
-        r.o.z = fmaf(f, v.z, r.o.z), r.o.w = fmaf(f, v.w, r.o.w);
+    for (int j0 = 0; j0 < n; j0 += N) {
+        float4 v[N];
+        float m[N], l[N], top = r.top;
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), m[j] = -3e38f, l[j] = 0.0f;
+            if (j0 + j < n) {
+                const float4* p = reinterpret_cast<const float4*>(part(j0 + j)) + i;
+                const float* q = ml(j0 + j) + h;
+                v[j] = GLOBAL ? __ldcg(p) : *p;
+                m[j] = ML_SHARED ? *q : __ldcg(q);
+                l[j] = ML_SHARED ? q[heads] : __ldcg(q + heads);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; j++) top = fmaxf(top, m[j]);
+        const float f0 = exp2_approx(r.top - top);
+        r.top = top;
+        r.l *= f0, r.o.x *= f0, r.o.y *= f0, r.o.z *= f0, r.o.w *= f0;
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const float f = exp2_approx(m[j] - top);
+            r.l = fmaf(f, l[j], r.l);
+            r.o.x = fmaf(f, v[j].x, r.o.x), r.o.y = fmaf(f, v[j].y, r.o.y);
+            r.o.z = fmaf(f, v[j].z, r.o.z), r.o.w = fmaf(f, v[j].w, r.o.w);
+        }
     }
     return r;
 }
@@ -700,40 +716,118 @@ __device__ __forceinline__ void store_partial(float* slot, const Joined& r, int 
     }
 }
 
-template <int THREADS>
-__device__ __forceinline__ void worker_barrier(int group) {
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(THREADS) : "memory");
+// Barrier of a worker's warps (barrier 0 is the CTA's).
+__device__ __forceinline__ void worker_barrier(int group, int warps) {
+    if (warps == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
 }
 
-// A sequence among the others: its span, and what precedes it.
-struct Place {
-    int b;
-    int64_t units_before;  // units of the sequences before it, all segments
-    uint32_t pieces_before;
+// How the segments are cut: into pieces of at most `cut` units, as equal as they come.
+struct Plan {
+    uint32_t warps, workers;  // warps of a worker; workers of the grid
+    uint32_t cut;
+    uint32_t pieces;          // of all segments
 };
 
-// The sequence whose pieces include number `id`, searched from `at` on (b = B: none).  Every segment of
-// a sequence of n units has ceil(n / cut) pieces.  The whole warp calls it.
-template <int KEYS>
-__device__ __forceinline__ Place locate(const AttnArgs& a, Place at, uint32_t id, int cut, int segs, int lane) {
-    while (at.b < a.B) {
+__device__ __forceinline__ uint32_t divide_up(uint64_t a, uint32_t d) {  // at most 2^30
+    if (a < (uint64_t{1} << 31)) return (static_cast<uint32_t>(a) + d - 1) / d;
+    const uint64_t q = (a + d - 1) / d;
+    return static_cast<uint32_t>(q < (1u << 30) ? q : (1u << 30));
+}
+
+// units(b): of sequence b.  The whole warp calls it.
+template <typename Units>
+__device__ __forceinline__ uint32_t count_pieces(const Units& units, int B, uint32_t segs, uint32_t cut, int lane) {
+    uint32_t p = 0;
+    for (int b = lane; b < B; b += 32) p += (units(b) + cut - 1) / cut;
+    return __reduce_add_sync(0xFFFFFFFFu, p) * segs;
+}
+
+// A rule on the lengths alone, the same in every CTA (one warp works it out).  W warps a CTA; a worker is
+// W / 2 of them, so that a CTA has one that streams while the other starts or joins a piece, except
+//  - all W, when there is at most a segment for each CTA and little to do: no second piece to overlap with;
+//  - fewer, when there are many segments too short to keep W / 2 warps busy.
+// Sequences of up to 8 units a warp are not cut: the join of partial results costs 3 us, about what these
+// units do.  Otherwise a call of up to 16 units a warp is one piece a worker, a longer one four, which
+// evens out the SMs' different speeds.  Rounding up the pieces of each segment must not start another round:
+// `cut` grows until the pieces fit (bisection), unless the segments alone fill the rounds.
+template <int W, typename Units>
+__device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t segs, int lane) {
+    uint32_t sum = 0, live = 0, longest = 0;
+    for (int b = lane; b < B; b += 32) {
+        const uint32_t n = units(b);
+        sum += n;
+        live += n > 0;
+        longest = max(longest, n);
+    }
+    sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+    live = __reduce_add_sync(0xFFFFFFFFu, live);
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    const uint64_t segments = static_cast<uint64_t>(live) * segs, total = static_cast<uint64_t>(sum) * segs;
+    Plan p;
+    p.warps = W / 2;
+    if (segments <= gridDim.x && total <= static_cast<uint64_t>(8 * W) * gridDim.x) p.warps = W;
+    while (p.warps > 1 && segments >= 2 * gridDim.x * (W / p.warps) && total < 4 * p.warps * segments) p.warps /= 2;
+    p.workers = gridDim.x * (W / p.warps);
+    if (longest <= 8 * p.warps) {
+        p.cut = 8 * p.warps;
+        p.pieces = static_cast<uint32_t>(segments);
+        return p;
+    }
+    const uint32_t rounds =
+        divide_up(total, p.workers) <= kLongUnits * p.warps && segments <= p.workers / 2 ? 1 : kPiecesPerWorker;
+    // (the second bound keeps the workspace's slots enough when a worker has few warps)
+    uint32_t low = max(divide_up(total, rounds * p.workers), divide_up(total, kPiecesPerWorker * gridDim.x * 2));
+    low = max(low, 2 * p.warps);
+    p.cut = low;
+    p.pieces = count_pieces(units, B, segs, low, lane);
+    const uint32_t most = rounds * p.workers;
+    if (p.pieces > most && segments <= most / 2) {
+        // at twice the cut and a unit, total / cut + segments <= most
+        uint32_t high = 2 * low + 1;
+        p.pieces = 0;
+        while (high - low > 1 + (low >> 5)) {
+            const uint32_t mid = low + (high - low) / 2, at_mid = count_pieces(units, B, segs, mid, lane);
+            if (at_mid > most)
+                low = mid;
+            else
+                high = mid, p.pieces = at_mid;
+        }
+        p.cut = high;
+        if (p.pieces == 0) p.pieces = count_pieces(units, B, segs, high, lane);
+    }
+    return p;
+}
+
+// A sequence among the others, and what precedes it.
+struct Place {
+    int b;
+    uint32_t units_before;   // units of the sequences before it (one segment each)
+    uint32_t pieces_before;  // pieces of all their segments
+};
+
+// The sequence whose pieces include number `id` (there is one), searched from `at` on: every segment of a
+// sequence of n units has ceil(n / cut) pieces.  The whole warp calls it.
+template <typename Units>
+__device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, uint32_t id, uint32_t cut, uint32_t segs,
+                                        int lane) {
+    if (B == 1) return at;
+    for (;;) {
         const int b = at.b + lane;
-        const int n = b < a.B ? span_of(a, b).units<KEYS>() : 0;
-        const uint32_t p = static_cast<uint32_t>((n + cut - 1) / cut) * segs;
-        uint32_t sum = p;
-        int64_t units = static_cast<int64_t>(n) * segs;
-        const int64_t own = units;
+        const uint32_t n = b < B ? units_of(b) : 0, p = (n + cut - 1) / cut * segs;
+        uint32_t sum = p, units = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            const int64_t up_units = __shfl_up_sync(0xFFFFFFFFu, units, o);
+            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o), up_units = __shfl_up_sync(0xFFFFFFFFu, units, o);
             if (lane >= o) sum += up, units += up_units;
         }
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, at.pieces_before + sum > id);
         if (past) {
             const int f = __ffs(past) - 1;
             at.b += f;
-            at.units_before += __shfl_sync(0xFFFFFFFFu, units - own, f);
+            at.units_before += __shfl_sync(0xFFFFFFFFu, units - n, f);
             at.pieces_before += __shfl_sync(0xFFFFFFFFu, sum - p, f);
             return at;
         }
@@ -741,19 +835,17 @@ __device__ __forceinline__ Place locate(const AttnArgs& a, Place at, uint32_t id
         at.units_before += __shfl_sync(0xFFFFFFFFu, units, 31);
         at.pieces_before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    at.b = a.B;
-    return at;
 }
 
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel(const AttnArgs a) {
     using S = Shape<FMT, D, NT>;
-    constexpr int WG = S::WG, NST = S::NST, THREADS = WG * 32, KS = S::KS, KEYS = 16 * KS;
+    constexpr int NST = S::NST, KS = S::KS, KEYS = 16 * KS;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint32_t s_word[S::NG][2];            // a worker's next piece; whether it joins
-    __shared__ float s_ml[S::NG][WG * 2 * NT * 8];   // the maxima and sums of its warps
-    const int lane = threadIdx.x % 32, group = threadIdx.x / THREADS;
-    const int tid = threadIdx.x % THREADS, warp = tid / 32;  // in the worker
+    __shared__ uint32_t s_word[S::W][2];            // a worker's next piece; whether it joins
+    __shared__ float s_ml[S::W * 2 * NT * 8];       // the maxima and sums of the warps
+    __shared__ Plan s_plan;
+    const int lane = threadIdx.x % 32;
     const uint32_t base = smem_u32(smem);
     if (FMT == kKvNf4) {
         for (int i = threadIdx.x; i < 256 * 32; i += S::W * 32) {
@@ -771,53 +863,48 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         return;
     }
 
-    // all units, and with them the size that segments are cut to
-    const int segs = a.c.kv_heads * a.chunks;  // segments of a sequence
-    const uint32_t worker = blockIdx.x * S::NG + group, workers = gridDim.x * S::NG;
-    int64_t total = 0;
-    for (int b = lane; b < a.B; b += 32) total += span_of(a, b).units<KEYS>();
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    total *= segs;
-    int cut;
-    {
-        const int64_t one = (total + workers - 1) / workers;  // a piece for each worker
-        const int64_t some = (total + workers * kPiecesPerWorker - 1) / (workers * kPiecesPerWorker);
-        int64_t c = one <= kLongUnits * WG ? one : some > kLongUnits * WG ? some : kLongUnits * WG;
-        if (c < WG) c = WG;
-        cut = static_cast<int>(c < (1 << 30) ? c : (1 << 30));
+    const uint32_t segs = a.c.kv_heads * a.chunks;  // segments of a sequence
+    auto units_of = [&](int b) { return static_cast<uint32_t>(span_of(a, b).units<KEYS>()); };
+    if (threadIdx.x < 32) {
+        const uint32_t mine = lane < a.B ? units_of(lane) : 0;  // read once
+        const Plan p = make_plan<S::W>([&](int b) { return b == lane ? mine : units_of(b); }, a.B, segs, lane);
+        if (lane == 0) s_plan = p;
     }
+    __syncthreads();
+    // (the plan is read where it is needed: it does not live in registers)
+    const volatile Plan& plan = s_plan;
+    const int wg = plan.warps, threads = wg * 32;
+    const int group = threadIdx.x / threads, tid = threadIdx.x - group * threads, warp = tid / 32;
 
-    const uint32_t ring = area_of<FMT>(base, group * WG + warp, S::kArea);
+    const uint32_t ring = area_of<FMT>(base, threadIdx.x / 32, S::kArea);
     auto area = [&](int w) {  // of warp w of this worker, once its ring is drained
-        return reinterpret_cast<float*>(smem + (area_of<FMT>(base, group * WG + w, S::kArea) - base));
+        return reinterpret_cast<float*>(smem + (area_of<FMT>(base, group * wg + w, S::kArea) - base));
     };
     const int blocks_per_page = a.c.page_size >> 4;
     WarpState<FMT, D, NT> s;
     Place at{0, 0, 0};
-    for (uint32_t id = worker;;) {
-        at = locate<KEYS>(a, at, id, cut, segs, lane);
-        if (at.b == a.B) break;
-        uint32_t next = 0;
-        if (tid == 0) next = atomicAdd(a.tickets, 1u) + workers;  // arrives while the piece is worked on
+    uint32_t id = blockIdx.x * (S::W / wg) + group;
+    while (id < plan.pieces) {
+        const uint32_t cut = plan.cut;
+        at = locate(units_of, a.B, at, id, cut, segs, lane);
         // piece `part` of `parts` of segment `seg`: units [u0, u1) of its n
         const Span span = span_of(a, at.b);
-        const int n = span.units<KEYS>();
-        const uint32_t parts = static_cast<uint32_t>((n + cut - 1) / cut);
+        const uint32_t n = span.units<KEYS>();
+        const uint32_t parts = (n + cut - 1) / cut;
         const uint32_t in_seq = id - at.pieces_before;
-        const int seg = static_cast<int>(in_seq / parts);
+        const int seg = static_cast<int>(parts == 1 ? in_seq : in_seq / parts);
         const uint32_t part = in_seq - seg * parts;
-        const int len = static_cast<int>((n + parts - 1) / parts);
-        const int u0 = min(n, static_cast<int>(part) * len), u1 = min(n, u0 + len);
+        const uint32_t len = parts == 1 ? n : (n + parts - 1) / parts;
+        const int u0 = static_cast<int>(part * len), u1 = static_cast<int>(min(n, part * len + len));
         const int kv = seg / a.chunks, head0 = (seg - kv * a.chunks) * a.chunk_heads;
         const int heads = min(a.chunk_heads, a.group - head0);
         const int64_t row0 = static_cast<int64_t>(at.b) * a.q_heads + static_cast<int64_t>(kv) * a.group + head0;
 
         // this warp's units: u0 + warp + WG j, j < mine; lane i holds where block 32 * batch + i of them lies
-        const int mine = u1 - u0 > warp ? (u1 - u0 - warp + WG - 1) / WG : 0;
+        const int mine = u1 - u0 > warp ? (u1 - u0 - warp + wg - 1) / wg : 0;
         const int first = span.start / KEYS + u0 + warp;
         auto place_of = [&](int i) -> int64_t {
-            const uint32_t block = (first + i / KS * WG) * KS + i % KS;
+            const uint32_t block = (first + i / KS * wg) * KS + i % KS;
             // past the warp's units, or nothing live in it: its page is not looked up
             if (i >= mine * KS || block * 16 >= static_cast<uint32_t>(span.end) ||
                 block * 16 + 16 <= static_cast<uint32_t>(span.start))
@@ -830,12 +917,14 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             }
             return (page * a.c.kv_heads + kv) * a.c.page_size + (block - p * blocks_per_page) * 16;
         };
+        uint32_t next = 0xFFFFFFFFu;
+        if (tid == 0 && plan.pieces > plan.workers) next = atomicAdd(a.tickets, 1u) + plan.workers;  // arrives meanwhile
         int64_t places = place_of(lane), next_places = mine * KS > 32 ? place_of(32 + lane) : -2;
-        load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);
 
         uint32_t bad = 0;  // bits of the blocks issued last (the newest lowest): no page
         uint32_t in_buf = ring, out_buf = ring;
         for (int j = 1 - NST; j < mine; j++) {
+            if (j == 0) load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);  // while the first stages arrive
             if (j >= 0) {
                 cp_async_wait<NST - 2>();
                 __syncwarp();  // the stage is complete for every lane, and the one before it is free
@@ -847,7 +936,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                     places = next_places;
                     next_places = place_of(ahead * KS + 32 + lane);
                 }
-                const int key0 = (first + ahead * WG) * KEYS;
+                const int key0 = (first + ahead * wg) * KEYS;
 #pragma unroll
                 for (int b = 0; b < KS; b++) {
                     const int64_t place = __shfl_sync(0xFFFFFFFFu, places, (ahead * KS + b) & 31);
@@ -859,7 +948,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (j >= 0) {
-                const int key0 = (first + j * WG) * KEYS, lo = span.start - key0, hi = span.end - key0;
+                const int key0 = (first + j * wg) * KEYS, lo = span.start - key0, hi = span.end - key0;
                 const uint32_t gone = (bad >> (KS * (NST - 1))) & ((1u << KS) - 1);
                 attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= KEYS && gone == 0, lo, hi, gone, lane);
                 out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
@@ -868,7 +957,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         cp_async_wait<0>();
         __syncwarp();  // the warp's ring is drained: its memory takes the warp's result
 
-        const int joiners = min(WG, u1 - u0);  // warps that had a unit
+        const int joiners = min(wg, u1 - u0);  // warps that had a unit
         if (warp < joiners) {
             float* dst = area(warp);
             const int g = lane >> 2, t = lane & 3;
@@ -890,60 +979,76 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                                 make_float2(s.o[nt][i][j] * back, s.o[nt][i][j + 2] * back);
                         }
                         if (g == 0) {
-                            s_ml[group][warp * 2 * heads + h] = s.m[nt][j];
-                            s_ml[group][warp * 2 * heads + heads + h] = l;
+                            float* ml = s_ml + (threadIdx.x / 32) * (2 * NT * 8);
+                            ml[h] = s.m[nt][j];
+                            ml[heads + h] = l;
                         }
                     }
                 }
         }
         if (tid == 0) s_word[group][0] = next;
-        worker_barrier<THREADS>(group);
+        worker_barrier(group, wg);
         id = s_word[group][0];
         uint2* out = reinterpret_cast<uint2*>(a.out + row0 * D);
         const int columns = heads * (D / 4);
         // slots of a segment's pieces: segments that are cut have more than `cut` units, so these runs are
         // disjoint
-        const int64_t slot0 = parts > 1 ? 2 * ((at.units_before + static_cast<int64_t>(seg) * n) / cut) : 0;
-        auto slot = [&](int64_t i) { return a.partials + (slot0 + i) * a.slot_floats; };
-        for (int i = tid; i < columns; i += THREADS) {
-            const Joined r = join<D, false>(area, s_ml[group], joiners, heads, i);
+        int slot0 = 0;
+        if (parts > 1) {
+            const uint64_t first_unit = static_cast<uint64_t>(at.units_before) * segs + static_cast<uint64_t>(seg) * n;
+            slot0 = 2 * static_cast<int>(first_unit < (uint64_t{1} << 32) ? static_cast<uint32_t>(first_unit) / cut
+                                                                          : first_unit / cut);
+        }
+        auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot0 + i) * a.slot_floats; };
+        for (int i = tid; i < columns; i += threads) {
+            const Joined r = join<D, false>(
+                area, [&](int w) { return s_ml + (group * wg + w) * (2 * NT * 8); }, joiners, heads, i);
             if (parts == 1)
                 out[i] = normalised(r);
             else
                 store_partial<D>(slot(part), r, heads, i);
         }
-        // joins `count` slots, `step` apart, once `tickets` says that all of them are there
-        auto join_slots = [&](uint32_t* ticket, int64_t from, int step, int count, bool last) {
-            __threadfence();
-            worker_barrier<THREADS>(group);
-            if (tid == 0) s_word[group][1] = atomicInc(ticket, count - 1) == static_cast<unsigned>(count - 1);
-            worker_barrier<THREADS>(group);
-            if (!s_word[group][1]) return false;
-            __threadfence();
-            float* ml = area(0);
-            for (int i = tid; i < count * 2 * heads; i += THREADS) {
-                const int j = i / (2 * heads);
-                ml[i] = __ldcg(slot(from + static_cast<int64_t>(j) * step) + heads * D + (i - j * 2 * heads));
+        // joins `count` slots, `step` apart, once `tickets` says that all of them are there; whether it did
+        auto join_slots = [&](uint32_t* ticket, int from, int step, int count, bool last) {
+            worker_barrier(group, wg);  // every thread's stores, then one fence and the ticket
+            if (tid == 0) {
+                __threadfence();
+                s_word[group][1] = atomicInc(ticket, count - 1) == static_cast<unsigned>(count - 1);
+                __threadfence();
             }
-            worker_barrier<THREADS>(group);
-            auto piece = [&](int j) { return slot(from + static_cast<int64_t>(j) * step); };
-            for (int i = tid; i < columns; i += THREADS) {
-                const Joined r = join<D, true>(piece, ml, count, heads, i);
+            worker_barrier(group, wg);
+            if (!s_word[group][1]) return false;
+            auto piece = [&](int j) { return slot(from + j * step); };
+            if (last && count <= 8) {  // everything in one round of loads
+                for (int i = tid; i < columns; i += threads)
+                    out[i] = normalised(
+                        join<D, true>(piece, [&](int j) { return piece(j) + heads * D; }, count, heads, i));
+                return true;
+            }
+            // the maxima and sums to shared memory first: one round for all of them, not one for each eight
+            float* ml = area(0);
+            for (int i = tid; i < count * 2 * heads; i += threads) {
+                const int j = i / (2 * heads);
+                ml[i] = __ldcg(piece(j) + heads * D + (i - j * 2 * heads));
+            }
+            worker_barrier(group, wg);
+            auto ml_of = [&](int j) { return ml + j * 2 * heads; };
+            for (int i = tid; i < columns; i += threads) {
+                const Joined r = join<D, true, true>(piece, ml_of, count, heads, i);
                 if (last)
                     out[i] = normalised(r);
-                else
+                else  // (into the first of them: nobody but this thread reads its column, nor the sums again)
                     store_partial<D>(slot(from), r, heads, i);
             }
             return true;
         };
         if (parts > 1) {
-            const int batch = part / kFanIn, batches = (parts + kFanIn - 1) / kFanIn;
-            const int64_t from = static_cast<int64_t>(batch) * kFanIn;
-            const int count = min(kFanIn, static_cast<int>(parts) - batch * kFanIn);
+            const int from = static_cast<int>(part) / kFanIn * kFanIn, batches = (parts + kFanIn - 1) / kFanIn;
+            const int count = min(kFanIn, static_cast<int>(parts) - from);
             if (join_slots(a.joins + slot0 + from, from, 1, count, batches == 1) && batches > 1)
                 join_slots(a.joins + kSlots + slot0, 0, kFanIn, batches, true);
         }
-        worker_barrier<THREADS>(group);  // the areas become rings again
+        worker_barrier(group, wg);  // the areas become rings again
     }
 
     // sequences with nothing to attend to, and lengths past their tables
@@ -954,7 +1059,10 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * (D / 8)) + i] = make_uint4(0, 0, 0, 0);
     }
     // the last worker leaves the tickets as it found them
-    if (tid == 0 && atomicInc(a.tickets + 1, workers - 1) == workers - 1) a.tickets[0] = 0;
+    if (tid == 0 && plan.pieces > plan.workers) {
+        const uint32_t last = plan.workers - 1;
+        if (atomicInc(a.tickets + 1, last) == last) a.tickets[0] = 0;
+    }
 }
 
 int slot_floats(int chunk_heads, int D) { return (chunk_heads * (D + 2) + 3) / 4 * 4; }
@@ -973,7 +1081,7 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
     if (attr_err != cudaSuccess) return attr_err;
     // as many CTAs as SMs, or fewer where the longest possible sequences leave less than that to do
     const int64_t most = a.B * static_cast<int64_t>(a.c.kv_heads) * a.chunks * ((a.max_pages * a.c.page_size + 16 * S::KS - 1) / (16 * S::KS));
-    int64_t grid = num_sms < kMaxWorkers / S::NG ? num_sms : kMaxWorkers / S::NG;
+    int64_t grid = num_sms < kMaxWorkers / 2 ? num_sms : kMaxWorkers / 2;
     if (grid > (most + S::W - 1) / S::W) grid = (most + S::W - 1) / S::W;
     if (grid < 1) grid = 1;
     cudaLaunchAttribute attr;
