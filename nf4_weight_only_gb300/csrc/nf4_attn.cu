@@ -25,7 +25,7 @@
 // further ones by a ticket.  Inside a piece its warps take units in turn, each with its own ring of
 // cp.async stages and no barrier; their results are joined in shared memory.  The pieces of a segment leave
 // partial results in the workspace; the worker that finishes the last of them joins them in their
-// order (16 at a time, then the joined ones), so results do not depend on timing.
+// order (24 at a time, then the joined ones), so results do not depend on timing.
 #include <mutex>
 
 #include "nf4_kv.cuh"
@@ -39,7 +39,7 @@ __device__ int g_attention_error;
 constexpr int kMaxWorkers = 320;      // of W / 2 warps
 constexpr int kPiecesPerWorker = 4;   // in long calls (see make_plan)
 constexpr int kLongUnits = 16;        // units a warp up to which a call is one piece a worker
-constexpr int kFanIn = 16;            // partial results joined at a time
+constexpr int kFanIn = 24;            // partial results joined at a time
 constexpr int kSlots = 2 * kMaxWorkers * kPiecesPerWorker + 2;  // partial results (see slot0)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;         // p may reach 2^8 before the running maximum moves
@@ -167,8 +167,8 @@ struct Shape {
     static constexpr int kStage = KS * kBlock;
     // Warps and stages: enough warps to issue the decoding (16 for the quantised formats where their
     // registers allow it), and about 100 KB in flight an SM.
-    static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : (NT == 2 || D == 256) ? 8 : FMT == kKvFp8 ? 12 : 16;
-    static constexpr int kRingMost = FMT == kKvNf4 ? (W == 16 ? 10240 : 20480) : 230400 / W / 16 * 16;
+    static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : D == 256 || NT == 2 ? 8 : 12;
+    static constexpr int kRingMost = FMT == kKvNf4 ? (W == 12 ? 8704 : 20480) : 230400 / W / 16 * 16;
     static constexpr int kStagesFit = kRingMost / kStage;
     static constexpr int NST = kStagesFit > 10 ? 10 : kStagesFit;
     static constexpr int kRing = NST * kStage;
@@ -253,14 +253,12 @@ __device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64
     }
 }
 
-// The same for a place that may be negative (nothing to read: zeros).
+// A block that may have nothing to read (place < 0: zeros) or dead keys.
 template <int FMT, int D, int NT>
-__device__ __forceinline__ void issue_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+__device__ __forceinline__ void copy_edge_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
     if (place < 0) {
         for (int i = lane * 4; i < Shape<FMT, D, NT>::kBlock; i += 128)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + i), "r"(0) : "memory");
-    } else if (lo <= 0 && hi >= 16) {
-        copy_block<FMT, D, NT, true>(c, buf, place, lo, hi, lane);
     } else {
         copy_block<FMT, D, NT, false>(c, buf, place, lo, hi, lane);
     }
@@ -446,36 +444,6 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
                     }
                 }
             }
-        if (!full) {
-#pragma unroll
-            for (int b = 0; b < KS; b++)
-#pragma unroll
-                for (int r = 0; r < 2; r++)
-#pragma unroll
-                    for (int c = 0; c < GR; c++)
-                        if (!on(b, r)) vs[b][r][c] = 0.0f;
-        }
-        // V scales in fp16 range: the largest times vn stays below 2^7
-        float top = 0.0f;
-#pragma unroll
-        for (int b = 0; b < KS; b++)
-#pragma unroll
-            for (int r = 0; r < 2; r++)
-#pragma unroll
-                for (int c = 0; c < GR; c++) top = fmaxf(top, vs[b][r][c]);
-        if (__any_sync(0xFFFFFFFFu, top > s.vlim)) {
-            top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 7), 254);
-            const float vn = __uint_as_float(static_cast<uint32_t>(260 - e) << 23), f = vn / s.vn;
-            s.vn = vn;
-            s.vlim = __uint_as_float(static_cast<uint32_t>(min(e + 1, 254)) << 23);
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int i = 0; i < D / 16; i++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) s.o[nt][i][j] *= f;
-        }
     }
 
     // y: S with K's scales; x = y mul - m: base-2 logits of keys (row g: j = 0, 1; row g + 8: 2, 3) and heads
@@ -509,6 +477,36 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     if (!on(b, j >> 1)) x[b][nt][j] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < KS; b++)
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+#pragma unroll
+                for (int c = 0; c < GR; c++)
+                    if (!on(b, r)) vs[b][r][c] = 0.0f;
+    }
+    if (FMT != kKvBf16) {
+        // V scales in fp16 range: the largest times vn stays below 2^7
+        float top = 0.0f;
+#pragma unroll
+        for (int b = 0; b < KS; b++)
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+#pragma unroll
+                for (int c = 0; c < GR; c++) top = fmaxf(top, vs[b][r][c]);
+        if (__any_sync(0xFFFFFFFFu, top > s.vlim)) {
+            top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 7), 254);
+            const float vn = __uint_as_float(static_cast<uint32_t>(260 - e) << 23), f = vn / s.vn;
+            s.vn = vn;
+            s.vlim = __uint_as_float(static_cast<uint32_t>(min(e + 1, 254)) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int i = 0; i < D / 16; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) s.o[nt][i][j] *= f;
+        }
     }
 #pragma unroll
     for (int b = 0; b < KS; b++)
@@ -776,8 +774,8 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
         p.pieces = static_cast<uint32_t>(segments);
         return p;
     }
-    const uint32_t rounds =
-        divide_up(total, p.workers) <= kLongUnits * p.warps && segments <= p.workers / 2 ? 1 : kPiecesPerWorker;
+    const uint32_t share = divide_up(total, p.workers) / p.warps;  // units a warp
+    const uint32_t rounds = segments > p.workers / 2 ? kPiecesPerWorker : share < 2 * kLongUnits ? 1 : share < 4 * kLongUnits ? 2 : kPiecesPerWorker;
     // (the second bound keeps the workspace's slots enough when a worker has few warps)
     uint32_t low = max(divide_up(total, rounds * p.workers), divide_up(total, kPiecesPerWorker * gridDim.x * 2));
     low = max(low, 2 * p.warps);
@@ -937,12 +935,25 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                     next_places = place_of(ahead * KS + 32 + lane);
                 }
                 const int key0 = (first + ahead * wg) * KEYS;
+                const int lo = span.start - key0, hi = span.end - key0;
+                int64_t place[KS];
+                bool fast = lo <= 0 && hi >= KEYS;
 #pragma unroll
                 for (int b = 0; b < KS; b++) {
-                    const int64_t place = __shfl_sync(0xFFFFFFFFu, places, (ahead * KS + b) & 31);
-                    bad |= place == -1 ? 1u << b : 0u;
-                    issue_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, place, span.start - key0 - 16 * b,
-                                            span.end - key0 - 16 * b, lane);
+                    place[b] = __shfl_sync(0xFFFFFFFFu, places, (ahead * KS + b) & 31);
+                    fast = fast && place[b] >= 0;
+                }
+                if (fast) {
+#pragma unroll
+                    for (int b = 0; b < KS; b++)
+                        copy_block<FMT, D, NT, true>(a.c, in_buf + b * S::kBlock, place[b], 0, 16, lane);
+                } else {
+#pragma unroll 1
+                    for (int b = 0; b < KS; b++) {
+                        const int64_t at_b = KS > 1 && b ? place[KS - 1] : place[0];
+                        bad |= at_b == -1 ? 1u << b : 0u;
+                        copy_edge_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, at_b, lo - 16 * b, hi - 16 * b, lane);
+                    }
                 }
                 in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
             }
