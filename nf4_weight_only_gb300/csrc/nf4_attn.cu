@@ -37,10 +37,10 @@ namespace {
 __device__ int g_attention_error;
 
 constexpr int kMaxWorkers = 320;      // of W / 2 warps
-constexpr int kPiecesPerWorker = 4;   // in long calls (see make_plan)
+constexpr int kRounds = 4;            // pieces a worker gets in long calls
 constexpr int kLongUnits = 16;        // units a warp up to which a call is one piece a worker
 constexpr int kFanIn = 24;            // partial results joined at a time
-constexpr int kSlots = 2 * kMaxWorkers * kPiecesPerWorker + 2;  // partial results (see slot0)
+constexpr int kSlots = 2 * kMaxWorkers * kRounds + 2;  // partial results (see slot0)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;         // p may reach 2^8 before the running maximum moves
 
@@ -722,11 +722,14 @@ __device__ __forceinline__ void worker_barrier(int group, int warps) {
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(warps * 32) : "memory");
 }
 
-// How the segments are cut: into pieces of at most `cut` units, as equal as they come.
+// How the work is cut.  By segment: every segment into pieces of at most `cut` units, as equal as they come.
+// By line (cut = 0): the units of all segments end to end into one cell of `cell` units a worker, a cell's
+// part of a segment being a piece.
 struct Plan {
     uint32_t warps, workers;  // warps of a worker; workers of the grid
-    uint32_t cut;
-    uint32_t pieces;          // of all segments
+    uint32_t count;           // pieces, or cells
+    uint32_t cut, cell;
+    uint64_t total;           // units
 };
 
 __device__ __forceinline__ uint32_t divide_up(uint64_t a, uint32_t d) {  // at most 2^30
@@ -748,10 +751,16 @@ __device__ __forceinline__ uint32_t count_pieces(const Units& units, int B, uint
 //  - all W, when there is at most a segment for each CTA and little to do: no second piece to overlap with;
 //  - fewer, when there are many segments too short to keep W / 2 warps busy.
 // Sequences of up to 8 units a warp are not cut: the join of partial results costs 3 us, about what these
-// units do.  Otherwise a call of up to 16 units a warp is one piece a worker, a longer one four, which
-// evens out the SMs' different speeds.  Rounding up the pieces of each segment must not start another round:
-// `cut` grows until the pieces fit (bisection), unless the segments alone fill the rounds.
-template <int W, typename Units>
+// units do.  The rest is cut by segment: one piece a worker where there are few segments and less than
+// 2 kLongUnits units a warp to do, else up to four, taken by ticket, since the SMs' shares of the memory's
+// rate differ by 20% (one bf16 sequence of 131071 keys and 8 kv heads: 102 us; four pieces whatever their
+// length, 110; equal runs laid end to end, 118).  Rounding up the pieces of each segment must not start
+// another round, so `cut` grows until they fit (bisection), unless the segments alone fill the rounds.
+// LINE: where decoding, not the memory, bounds the SM (NF4), SMs are equally fast, and long segments (8 units
+// a warp on average) are cut by line: the same work for every worker (32 sequences up to 16384: 89 us;
+// by segment 95), which shorter ones would pay for with a start and a join for each (64 sequences up
+// to 2000: 60 us; by segment 46).
+template <int W, bool LINE, typename Units>
 __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t segs, int lane) {
     uint32_t sum = 0, live = 0, longest = 0;
     for (int b = lane; b < B; b += 32) {
@@ -765,63 +774,83 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     const uint64_t segments = static_cast<uint64_t>(live) * segs, total = static_cast<uint64_t>(sum) * segs;
     Plan p;
+    p.total = total;
     p.warps = W / 2;
     if (segments <= gridDim.x && total <= static_cast<uint64_t>(8 * W) * gridDim.x) p.warps = W;
     while (p.warps > 1 && segments >= 2 * gridDim.x * (W / p.warps) && total < 4 * p.warps * segments) p.warps /= 2;
     p.workers = gridDim.x * (W / p.warps);
     if (longest <= 8 * p.warps) {
         p.cut = 8 * p.warps;
-        p.pieces = static_cast<uint32_t>(segments);
+        p.count = static_cast<uint32_t>(segments);
         return p;
     }
-    const uint32_t share = divide_up(total, p.workers) / p.warps;  // units a warp
-    const uint32_t rounds = segments > p.workers / 2 ? kPiecesPerWorker : share < 2 * kLongUnits ? 1 : share < 4 * kLongUnits ? 2 : kPiecesPerWorker;
-    // (the second bound keeps the workspace's slots enough when a worker has few warps)
-    uint32_t low = max(divide_up(total, rounds * p.workers), divide_up(total, kPiecesPerWorker * gridDim.x * 2));
+    const uint32_t share = divide_up(total, p.workers);
+    p.cut = 0;
+    if (LINE && p.warps >= W / 2 && (share >= 2 * kLongUnits * p.warps || segments > p.workers / 2) &&
+        total >= 8 * p.warps * segments) {
+        p.cell = share;
+        p.count = p.workers;
+        return p;
+    }
+    const uint32_t rounds = segments > p.workers / 2 || share >= 4 * kLongUnits * p.warps ? kRounds
+                            : share >= 2 * kLongUnits * p.warps                           ? 2
+                                                                                          : 1;
+    // (the second bound keeps the workspace's slots enough when workers of few warps are many)
+    uint32_t low = max(divide_up(total, rounds * p.workers), divide_up(total, kRounds * gridDim.x * 2));
     low = max(low, 2 * p.warps);
     p.cut = low;
-    p.pieces = count_pieces(units, B, segs, low, lane);
+    p.count = count_pieces(units, B, segs, low, lane);
     const uint32_t most = rounds * p.workers;
-    if (p.pieces > most && segments <= most / 2) {
+    if (p.count > most && segments <= most / 2) {
         // at twice the cut and a unit, total / cut + segments <= most
         uint32_t high = 2 * low + 1;
-        p.pieces = 0;
+        p.count = 0;
         while (high - low > 1 + (low >> 5)) {
             const uint32_t mid = low + (high - low) / 2, at_mid = count_pieces(units, B, segs, mid, lane);
             if (at_mid > most)
                 low = mid;
             else
-                high = mid, p.pieces = at_mid;
+                high = mid, p.count = at_mid;
         }
         p.cut = high;
-        if (p.pieces == 0) p.pieces = count_pieces(units, B, segs, high, lane);
+        if (p.count == 0) p.count = count_pieces(units, B, segs, high, lane);
     }
     return p;
+}
+
+// By line: the first unit of a cell, and the cell of a unit.
+__device__ __forceinline__ uint64_t cell_start(const volatile Plan& p, uint32_t cell) {
+    const uint64_t x = static_cast<uint64_t>(cell) * p.cell;
+    return x < p.total ? x : p.total;
+}
+__device__ __forceinline__ uint32_t cell_of(const volatile Plan& p, uint64_t x) {
+    const uint32_t size = p.cell;
+    return x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / size : static_cast<uint32_t>(x / size);
 }
 
 // A sequence among the others, and what precedes it.
 struct Place {
     int b;
     uint32_t units_before;   // units of the sequences before it (one segment each)
-    uint32_t pieces_before;  // pieces of all their segments
+    uint32_t pieces_before;  // by segment: pieces of those sequences (one segment each)
 };
 
-// The sequence whose pieces include number `id` (there is one), searched from `at` on: every segment of a
-// sequence of n units has ceil(n / cut) pieces.  The whole warp calls it.
+// The sequence in which number `id` falls (there is one), searched from `at` on: of the pieces of one segment
+// of each sequence, ceil(n / cut) for n units, or (cut = 0) of its units.  The whole warp calls it.
 template <typename Units>
-__device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, uint32_t id, uint32_t cut, uint32_t segs,
-                                        int lane) {
+__device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, uint32_t id, uint32_t cut, int lane) {
     if (B == 1) return at;
     for (;;) {
         const int b = at.b + lane;
-        const uint32_t n = b < B ? units_of(b) : 0, p = (n + cut - 1) / cut * segs;
+        const uint32_t n = b < B ? units_of(b) : 0, p = cut ? (n + cut - 1) / cut : 0;
         uint32_t sum = p, units = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o), up_units = __shfl_up_sync(0xFFFFFFFFu, units, o);
             if (lane >= o) sum += up, units += up_units;
         }
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, at.pieces_before + sum > id);
+        const uint32_t past =
+            __ballot_sync(0xFFFFFFFFu, cut ? at.pieces_before + sum > id : at.units_before + units > id);
         if (past) {
             const int f = __ffs(past) - 1;
             at.b += f;
@@ -865,7 +894,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     auto units_of = [&](int b) { return static_cast<uint32_t>(span_of(a, b).units<KEYS>()); };
     if (threadIdx.x < 32) {
         const uint32_t mine = lane < a.B ? units_of(lane) : 0;  // read once
-        const Plan p = make_plan<S::W>([&](int b) { return b == lane ? mine : units_of(b); }, a.B, segs, lane);
+        const Plan p = make_plan<S::W, FMT == kKvNf4>([&](int b) { return b == lane ? mine : units_of(b); }, a.B, segs, lane);
         if (lane == 0) s_plan = p;
     }
     __syncthreads();
@@ -881,19 +910,44 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     const int blocks_per_page = a.c.page_size >> 4;
     WarpState<FMT, D, NT> s;
     Place at{0, 0, 0};
-    uint32_t id = blockIdx.x * (S::W / wg) + group;
-    while (id < plan.pieces) {
+    uint32_t id = blockIdx.x * (S::W / wg) + group, next = 0;
+    uint64_t x = 0, stop = 0;  // by line: what is left of the cell
+    while (id < plan.count) {
         const uint32_t cut = plan.cut;
-        at = locate(units_of, a.B, at, id, cut, segs, lane);
-        // piece `part` of `parts` of segment `seg`: units [u0, u1) of its n
+        if (x == stop) {
+            if (!cut) {
+                x = cell_start(plan, id), stop = cell_start(plan, id + 1);
+                if (x == stop) break;
+                at = locate(units_of, a.B, at, x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / segs
+                                                                       : static_cast<uint32_t>(x / segs), 0, lane);
+            } else {
+                at = locate(units_of, a.B, at, id / segs, cut, lane);
+            }
+            if (tid == 0) next = plan.count > plan.workers ? atomicAdd(a.tickets, 1u) + plan.workers : 0xFFFFFFFFu;
+        }
+        // the piece: units [u0, u1) of the n of segment `seg`
         const Span span = span_of(a, at.b);
         const uint32_t n = span.units<KEYS>();
-        const uint32_t parts = (n + cut - 1) / cut;
-        const uint32_t in_seq = id - at.pieces_before;
-        const int seg = static_cast<int>(parts == 1 ? in_seq : in_seq / parts);
-        const uint32_t part = in_seq - seg * parts;
-        const uint32_t len = parts == 1 ? n : (n + parts - 1) / parts;
-        const int u0 = static_cast<int>(part * len), u1 = static_cast<int>(min(n, part * len + len));
+        uint32_t parts = 1, part = 0;  // by segment: of how many it is which
+        int seg, u0, u1;
+        if (cut) {
+            parts = (n + cut - 1) / cut;
+            const uint32_t in_seq = id - at.pieces_before * segs, len = parts == 1 ? n : (n + parts - 1) / parts;
+            seg = static_cast<int>(parts == 1 ? in_seq : in_seq / parts);
+            part = in_seq - seg * parts;
+            u0 = static_cast<int>(part * len), u1 = static_cast<int>(min(n, part * len + len));
+        } else {
+            const uint64_t in_seq = x - static_cast<uint64_t>(at.units_before) * segs, left = stop - x;
+            if (n == 0 || in_seq >= static_cast<uint64_t>(n) * segs) {  // on to the next sequence
+                at.units_before += n;
+                at.b++;
+                continue;
+            }
+            seg = static_cast<int>(in_seq < (uint64_t{1} << 32) ? static_cast<uint32_t>(in_seq) / n : in_seq / n);
+            u0 = static_cast<int>(in_seq - static_cast<uint64_t>(seg) * n);
+            u1 = static_cast<int>(left < n - u0 ? u0 + left : n);
+            x += u1 - u0;
+        }
         const int kv = seg / a.chunks, head0 = (seg - kv * a.chunks) * a.chunk_heads;
         const int heads = min(a.chunk_heads, a.group - head0);
         const int64_t row0 = static_cast<int64_t>(at.b) * a.q_heads + static_cast<int64_t>(kv) * a.group + head0;
@@ -915,8 +969,6 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             }
             return (page * a.c.kv_heads + kv) * a.c.page_size + (block - p * blocks_per_page) * 16;
         };
-        uint32_t next = 0xFFFFFFFFu;
-        if (tid == 0 && plan.pieces > plan.workers) next = atomicAdd(a.tickets, 1u) + plan.workers;  // arrives meanwhile
         int64_t places = place_of(lane), next_places = mine * KS > 32 ? place_of(32 + lane) : -2;
 
         uint32_t bad = 0;  // bits of the blocks issued last (the newest lowest): no page
@@ -999,22 +1051,31 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         }
         if (tid == 0) s_word[group][0] = next;
         worker_barrier(group, wg);
-        id = s_word[group][0];
         uint2* out = reinterpret_cast<uint2*>(a.out + row0 * D);
         const int columns = heads * (D / 4);
-        // slots of a segment's pieces: segments that are cut have more than `cut` units, so these runs are
-        // disjoint
+        // The slots of a segment's pieces.  By line: two a cell, for the piece that begins a segment and for one
+        // that goes on with it.  By segment: segments that are cut have more than `cut` units, so the runs of
+        // slots from twice their first unit's quotient are disjoint.
+        const bool whole = u0 == 0 && u1 == static_cast<int>(n);
         int slot0 = 0;
-        if (parts > 1) {
+        if (!whole) {
             const uint64_t first_unit = static_cast<uint64_t>(at.units_before) * segs + static_cast<uint64_t>(seg) * n;
-            slot0 = 2 * static_cast<int>(first_unit < (uint64_t{1} << 32) ? static_cast<uint32_t>(first_unit) / cut
-                                                                          : first_unit / cut);
+            if (cut) {
+                slot0 = 2 * static_cast<int>(first_unit < (uint64_t{1} << 32) ? static_cast<uint32_t>(first_unit) / cut
+                                                                              : first_unit / cut);
+            } else {
+                const uint32_t cell0 = cell_of(plan, first_unit);
+                slot0 = 2 * cell0 + 1;
+                parts = cell_of(plan, first_unit + n - 1) - cell0 + 1;
+                part = id - cell0;
+            }
         }
-        auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot0 + i) * a.slot_floats; };
+        auto slot_index = [&](int i) { return slot0 + (cut ? i : 2 * i - (i > 0)); };
+        auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot_index(i)) * a.slot_floats; };
         for (int i = tid; i < columns; i += threads) {
             const Joined r = join<D, false>(
                 area, [&](int w) { return s_ml + (group * wg + w) * (2 * NT * 8); }, joiners, heads, i);
-            if (parts == 1)
+            if (whole)
                 out[i] = normalised(r);
             else
                 store_partial<D>(slot(part), r, heads, i);
@@ -1053,12 +1114,13 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             }
             return true;
         };
-        if (parts > 1) {
+        if (!whole) {
             const int from = static_cast<int>(part) / kFanIn * kFanIn, batches = (parts + kFanIn - 1) / kFanIn;
             const int count = min(kFanIn, static_cast<int>(parts) - from);
-            if (join_slots(a.joins + slot0 + from, from, 1, count, batches == 1) && batches > 1)
+            if (join_slots(a.joins + slot_index(from), from, 1, count, batches == 1) && batches > 1)
                 join_slots(a.joins + kSlots + slot0, 0, kFanIn, batches, true);
         }
+        if (x == stop) id = s_word[group][0];
         worker_barrier(group, wg);  // the areas become rings again
     }
 
@@ -1070,7 +1132,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * (D / 8)) + i] = make_uint4(0, 0, 0, 0);
     }
     // the last worker leaves the tickets as it found them
-    if (tid == 0 && plan.pieces > plan.workers) {
+    if (tid == 0 && plan.count > plan.workers) {
         const uint32_t last = plan.workers - 1;
         if (atomicInc(a.tickets + 1, last) == last) a.tickets[0] = 0;
     }
