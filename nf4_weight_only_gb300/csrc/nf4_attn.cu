@@ -914,8 +914,9 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     uint64_t x = 0, stop = 0;  // by line: what is left of the cell
     while (id < plan.count) {
         const uint32_t cut = plan.cut;
+        const bool by_line = FMT == kKvNf4 && cut == 0;
         if (x == stop) {
-            if (!cut) {
+            if (by_line) {
                 x = cell_start(plan, id), stop = cell_start(plan, id + 1);
                 if (x == stop) break;
                 at = locate(units_of, a.B, at, x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / segs
@@ -930,7 +931,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         const uint32_t n = span.units<KEYS>();
         uint32_t parts = 1, part = 0;  // by segment: of how many it is which
         int seg, u0, u1;
-        if (cut) {
+        if (!by_line) {
             parts = (n + cut - 1) / cut;
             const uint32_t in_seq = id - at.pieces_before * segs, len = parts == 1 ? n : (n + parts - 1) / parts;
             seg = static_cast<int>(parts == 1 ? in_seq : in_seq / parts);
@@ -973,13 +974,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
 
         uint32_t bad = 0;  // bits of the blocks issued last (the newest lowest): no page
         uint32_t in_buf = ring, out_buf = ring;
-        for (int j = 1 - NST; j < mine; j++) {
-            if (j == 0) load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);  // while the first stages arrive
-            if (j >= 0) {
-                cp_async_wait<NST - 2>();
-                __syncwarp();  // the stage is complete for every lane, and the one before it is free
-            }
-            const int ahead = j + NST - 1;
+        auto issue = [&](int ahead) {
             bad <<= KS;
             if (ahead < mine) {
                 if (ahead > 0 && (ahead * KS & 31) == 0) {
@@ -1010,12 +1005,19 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (j >= 0) {
-                const int key0 = (first + j * wg) * KEYS, lo = span.start - key0, hi = span.end - key0;
-                const uint32_t gone = (bad >> (KS * (NST - 1))) & ((1u << KS) - 1);
-                attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= KEYS && gone == 0, lo, hi, gone, lane);
-                out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
-            }
+        };
+#pragma unroll 1
+        for (int j = 0; j < NST - 1; j++) issue(j);
+        load_q<FMT, D, NT>(a, s, a.q + row0 * D, heads, lane);  // while the first stages arrive
+#pragma unroll 1
+        for (int j = 0; j < mine; j++) {
+            cp_async_wait<NST - 2>();
+            __syncwarp();  // the stage is complete for every lane, and the one before it is free
+            issue(j + NST - 1);
+            const int key0 = (first + j * wg) * KEYS, lo = span.start - key0, hi = span.end - key0;
+            const uint32_t gone = (bad >> (KS * (NST - 1))) & ((1u << KS) - 1);
+            attend_unit<FMT, D, NT>(s, out_buf, lo <= 0 && hi >= KEYS && gone == 0, lo, hi, gone, lane);
+            out_buf = out_buf + S::kStage == ring + S::kRing ? ring : out_buf + S::kStage;
         }
         cp_async_wait<0>();
         __syncwarp();  // the warp's ring is drained: its memory takes the warp's result
@@ -1060,7 +1062,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         int slot0 = 0;
         if (!whole) {
             const uint64_t first_unit = static_cast<uint64_t>(at.units_before) * segs + static_cast<uint64_t>(seg) * n;
-            if (cut) {
+            if (!by_line) {
                 slot0 = 2 * static_cast<int>(first_unit < (uint64_t{1} << 32) ? static_cast<uint32_t>(first_unit) / cut
                                                                               : first_unit / cut);
             } else {
@@ -1070,7 +1072,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 part = id - cell0;
             }
         }
-        auto slot_index = [&](int i) { return slot0 + (cut ? i : 2 * i - (i > 0)); };
+        auto slot_index = [&](int i) { return slot0 + (by_line ? 2 * i - (i > 0) : i); };
         auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot_index(i)) * a.slot_floats; };
         for (int i = tid; i < columns; i += threads) {
             const Joined r = join<D, false>(
