@@ -13,18 +13,43 @@ namespace {
 // A thread owns eight pairs of one token (16 values a head, two 16-byte pieces) and walks some of the
 // token's q and k heads with them, so the angles are computed once for all of these heads.
 //
-// Angle of a pair: positions * inv_freq radians, a real product, needed modulo 2 pi.  inv_freq / (2 pi)
-// is formed once in double and its fraction held as a 64-bit binary fraction F of a turn; F * position
-// modulo 2^64 is then the fraction of the product, exactly, by integer wrap-around (error: that of F,
-// 2^-53 relative, times the position: below 2^-22 turn at |position| < 2^31).  Its upper 32 bits, as a
-// signed number, are an angle in [-pi, pi), where the hardware sine and cosine have an absolute
-// error near 2^-21, far below the 2^-9 of the bf16 result.
+// Angle of a pair: positions * inv_freq radians, a real product, needed modulo 2 pi.  inv_freq / (2 pi) is
+// held as a 64-bit binary fraction F of a turn; F * position modulo 2^64 is then the fraction of the product,
+// exactly, by integer wrap-around.  With inv_freq = m 2^e (m of 24 bits) F is the product of m and 2^64 / (2 pi),
+// shifted by e, all in integers (double precision here runs at a sixty-fourth of the single rate and took
+// half of the kernel's time); F's error, 2^-63 below inv_freq = 1, times the position is below 2^-31 turn.
+// The upper 32 bits of F * position, as a signed number, are an angle in [-pi, pi), where the hardware sine and
+// cosine have an absolute error near 2^-21, far below the 2^-9 of the bf16 result.
 constexpr int kRopeThreads = 256;
 
 struct Turn {
     float c[8], s[8];
 };
 
+// (Kept out of line: inlined, the compiler computes it for every pair and selects.)
+__device__ __noinline__ uint64_t turn_fraction_large(float f) {
+    const double turns = static_cast<double>(f) * 0.15915494309189533577;
+    return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+}
+
+// The fraction of a turn, times 2^64, that one position moves a pair of angular frequency f.
+__device__ __forceinline__ uint64_t turn_fraction(float f) {
+    const uint32_t bits = __float_as_uint(f) & 0x7FFFFFFFu;
+    const int e = max(static_cast<int>(bits >> 23), 1) - 150;  // |f| = m 2^e
+    const uint64_t m = (bits & 0x7FFFFFu) | (bits >= 0x800000u ? 0x800000u : 0u);
+    uint64_t frac;
+    if (e <= -16) {  // |f| < 256
+        const uint64_t high = __umul64hi(2935890503282001226ull, m << 40);  // m 2^64 / (2 pi) / 2^24
+        const int shift = e + 24;
+        frac = shift >= 0 ? high << shift : shift > -64 ? high >> -shift : 0;
+    } else {
+        frac = turn_fraction_large(__uint_as_float(bits));
+    }
+    return f < 0.0f ? 0 - frac : frac;
+}
+
+// AHEAD: heads whose loads are in flight together.
+template <int AHEAD>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, int heads_step) {
     pdl_launch_dependents();
     const int chunks = a.head_dim / 16, rot = a.rotary_dim / 16;
@@ -46,12 +71,31 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
     }
     const int c = id % chunks, h0 = id / chunks;
     pdl_wait();
+    const bool turn = c < rot;
     // elements of this thread's two pieces inside a head
-    int e0, e1;
+    const int e0 = turn && !a.interleaved ? 8 * c : 16 * c;
+    const int e1 = turn && !a.interleaved ? 8 * c + a.rotary_dim / 2 : 16 * c + 8;
+    const int heads = a.q_heads + a.k_heads;
+    uint4 u[AHEAD], v[AHEAD];
+    uint16_t* dst[AHEAD];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int n = 0; n < AHEAD; n++) {
+            const int hn = h + n * heads_step;
+            dst[n] = nullptr;
+            if (hn < heads) {
+                const bool is_q = hn < a.q_heads;
+                const int64_t row = (is_q ? t * a.q_heads + hn : t * a.k_heads + (hn - a.q_heads)) * a.head_dim;
+                const uint16_t* src = (is_q ? a.q : a.k) + row;
+                dst[n] = (is_q ? a.q_out : a.k_out) + row;
+                u[n] = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+                v[n] = __ldcs(reinterpret_cast<const uint4*>(src + e1));
+            }
+        }
+    };
+    load(h0);  // in flight while the angles are worked out
     Turn r;
-    if (c < rot) {
-        e0 = a.interleaved ? 16 * c : 8 * c;
-        e1 = a.interleaved ? 16 * c + 8 : 8 * c + a.rotary_dim / 2;
+    if (turn) {
         int32_t pos[4];
 #pragma unroll
         for (int x = 0; x < 4; x++) pos[x] = x < a.axes ? a.positions[x * a.T + t] : 0;
@@ -59,49 +103,43 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
         for (int j = 0; j < 8; j++) {
             const int i = 8 * c + j;
             const int32_t p = i < a.section_end[0] ? pos[0] : i < a.section_end[1] ? pos[1] : i < a.section_end[2] ? pos[2] : pos[3];
-            const double turns = static_cast<double>(a.inv_freq[i]) * 0.15915494309189533577;
-            const uint64_t frac = __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
-            const uint64_t at = frac * static_cast<uint64_t>(static_cast<int64_t>(p));
+            const uint64_t at = turn_fraction(a.inv_freq[i]) * static_cast<uint64_t>(static_cast<int64_t>(p));
             const float angle = static_cast<float>(static_cast<int32_t>(at >> 32)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
             r.s[j] = __sinf(angle) * a.magnitude;
             r.c[j] = __cosf(angle) * a.magnitude;
         }
-    } else {
-        e0 = 16 * c;
-        e1 = 16 * c + 8;
     }
-    for (int h = h0; h < a.q_heads + a.k_heads; h += heads_step) {
-        const bool is_q = h < a.q_heads;
-        const uint16_t* src = is_q ? a.q : a.k;
-        uint16_t* dst = is_q ? a.q_out : a.k_out;
-        const int64_t row = (is_q ? t * a.q_heads + h : t * a.k_heads + (h - a.q_heads)) * a.head_dim;
-        uint4 u = *reinterpret_cast<const uint4*>(src + row + e0), v = *reinterpret_cast<const uint4*>(src + row + e1);
-        if (c < rot) {
-            uint32_t in0[4] = {u.x, u.y, u.z, u.w}, in1[4] = {v.x, v.y, v.z, v.w}, o0[4], o1[4];
-            if (a.interleaved) {
+    for (int h = h0; h < heads;) {
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    const float2 p = bf16x2_to_f32x2(j < 4 ? in0[j] : in1[j - 4]);
-                    const uint32_t w = f32x2_to_bf16x2(p.x * r.c[j] - p.y * r.s[j], p.y * r.c[j] + p.x * r.s[j]);
-                    if (j < 4)
-                        o0[j] = w;
-                    else
-                        o1[j - 4] = w;
-                }
-            } else {
+        for (int n = 0; n < AHEAD; n++) {
+            if (!dst[n]) continue;
+            if (turn) {
+                const uint32_t in0[4] = {u[n].x, u[n].y, u[n].z, u[n].w}, in1[4] = {v[n].x, v[n].y, v[n].z, v[n].w};
+                uint32_t o0[4], o1[4];
+                if (a.interleaved) {
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float2 p = bf16x2_to_f32x2(in0[j]), q = bf16x2_to_f32x2(in1[j]);
-                    const float c0 = r.c[2 * j], c1 = r.c[2 * j + 1], s0 = r.s[2 * j], s1 = r.s[2 * j + 1];
-                    o0[j] = f32x2_to_bf16x2(p.x * c0 - q.x * s0, p.y * c1 - q.y * s1);
-                    o1[j] = f32x2_to_bf16x2(q.x * c0 + p.x * s0, q.y * c1 + p.y * s1);
+                    for (int j = 0; j < 8; j++) {
+                        const float2 p = bf16x2_to_f32x2(j < 4 ? in0[j & 3] : in1[j & 3]);
+                        const uint32_t w = f32x2_to_bf16x2(p.x * r.c[j] - p.y * r.s[j], p.y * r.c[j] + p.x * r.s[j]);
+                        (j < 4 ? o0 : o1)[j & 3] = w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float2 p = bf16x2_to_f32x2(in0[j]), q = bf16x2_to_f32x2(in1[j]);
+                        const float c0 = r.c[2 * j], c1 = r.c[2 * j + 1], s0 = r.s[2 * j], s1 = r.s[2 * j + 1];
+                        o0[j] = f32x2_to_bf16x2(p.x * c0 - q.x * s0, p.y * c1 - q.y * s1);
+                        o1[j] = f32x2_to_bf16x2(q.x * c0 + p.x * s0, q.y * c1 + p.y * s1);
+                    }
                 }
+                u[n] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+                v[n] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
             }
-            u = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            v = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            __stcs(reinterpret_cast<uint4*>(dst[n] + e0), u[n]);
+            __stcs(reinterpret_cast<uint4*>(dst[n] + e1), v[n]);
         }
-        *reinterpret_cast<uint4*>(dst + row + e0) = u;
-        *reinterpret_cast<uint4*>(dst + row + e1) = v;
+        h += AHEAD * heads_step;
+        if (h < heads) load(h);
     }
 }
 
@@ -277,7 +315,7 @@ cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
     }
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = pdl_config(grid, kRopeThreads, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, rope_kernel, a, step);
+    return walk > 1 ? cudaLaunchKernelEx(&cfg, rope_kernel<4>, a, step) : cudaLaunchKernelEx(&cfg, rope_kernel<1>, a, step);
 }
 
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int64_t H,
