@@ -1,6 +1,7 @@
 // Rotary positions and the residual RMS norm: elementwise work over rows of activations, bound by the
 // bytes of their rows (long calls) or by the latency of one launch (decode).
 #include <cmath>
+#include <mutex>
 
 #include "nf4_kv.cuh"
 
@@ -146,9 +147,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
 // ---------------------------------------------------------------------------------------------
 // Residual RMS norm
 // ---------------------------------------------------------------------------------------------
-// One CTA a row.  h = x + residual stays in registers (CH pieces of eight values a thread; CH = 0, for
+// Two forms.  rmsnorm_kernel, for few rows or very wide ones: one CTA a row.  h = x + residual stays in registers (CH pieces of eight values a thread; CH = 0, for
 // rows too wide for that, reads the row again), one block reduction gives sum(h^2) and max |h w| at once:
-// max |y| = rsqrt(...) * max |h w|, so the 8-bit scale needs no second one.
+// max |y| = rsqrt(...) * max |h w|, so the 8-bit scale needs no second one.  With many rows its CTAs spend
+// their time waiting for their loads (8192 x 5120, 8 bits out: 58 us, 75% of the measured copy rate).
+// rmsnorm_ring_kernel, for those: persistent CTAs whose next two rows are on their way into shared memory;
+// each thread copies what it will read itself, so the ring needs no barrier.
 __device__ __forceinline__ float2 block_sum_max(float2 v, float2* part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -286,6 +290,89 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
     }
 }
 
+constexpr int kNormStages = 3;
+
+__device__ __forceinline__ void unpack(const uint4& x, float (&h)[8]) {
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 f = bf16x2_to_f32x2(xs[j]);
+        h[2 * j] = f.x, h[2 * j + 1] = f.y;
+    }
+}
+
+constexpr int kNormPieces = 2;  // 16-byte pieces of a row a thread
+
+__global__ void __launch_bounds__(512, 2) rmsnorm_ring_kernel(const NormArgs a, int rows) {
+    extern __shared__ __align__(16) uint4 ring[];  // [kNormStages][x, residual][vecs]
+    __shared__ float2 part[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int sides = a.residual ? 2 : 1;
+    uint4 w[kNormPieces];
+#pragma unroll
+    for (int c = 0; c < kNormPieces; c++) {
+        const int i = threadIdx.x + c * blockDim.x;
+        w[c] = i < a.vecs ? a.weight[i] : make_uint4(0, 0, 0, 0);
+    }
+    int stage_in = 0, stage = 0;
+    auto issue = [&](int64_t row) {
+        if (row < rows) {
+            uint4* to = ring + stage_in * sides * a.vecs;
+#pragma unroll
+            for (int c = 0; c < kNormPieces; c++) {
+                const int i = threadIdx.x + c * blockDim.x;
+                if (i < a.vecs) {
+                    cp_async16(to + i, a.x + row * a.vecs + i);
+                    if (a.residual) cp_async16(to + a.vecs + i, a.residual + row * a.vecs + i);
+                }
+            }
+            stage_in = stage_in + 1 == kNormStages ? 0 : stage_in + 1;
+        }
+        cp_async_commit();
+    };
+    for (int k = 0; k < kNormStages - 1; k++) issue(blockIdx.x + static_cast<int64_t>(k) * gridDim.x);
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, flip ^= 1) {
+        cp_async_wait<kNormStages - 2>();
+        const uint4* from = ring + stage * sides * a.vecs;
+        stage = stage + 1 == kNormStages ? 0 : stage + 1;
+        float h[kNormPieces][8];
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < kNormPieces; c++) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i >= a.vecs) continue;
+            unpack(from[i], h[c]);
+            float v[8];
+            if (a.residual) {
+                unpack(from[a.vecs + i], v);
+#pragma unroll
+                for (int j = 0; j < 8; j++) h[c][j] += v[j];
+            }
+            unpack(w[c], v);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                acc.x = fmaf(h[c][j], h[c][j], acc.x);
+                if (a.y8) acc.y = fmaxf(acc.y, fabsf(h[c][j] * v[j]));
+            }
+        }
+        issue(row + static_cast<int64_t>(kNormStages - 1) * gridDim.x);
+        acc = block_sum_max(acc, part[flip]);
+        const float rstd = 1.0f / sqrtf(acc.x * a.inv_h + a.eps);
+        const float scale = acc.y * rstd / kFp8Max, inv_scale = scale > 0.0f ? 1.0f / scale : 0.0f;
+        if (a.y8 && threadIdx.x == 0) a.y8_scales[row] = scale;
+#pragma unroll
+        for (int c = 0; c < kNormPieces; c++) {
+            const int i = threadIdx.x + c * blockDim.x;
+            if (i >= a.vecs) continue;
+            float v[8];
+            unpack(w[c], v);
+            store_out(a, row * a.vecs + i, h[c], v, rstd, inv_scale);
+        }
+    }
+}
+
 cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
     attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr->val.programmaticStreamSerializationAllowed = 1;
@@ -332,6 +419,29 @@ cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const ui
     a.vecs = static_cast<int>(H / 8);
     a.inv_h = static_cast<float>(1.0 / static_cast<double>(H));
     a.eps = eps;
+    // Many rows of 2048 to 8192 values: the ring (8192 x 5120, 8 bits out: 48 us, without it 58; 4096 x 6144: 35
+    // and 40; narrower rows gain nothing, 32768 x 1024: 46 and 40).
+    if (T > 4 * num_sms && a.vecs > 256 && a.vecs <= 512 * kNormPieces) {
+        static std::once_flag attr_once[64];  // once per device
+        int dev = 0;
+        cudaGetDevice(&dev);
+        cudaError_t attr_err = cudaSuccess;
+        std::call_once(attr_once[dev & 63], [&] {
+            attr_err = cudaFuncSetAttribute(rmsnorm_ring_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kNormStages * 2 * 512 * kNormPieces * 16);
+        });
+        if (attr_err != cudaSuccess) return attr_err;
+        const int ring_bytes = kNormStages * (residual ? 2 : 1) * a.vecs * 16;
+        const int threads = ((a.vecs + kNormPieces - 1) / kNormPieces + 31) / 32 * 32;
+        int per_sm = 224 * 1024 / (ring_bytes + 2048);
+        if (per_sm > 1024 / threads) per_sm = 1024 / threads;  // 64 registers a thread
+        int64_t grid = static_cast<int64_t>(num_sms) * per_sm;
+        if (grid > T) grid = T;
+        cudaLaunchAttribute attr;
+        cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(grid)), threads, stream, &attr);
+        cfg.dynamicSmemBytes = ring_bytes;
+        return cudaLaunchKernelEx(&cfg, rmsnorm_ring_kernel, a, static_cast<int>(T));
+    }
     // Few rows: as many threads as the row has pieces.  Many rows: up to four pieces a thread, which
     // leaves room for more rows an SM.
     const int want = T <= 2 * num_sms ? 1024 : 256;
