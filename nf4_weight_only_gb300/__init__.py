@@ -8,6 +8,7 @@ torch tensors (device memory and streams) into the C calls of the same names and
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -262,6 +263,9 @@ def nf4_check_device_error() -> int:
 # ---------------------------------------------------------------------------------------------
 # Operators around the linears of a decoder layer
 # ---------------------------------------------------------------------------------------------
+# (torch.cuda.current_stream() builds a stream object, about a microsecond)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
 KV_FORMATS = {"bf16": 0, "fp8": 1, "nf4": 2}
 
 
@@ -274,18 +278,18 @@ class _KvCacheStruct(ctypes.Structure):
 
 def _expect(t: torch.Tensor, name: str, dtype, shape) -> int:
     """The address of a contiguous CUDA tensor of exactly this type and shape (or ValueError)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: want a CUDA tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: want a CUDA tensor")
 
 
 def _current(stream) -> int:
     """The raw handle of `stream`, or of the current device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -381,16 +385,16 @@ def nf4_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tens
                          stream=None) -> None:
     """out[b, h] = attention of q bf16 [B, q_heads, head_dim] over the cache's places of each sequence:
     page_table int32 [B, max_pages], lengths int32 [B]; scale defaults to head_dim ** -0.5."""
-    b, q_heads, d = q.shape
+    shape, max_pages, size = q.shape, page_table.shape[-1], workspace.numel()
+    b, q_heads, d = shape
     if d != cache.head_dim:
         raise ValueError(f"q: head_dim {d}, the cache has {cache.head_dim}")
-    shape, max_pages = q.shape, page_table.shape[-1]
     _check(load().nf4_attention_decode(
         cache._address, _expect(q, "q", torch.bfloat16, shape),
         _expect(page_table, "page_table", torch.int32, (b, max_pages)), max_pages,
         _expect(lengths, "lengths", torch.int32, (b,)), b, q_heads, d ** -0.5 if scale is None else scale, window,
-        _expect(out, "out", torch.bfloat16, shape), _expect(workspace, "workspace", torch.uint8, workspace.shape),
-        workspace.numel(), _current(stream)), "nf4_attention_decode")
+        _expect(out, "out", torch.bfloat16, shape), _expect(workspace, "workspace", torch.uint8, (size,)), size,
+        _current(stream)), "nf4_attention_decode")
 
 
 def nf4_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -404,21 +408,26 @@ def nf4_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: to
         raise ValueError("q and k are both None")
     t, _, d = one.shape
     axes, pairs = positions.shape[0], inv_freq.shape[0]
-    sections = [pairs] if sections is None else sections
-    if len(sections) != axes:
+    counts = _section_counts((pairs,) if sections is None else tuple(sections))
+    if len(counts) != axes:
         raise ValueError(f"sections: want one count for each of the {axes} axes")
-    side = []
-    for name, x, o in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            side.append((0, 0, 0))
-        else:
-            shape = (t, x.shape[1], d)
-            side.append((_expect(x, name, torch.bfloat16, shape), x.shape[1],
-                         _expect(o, name + "_out", torch.bfloat16, shape)))
-    (pq, hq, pqo), (pk, hk, pko) = side
-    _check(load().nf4_rope(pq, hq, pk, hk, t, d, _expect(positions, "positions", torch.int32, (axes, t)), axes,
-                           (ctypes.c_int32 * axes)(*sections), _expect(inv_freq, "inv_freq", torch.float32, (pairs,)),
-                           2 * pairs, int(interleaved), magnitude, pqo, pko, _current(stream)), "nf4_rope")
+    bf16 = torch.bfloat16
+    pq = hq = pqo = pk = hk = pko = 0
+    if q is not None:
+        hq = q.shape[1]
+        pq, pqo = _expect(q, "q", bf16, (t, hq, d)), _expect(q_out, "q_out", bf16, (t, hq, d))
+    if k is not None:
+        hk = k.shape[1]
+        pk, pko = _expect(k, "k", bf16, (t, hk, d)), _expect(k_out, "k_out", bf16, (t, hk, d))
+    _check(load().nf4_rope(pq, hq, pk, hk, t, d, _expect(positions, "positions", torch.int32, (axes, t)), axes, counts,
+                           _expect(inv_freq, "inv_freq", torch.float32, (pairs,)), 2 * pairs, int(interleaved),
+                           magnitude, pqo, pko, _current(stream)), "nf4_rope")
+
+
+@functools.lru_cache(maxsize=64)
+def _section_counts(sections):
+    """The counts as the host array nf4_rope reads."""
+    return (ctypes.c_int32 * len(sections))(*sections)
 
 
 def nf4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
@@ -426,16 +435,15 @@ def nf4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
                 y8: Optional[torch.Tensor] = None, y8_scales: Optional[torch.Tensor] = None, stream=None) -> None:
     """Norm of x (+ residual) bf16 [T, H] into y bf16 and / or y8 float8_e4m3fn with y8_scales fp32 [T];
     residual_out receives the sum."""
-    t, h = x.shape
     bf16, shape = torch.bfloat16, x.shape
-
-    def at(v, name, dtype, want):
-        return None if v is None else _expect(v, name, dtype, want)
-
-    _check(load().nf4_rmsnorm(_expect(x, "x", bf16, shape), at(residual, "residual", bf16, shape),
+    t, h = shape
+    _check(load().nf4_rmsnorm(_expect(x, "x", bf16, shape),
+                              None if residual is None else _expect(residual, "residual", bf16, shape),
                               _expect(weight, "weight", bf16, (h,)), t, h, eps,
-                              at(residual_out, "residual_out", bf16, shape), at(y, "y", bf16, shape),
-                              at(y8, "y8", torch.float8_e4m3fn, shape), at(y8_scales, "y8_scales", torch.float32, (t,)),
+                              None if residual_out is None else _expect(residual_out, "residual_out", bf16, shape),
+                              None if y is None else _expect(y, "y", bf16, shape),
+                              None if y8 is None else _expect(y8, "y8", torch.float8_e4m3fn, shape),
+                              None if y8_scales is None else _expect(y8_scales, "y8_scales", torch.float32, (t,)),
                               _current(stream)), "nf4_rmsnorm")
 
 

@@ -755,7 +755,7 @@ __device__ __forceinline__ uint32_t count_pieces(const Units& units, int B, uint
 // 2 kLongUnits units a warp to do, else up to four, taken by ticket, since the SMs' shares of the memory's
 // rate differ by 20% (one bf16 sequence of 131071 keys and 8 kv heads: 102 us; four pieces whatever their
 // length, 110; equal runs laid end to end, 118).  Rounding up the pieces of each segment must not start
-// another round, so `cut` grows until they fit (bisection), unless the segments alone fill the rounds.
+// another round, so `cut` grows until they fit, unless the segments alone fill the rounds.
 // LINE: where decoding, not the memory, bounds the SM (NF4), SMs are equally fast, and long segments (8 units
 // a warp on average) are cut by line: the same work for every worker (32 sequences up to 16384: 89 us;
 // by segment 95), which shorter ones would pay for with a start and a join for each (64 sequences up
@@ -802,18 +802,28 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     p.count = count_pieces(units, B, segs, low, lane);
     const uint32_t most = rounds * p.workers;
     if (p.count > most && segments <= most / 2) {
-        // at twice the cut and a unit, total / cut + segments <= most
+        // at twice the cut and a unit they fit: total / cut + segments <= most
         uint32_t high = 2 * low + 1;
-        p.count = 0;
-        while (high - low > 1 + (low >> 5)) {
-            const uint32_t mid = low + (high - low) / 2, at_mid = count_pieces(units, B, segs, mid, lane);
-            if (at_mid > most)
-                low = mid;
-            else
-                high = mid, p.count = at_mid;
+        if (B <= 32) {  // lane i tries low + i low / 32
+            // (ceilings in floating point: a cut that is off by one costs nothing but balance)
+            const uint32_t tried = low + (low * (lane + 1) + 31) / 32, mine = lane < B ? units(lane) : 0;
+            const float inverse = 1.0f / static_cast<float>(tried);
+            float pieces = 0.0f;
+            for (int b = 0; b < B; b++)
+                pieces += ceilf(static_cast<float>(__shfl_sync(0xFFFFFFFFu, mine, b)) * inverse);
+            const uint32_t fits = __ballot_sync(0xFFFFFFFFu, pieces * segs <= static_cast<float>(most));
+            if (fits) high = __shfl_sync(0xFFFFFFFFu, tried, __ffs(fits) - 1);
+        } else {  // bisection
+            while (high - low > 1 + (low >> 5)) {
+                const uint32_t mid = low + (high - low) / 2;
+                if (count_pieces(units, B, segs, mid, lane) > most)
+                    low = mid;
+                else
+                    high = mid;
+            }
         }
         p.cut = high;
-        if (p.count == 0) p.count = count_pieces(units, B, segs, high, lane);
+        p.count = count_pieces(units, B, segs, high, lane);
     }
     return p;
 }
