@@ -120,13 +120,28 @@ __device__ __forceinline__ uint32_t lds_table(uint32_t a) {
 }
 
 // B bytes (4, 8 or 16) global -> shared; B source bytes are read, or none and zeros written.
+// policy: of the L2 lines that 16-byte copies bring.
 template <int B>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live, uint64_t policy) {
     const uint32_t n = live ? B : 0;
     if (B == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(n),
+                     "l"(policy)
+                     : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(B) : "memory");
+}
+
+// What a long call reads of the cache is read once and leaves the L2 (129 MB) first: partial results, page tables
+// and the next kernels' data stay (64 sequences up to 8192, fp8: 110 -> 108 us; one of 131071: 52 -> 50).  A
+// short call's may stay: it may still be there when the layer comes round again (8 ragged sequences, fp8, 23 MB:
+// 12.3 -> 11.7 us).
+constexpr int64_t kStreamBytes = 32 << 20;
+__device__ __forceinline__ uint64_t l2_policy(bool stream) {
+    uint64_t first, normal;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(normal));
+    return stream ? first : normal;
 }
 
 // The NF4 table in fp16, times kTableUnit.  A table rounded entry by entry has a mean error of up to
@@ -224,7 +239,8 @@ __device__ __forceinline__ uint32_t piece_at(int row, int p) {
 // place: vector index of the block's first key.  lo and hi: its live keys (ALL: every one);
 // dead ones are filled with zeros so that nothing non-finite meets a weight of 0.
 template <int FMT, int D, int NT, bool ALL>
-__device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+__device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane,
+                                           uint64_t policy) {
     using S = Shape<FMT, D, NT>;
     const uint32_t kb = buf, vb = buf + 16 * S::VB, sb = buf + 32 * S::VB;
     const uint8_t* k = c.k + place * S::VB;
@@ -234,8 +250,8 @@ __device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64
 #pragma unroll
     for (int j = 0; j < P / 2; j++) {
         const int n = j * 32 + lane, key = n / P, p = n % P;
-        cp_async<16>(kb + piece_at<FMT, D, false>(key, p), k + n * 16, live(key));
-        cp_async<16>(vb + piece_at<FMT, D, true>(key, p), v + n * 16, live(key));
+        cp_async<16>(kb + piece_at<FMT, D, false>(key, p), k + n * 16, live(key), policy);
+        cp_async<16>(vb + piece_at<FMT, D, true>(key, p), v + n * 16, live(key), policy);
     }
     if (S::SB) {
         constexpr int SK = S::SB ? S::SB / 16 : 1;  // scale bytes of a key
@@ -247,7 +263,7 @@ __device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64
             if (o < 2 * S::SB) {
                 const int at = o < S::SB ? o : o - S::SB;
                 const bool on = live(at / SK) || live((at + 3) / SK);
-                cp_async<4>(sb + o, (o < S::SB ? ks : vs) + at, on);
+                cp_async<4>(sb + o, (o < S::SB ? ks : vs) + at, on, policy);
             }
         }
     }
@@ -255,12 +271,13 @@ __device__ __forceinline__ void copy_block(const KvCache& c, uint32_t buf, int64
 
 // A block that may have nothing to read (place < 0: zeros) or dead keys.
 template <int FMT, int D, int NT>
-__device__ __forceinline__ void copy_edge_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane) {
+__device__ __forceinline__ void copy_edge_block(const KvCache& c, uint32_t buf, int64_t place, int lo, int hi, int lane,
+                                                uint64_t policy) {
     if (place < 0) {
         for (int i = lane * 4; i < Shape<FMT, D, NT>::kBlock; i += 128)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(buf + i), "r"(0) : "memory");
     } else {
-        copy_block<FMT, D, NT, false>(c, buf, place, lo, hi, lane);
+        copy_block<FMT, D, NT, false>(c, buf, place, lo, hi, lane, policy);
     }
 }
 
@@ -661,43 +678,49 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
 }
 
 // Four dims (column i) of one head, joined over `n` results in their order: part(j) is result j, [heads][D]
-// sums of weighted values, then [heads] maxima and [heads] sums of weights at ml(j).  Eight results are
-// loaded at a time, so the latency of the memory that holds them is met once for each eight.
+// sums of weighted values, then [heads] maxima and [heads] sums of weights at ml(j).
 struct Joined {
     float4 o;
     float top, l;
 };
-template <int D, bool GLOBAL, bool ML_SHARED = !GLOBAL, typename Part, typename Ml>
+template <int N>
+__device__ __forceinline__ void join_some(Joined& r, const float4 (&v)[N], const float (&m)[N], const float (&l)[N]) {
+    float top = r.top;
+#pragma unroll
+    for (int j = 0; j < N; j++) top = fmaxf(top, m[j]);
+    const float f0 = exp2_approx(r.top - top);
+    r.top = top;
+    r.l *= f0, r.o.x *= f0, r.o.y *= f0, r.o.z *= f0, r.o.w *= f0;
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+        const float f = exp2_approx(m[j] - top);
+        r.l = fmaf(f, l[j], r.l);
+        r.o.x = fmaf(f, v[j].x, r.o.x), r.o.y = fmaf(f, v[j].y, r.o.y);
+        r.o.z = fmaf(f, v[j].z, r.o.z), r.o.w = fmaf(f, v[j].w, r.o.w);
+    }
+}
+// N results are loaded at a time.  R_SHARED, M_SHARED: the results, and their maxima and sums, are in shared
+// memory.
+template <int D, int N, bool R_SHARED, bool M_SHARED, typename Part, typename Ml>
 __device__ __forceinline__ Joined join(const Part& part, const Ml& ml, int n, int heads, int i) {
-    constexpr int N = GLOBAL ? 8 : 4;
     const int h = i / (D / 4);
     Joined r{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -3e38f, 0.0f};
+#pragma unroll 1
     for (int j0 = 0; j0 < n; j0 += N) {
         float4 v[N];
-        float m[N], l[N], top = r.top;
+        float m[N], l[N];
 #pragma unroll
         for (int j = 0; j < N; j++) {
             v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), m[j] = -3e38f, l[j] = 0.0f;
             if (j0 + j < n) {
                 const float4* p = reinterpret_cast<const float4*>(part(j0 + j)) + i;
                 const float* q = ml(j0 + j) + h;
-                v[j] = GLOBAL ? __ldcg(p) : *p;
-                m[j] = ML_SHARED ? *q : __ldcg(q);
-                l[j] = ML_SHARED ? q[heads] : __ldcg(q + heads);
+                v[j] = R_SHARED ? *p : __ldcg(p);
+                m[j] = M_SHARED ? *q : __ldcg(q);
+                l[j] = M_SHARED ? q[heads] : __ldcg(q + heads);
             }
         }
-#pragma unroll
-        for (int j = 0; j < N; j++) top = fmaxf(top, m[j]);
-        const float f0 = exp2_approx(r.top - top);
-        r.top = top;
-        r.l *= f0, r.o.x *= f0, r.o.y *= f0, r.o.z *= f0, r.o.w *= f0;
-#pragma unroll
-        for (int j = 0; j < N; j++) {
-            const float f = exp2_approx(m[j] - top);
-            r.l = fmaf(f, l[j], r.l);
-            r.o.x = fmaf(f, v[j].x, r.o.x), r.o.y = fmaf(f, v[j].y, r.o.y);
-            r.o.z = fmaf(f, v[j].z, r.o.z), r.o.w = fmaf(f, v[j].w, r.o.w);
-        }
+        join_some(r, v, m, l);
     }
     return r;
 }
@@ -738,7 +761,7 @@ __device__ __forceinline__ uint32_t divide_up(uint64_t a, uint32_t d) {  // at m
     return static_cast<uint32_t>(q < (1u << 30) ? q : (1u << 30));
 }
 
-// units(b): of sequence b.  The whole warp calls it.
+// units(b): of sequence b, asked by lane b % 32.  The whole warp calls it.
 template <typename Units>
 __device__ __forceinline__ uint32_t count_pieces(const Units& units, int B, uint32_t segs, uint32_t cut, int lane) {
     uint32_t p = 0;
@@ -845,11 +868,42 @@ struct Place {
     uint32_t pieces_before;  // by segment: pieces of those sequences (one segment each)
 };
 
-// The sequence in which number `id` falls (there is one), searched from `at` on: of the pieces of one segment
-// of each sequence, ceil(n / cut) for n units, or (cut = 0) of its units.  The whole warp calls it.
+// What precedes each 32nd sequence (units and pieces of one segment each), for as many as kBlocks of them.
+constexpr int kBlocks = 64;
+struct Before {
+    uint32_t units, pieces;
+};
+constexpr int kUnitsKept = 4096;  // sequences whose units are kept while the plan is made
+
+// The whole warp calls it.
 template <typename Units>
-__device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, uint32_t id, uint32_t cut, int lane) {
+__device__ __forceinline__ void make_blocks(const Units& units, int B, uint32_t cut, int lane, Before* blocks) {
+    Before sum{0, 0};
+    for (int i = 0; i * 32 < B; i++) {
+        if (lane == 0) blocks[i] = sum;
+        const int b = i * 32 + lane;
+        const uint32_t n = b < B ? units(b) : 0;
+        sum.units += __reduce_add_sync(0xFFFFFFFFu, n);
+        sum.pieces += __reduce_add_sync(0xFFFFFFFFu, cut ? (n + cut - 1) / cut : 0);
+    }
+}
+
+// The sequence in which number `id` falls (there is one): of the pieces of one segment of each sequence,
+// ceil(n / cut) for n units, or (cut = 0) of its units.  Searched from its block of 32 on, or, with more
+// sequences than the blocks cover, from the last place found.  The whole warp calls it.
+template <typename Units>
+__device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, const Before* blocks, uint32_t id,
+                                        uint32_t cut, int lane) {
     if (B == 1) return at;
+    if (B > 32 && B <= 32 * kBlocks) {
+        int block = -1;  // the last one that nothing past `id` precedes
+#pragma unroll
+        for (int i = 0; i < kBlocks; i += 32) {
+            const bool reached = (i + lane) * 32 < B && (cut ? blocks[i + lane].pieces : blocks[i + lane].units) <= id;
+            block += __popc(__ballot_sync(0xFFFFFFFFu, reached));
+        }
+        at = Place{block * 32, blocks[block].units, blocks[block].pieces};
+    }
     for (;;) {
         const int b = at.b + lane;
         const uint32_t n = b < B ? units_of(b) : 0, p = cut ? (n + cut - 1) / cut : 0;
@@ -882,6 +936,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     __shared__ uint32_t s_word[S::W][2];            // a worker's next piece; whether it joins
     __shared__ float s_ml[S::W * 2 * NT * 8];       // the maxima and sums of the warps
     __shared__ Plan s_plan;
+    __shared__ Before s_blocks[kBlocks];
     const int lane = threadIdx.x % 32;
     const uint32_t base = smem_u32(smem);
     if (FMT == kKvNf4) {
@@ -902,14 +957,23 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
 
     const uint32_t segs = a.c.kv_heads * a.chunks;  // segments of a sequence
     auto units_of = [&](int b) { return static_cast<uint32_t>(span_of(a, b).units<KEYS>()); };
+    // the lengths are read once: one a lane of the planning warp, or by everyone into what will be the rings
+    uint32_t* s_units = reinterpret_cast<uint32_t*>(smem);
+    if (a.B > 32) {
+        for (int b = threadIdx.x; b < a.B && b < kUnitsKept; b += S::W * 32) s_units[b] = units_of(b);
+        __syncthreads();
+    }
     if (threadIdx.x < 32) {
-        const uint32_t mine = lane < a.B ? units_of(lane) : 0;  // read once
-        const Plan p = make_plan<S::W, FMT == kKvNf4>([&](int b) { return b == lane ? mine : units_of(b); }, a.B, segs, lane);
+        const uint32_t mine = a.B <= 32 && lane < a.B ? units_of(lane) : 0;
+        auto kept = [&](int b) { return a.B <= 32 ? mine : b < kUnitsKept ? s_units[b] : units_of(b); };
+        const Plan p = make_plan<S::W, FMT == kKvNf4>(kept, a.B, segs, lane);
         if (lane == 0) s_plan = p;
+        if (a.B > 32 && a.B <= 32 * kBlocks) make_blocks(kept, a.B, p.cut, lane, s_blocks);
     }
     __syncthreads();
     // (the plan is read where it is needed: it does not live in registers)
     const volatile Plan& plan = s_plan;
+    const uint64_t policy = l2_policy(plan.total > kStreamBytes / static_cast<uint64_t>(S::kStage));
     const int wg = plan.warps, threads = wg * 32;
     const int group = threadIdx.x / threads, tid = threadIdx.x - group * threads, warp = tid / 32;
 
@@ -929,10 +993,10 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             if (by_line) {
                 x = cell_start(plan, id), stop = cell_start(plan, id + 1);
                 if (x == stop) break;
-                at = locate(units_of, a.B, at, x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / segs
+                at = locate(units_of, a.B, at, s_blocks, x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / segs
                                                                        : static_cast<uint32_t>(x / segs), 0, lane);
             } else {
-                at = locate(units_of, a.B, at, id / segs, cut, lane);
+                at = locate(units_of, a.B, at, s_blocks, id / segs, cut, lane);
             }
             if (tid == 0) next = plan.count > plan.workers ? atomicAdd(a.tickets, 1u) + plan.workers : 0xFFFFFFFFu;
         }
@@ -1003,13 +1067,13 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 if (fast) {
 #pragma unroll
                     for (int b = 0; b < KS; b++)
-                        copy_block<FMT, D, NT, true>(a.c, in_buf + b * S::kBlock, place[b], 0, 16, lane);
+                        copy_block<FMT, D, NT, true>(a.c, in_buf + b * S::kBlock, place[b], 0, 16, lane, policy);
                 } else {
 #pragma unroll 1
                     for (int b = 0; b < KS; b++) {
                         const int64_t at_b = KS > 1 && b ? place[KS - 1] : place[0];
                         bad |= at_b == -1 ? 1u << b : 0u;
-                        copy_edge_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, at_b, lo - 16 * b, hi - 16 * b, lane);
+                        copy_edge_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, at_b, lo - 16 * b, hi - 16 * b, lane, policy);
                     }
                 }
                 in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
@@ -1033,7 +1097,31 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         __syncwarp();  // the warp's ring is drained: its memory takes the warp's result
 
         const int joiners = min(wg, u1 - u0);  // warps that had a unit
-        if (warp < joiners) {
+        const bool whole = u0 == 0 && u1 == static_cast<int>(n);
+        const bool alone = whole && joiners == 1;  // nothing to join: the warp writes the output
+        if (alone && warp == 0) {
+            const int g = lane >> 2, t = lane & 3;
+            constexpr int RUN = v_run<FMT, D>();
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const int h = nt * 8 + 2 * t + j;
+                    float l = s.l[nt][j];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+                    const float back = FMT == kKvBf16 ? 1.0f : (FMT == kKvNf4 ? 1.0f / kTableUnit : 1.0f) / s.vn;
+                    const float f = l > 0.0f ? back / l : 0.0f;
+                    if (h < heads) {
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) {
+                            const int dim = (2 * i) / RUN * (8 * RUN) + g * RUN + (2 * i) % RUN;
+                            *reinterpret_cast<uint32_t*>(a.out + (row0 + h) * D + dim) =
+                                f32x2_to_bf16x2(s.o[nt][i][j] * f, s.o[nt][i][j + 2] * f);
+                        }
+                    }
+                }
+        } else if (warp < joiners) {
             float* dst = area(warp);
             const int g = lane >> 2, t = lane & 3;
             const float back = FMT == kKvBf16 ? 1.0f : (FMT == kKvNf4 ? 1.0f / kTableUnit : 1.0f) / s.vn;
@@ -1068,7 +1156,6 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         // The slots of a segment's pieces.  By line: two a cell, for the piece that begins a segment and for one
         // that goes on with it.  By segment: segments that are cut have more than `cut` units, so the runs of
         // slots from twice their first unit's quotient are disjoint.
-        const bool whole = u0 == 0 && u1 == static_cast<int>(n);
         int slot0 = 0;
         if (!whole) {
             const uint64_t first_unit = static_cast<uint64_t>(at.units_before) * segs + static_cast<uint64_t>(seg) * n;
@@ -1084,8 +1171,8 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         }
         auto slot_index = [&](int i) { return slot0 + (by_line ? 2 * i - (i > 0) : i); };
         auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot_index(i)) * a.slot_floats; };
-        for (int i = tid; i < columns; i += threads) {
-            const Joined r = join<D, false>(
+        for (int i = alone ? columns : tid; i < columns; i += threads) {
+            const Joined r = join<D, 4, true, true>(
                 area, [&](int w) { return s_ml + (group * wg + w) * (2 * NT * 8); }, joiners, heads, i);
             if (whole)
                 out[i] = normalised(r);
@@ -1105,8 +1192,8 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             auto piece = [&](int j) { return slot(from + j * step); };
             if (last && count <= 8) {  // everything in one round of loads
                 for (int i = tid; i < columns; i += threads)
-                    out[i] = normalised(
-                        join<D, true>(piece, [&](int j) { return piece(j) + heads * D; }, count, heads, i));
+                    out[i] = normalised(join<D, 8, false, false>(
+                        piece, [&](int j) { return piece(j) + heads * D; }, count, heads, i));
                 return true;
             }
             // the maxima and sums to shared memory first: one round for all of them, not one for each eight
@@ -1116,9 +1203,9 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 ml[i] = __ldcg(piece(j) + heads * D + (i - j * 2 * heads));
             }
             worker_barrier(group, wg);
-            auto ml_of = [&](int j) { return ml + j * 2 * heads; };
             for (int i = tid; i < columns; i += threads) {
-                const Joined r = join<D, true, true>(piece, ml_of, count, heads, i);
+                const Joined r =
+                    join<D, 8, false, true>(piece, [&](int j) { return ml + j * 2 * heads; }, count, heads, i);
                 if (last)
                     out[i] = normalised(r);
                 else  // (into the first of them: nobody but this thread reads its column, nor the sums again)
