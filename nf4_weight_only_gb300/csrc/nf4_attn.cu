@@ -771,13 +771,15 @@ __device__ __forceinline__ uint32_t count_pieces(const Units& units, int B, uint
 
 // A rule on the lengths alone, the same in every CTA (one warp works it out).  W warps a CTA; a worker is
 // W / 2 of them, so that a CTA has one that streams while the other starts or joins a piece, except
-//  - all W, when there is at most a segment for each CTA and little to do: no second piece to overlap with;
+//  - all W, when there is at most a segment for each CTA and little to do (no second piece to overlap with), or
+//    a segment for eight CTAs (half as many partial results to join; one bf16 sequence of 131071 keys and 8
+//    heads: 92 us, 98 with halves);
 //  - fewer, when there are many segments too short to keep W / 2 warps busy.
 // Sequences of up to 8 units a warp are not cut: the join of partial results costs 3 us, about what these
 // units do.  The rest is cut by segment: one piece a worker where there are few segments and less than
 // 2 kLongUnits units a warp to do, else up to four, taken by ticket, since the SMs' shares of the memory's
-// rate differ by 20% (one bf16 sequence of 131071 keys and 8 kv heads: 102 us; four pieces whatever their
-// length, 110; equal runs laid end to end, 118).  Rounding up the pieces of each segment must not start
+// rate differ by 20% (one bf16 sequence of 131071 keys and 8 kv heads, in two: 102 us; in four, 110; in equal
+// runs laid end to end, 118).  Rounding up the pieces of each segment must not start
 // another round, so `cut` grows until they fit, unless the segments alone fill the rounds.
 // LINE: where decoding, not the memory, bounds the SM (NF4), SMs are equally fast, and long segments (8 units
 // a warp on average) are cut by line: the same work for every worker (32 sequences up to 16384: 89 us;
@@ -799,7 +801,8 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     Plan p;
     p.total = total;
     p.warps = W / 2;
-    if (segments <= gridDim.x && total <= static_cast<uint64_t>(8 * W) * gridDim.x) p.warps = W;
+    if (segments * 8 <= gridDim.x || (segments <= gridDim.x && total <= static_cast<uint64_t>(8 * W) * gridDim.x))
+        p.warps = W;
     while (p.warps > 1 && segments >= 2 * gridDim.x * (W / p.warps) && total < 4 * p.warps * segments) p.warps /= 2;
     p.workers = gridDim.x * (W / p.warps);
     if (longest <= 8 * p.warps) {
