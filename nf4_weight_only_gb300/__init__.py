@@ -9,6 +9,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -17,6 +19,8 @@ import torch
 from . import build as _build
 
 GROUP = 64
+# (torch.cuda.current_stream() builds a stream object, about a microsecond)
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 LIB_PATH = _build.LIB_PATH
 
 STATUS_NAMES = {0: "NF4_OK", 1: "NF4_ERR_NULL", 2: "NF4_ERR_SHAPE", 3: "NF4_ERR_ALIGN",
@@ -105,6 +109,23 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     if path is None:
         _lib = lib
     return lib
+
+
+_calls = None
+
+
+def _load_calls(lib: ctypes.CDLL) -> None:
+    """The compiled short way into `lib` for the calls of a decode loop (csrc/nf4_python.c)."""
+    global _calls
+    if not os.path.exists(_build.CALLS_PATH):
+        raise RuntimeError(f"{_build.CALLS_PATH} is missing: build it with nf4_weight_only_gb300.build.build()")
+    loader = importlib.machinery.ExtensionFileLoader("nf4_calls", _build.CALLS_PATH)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("nf4_calls", loader))
+    loader.exec_module(module)
+    functions = (lib.nf4_kv_append, lib.nf4_kv_read, lib.nf4_attention_decode, lib.nf4_rope, lib.nf4_rmsnorm)
+    module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in functions), torch.bfloat16, torch.float8_e4m3fn,
+                torch.float32, torch.int32, torch.int64, torch.uint8, _raw_stream, _current_device)
+    _calls = module
 
 
 def status_str(status: int) -> str:
@@ -263,9 +284,6 @@ def nf4_check_device_error() -> int:
 # ---------------------------------------------------------------------------------------------
 # Operators around the linears of a decoder layer
 # ---------------------------------------------------------------------------------------------
-# (torch.cuda.current_stream() builds a stream object, about a microsecond)
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
 KV_FORMATS = {"bf16": 0, "fp8": 1, "nf4": 2}
 
 
@@ -274,6 +292,14 @@ class _KvCacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+def _ready():
+    """The compiled calls.  Each returns a status, or None for tensors that it does not take: the wrappers then go
+    through their own checks, which say what is wrong."""
+    if _calls is None:
+        _load_calls(load())
+    return _calls
 
 
 def _expect(t: torch.Tensor, name: str, dtype, shape) -> int:
@@ -350,6 +376,9 @@ class KVCache:
 
 def nf4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
     """Write k, v bf16 [T, kv_heads, head_dim] at int64 slots [T] (page * page_size + offset; < 0: skip)."""
+    status = _ready().append(cache._address, cache.kv_heads, cache.head_dim, k, v, slots, stream)
+    if status is not None:
+        return _check(status, "nf4_kv_append")
     t = slots.shape[0]
     shape = (t, cache.kv_heads, cache.head_dim)
     _check(load().nf4_kv_append(cache._address, _expect(k, "k", torch.bfloat16, shape),
@@ -360,6 +389,9 @@ def nf4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch
 def nf4_kv_read(cache: KVCache, slots: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
                 stream=None) -> None:
     """Read int64 slots [T] back into k and / or v bf16 [T, kv_heads, head_dim]."""
+    status = _ready().read(cache._address, cache.kv_heads, cache.head_dim, slots, k, v, stream)
+    if status is not None:
+        return _check(status, "nf4_kv_read")
     t = slots.shape[0]
     shape = (t, cache.kv_heads, cache.head_dim)
     _check(load().nf4_kv_read(cache._address, _expect(slots, "slots", torch.int64, (t,)), t,
@@ -385,6 +417,10 @@ def nf4_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tens
                          stream=None) -> None:
     """out[b, h] = attention of q bf16 [B, q_heads, head_dim] over the cache's places of each sequence:
     page_table int32 [B, max_pages], lengths int32 [B]; scale defaults to head_dim ** -0.5."""
+    status = _ready().attention(cache._address, cache.head_dim, q, page_table, lengths, out, workspace, scale, window,
+                                stream)
+    if status is not None:
+        return _check(status, "nf4_attention_decode")
     shape, max_pages, size = q.shape, page_table.shape[-1], workspace.numel()
     b, q_heads, d = shape
     if d != cache.head_dim:
@@ -403,6 +439,9 @@ def nf4_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: to
     """Rotary positions on q [T, q_heads, D] and k [T, k_heads, D] (bf16; either may be None; the outputs
     may be the inputs): positions int32 [axes, T], inv_freq fp32 [rotary_dim / 2], `sections` the pairs of
     each axis (default: one axis)."""
+    status = _ready().rope(q, k, positions, inv_freq, q_out, k_out, sections, interleaved, magnitude, stream)
+    if status is not None:
+        return _check(status, "nf4_rope")
     one = q if q is not None else k
     if one is None:
         raise ValueError("q and k are both None")
@@ -435,6 +474,9 @@ def nf4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
                 y8: Optional[torch.Tensor] = None, y8_scales: Optional[torch.Tensor] = None, stream=None) -> None:
     """Norm of x (+ residual) bf16 [T, H] into y bf16 and / or y8 float8_e4m3fn with y8_scales fp32 [T];
     residual_out receives the sum."""
+    status = _ready().rmsnorm(x, weight, eps, residual, residual_out, y, y8, y8_scales, stream)
+    if status is not None:
+        return _check(status, "nf4_rmsnorm")
     bf16, shape = torch.bfloat16, x.shape
     t, h = shape
     _check(load().nf4_rmsnorm(_expect(x, "x", bf16, shape),

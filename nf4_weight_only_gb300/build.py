@@ -1,9 +1,11 @@
-"""Build libnf4.so (the CUDA kernels and the C ABI) in-tree for sm_103a with nvcc."""
+"""Build libnf4.so (the CUDA kernels and the C ABI) in-tree for sm_103a with nvcc, and the binding's compiled
+calls (csrc/nf4_python.c) with the host compiler."""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from typing import List
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,6 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libnf4.so")
+CALLS_PATH = os.path.join(BUILD_DIR, "nf4_calls.so")
 
 SOURCES = ["nf4_api.cu", "nf4_quant.cu", "nf4_gemv.cu", "nf4_ring.cu", "nf4_kv.cu", "nf4_attn.cu",
            "nf4_rows.cu"]
@@ -33,9 +36,9 @@ def _inputs() -> List[str]:
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -46,6 +49,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
     procs, objs = [], []
+    calls_tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "nf4_python.c"), "-lm", "-o", calls_tmp]
+    procs.append(("nf4_python.c", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -65,6 +72,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB_PATH)
+    os.replace(calls_tmp, CALLS_PATH)
     return LIB_PATH
 
 
