@@ -4,11 +4,19 @@
 //   S = K q^T [keys x heads],  p = 2^(S c - m),  O^T = V^T p^T [dims x heads],  l = sum p,
 // one pass over the cache with a running maximum m a head (c = scale log2 e); O / l at the end.  Both
 // products go through mma.sync m16n8k16 with the cache as the 16-row operand and the heads as the
-// eight columns: 128 bytes of bf16 cache feed one instruction, so the tensor work is far below what
+// eight columns: 512 bytes of bf16 cache feed one instruction, so the tensor work is far below what
 // the cache's bytes cost, and the fragments are read in an order that needs no rearrangement of the
 // cache: the dims of a product's k axis may be permuted at will (q is permuted alike), and so may the
-// keys.  tcgen05 wants 64 or 128 rows from shared memory in canonical tiles; here the rows are in
-// pages of 16 and more, quantised, and a tile would be used once, for eight columns.
+// keys.  tcgen05 takes 64 or 128 rows from shared or tensor memory in canonical tiles; here the rows are in
+// pages of 16 and more, quantised, a tile would be used once, for eight columns, and the tensor pipe is busy
+// for 12 to 20% of the time as it is.
+//
+// What bounds it, measured on GB300 (DRAM copy rate 6774 GB/s): with a bf16 cache the memory (64 sequences up to
+// 8192, 8 kv heads: 184 us, 97% of that rate) and, for one sequence of 131071, the SMs' unequal shares of it (93 us,
+// 85%); with fp8 the latency of a ring of two stages (109 us, 85%); with NF4 the decoding: 64 table lookups of
+// 81 shared-memory reads and 340 instructions for 16 keys, 53% of the issue slots (32 sequences up to 16384:
+// 83 us, 57%); short calls the chain of dependent loads (lengths, page table, data, partial results): 5 us
+// for one sequence of 128 tokens, 12 us for 8 of up to 4095.
 //
 // Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte
 // (two codes) indexes a table of fp16 pairs in shared memory (see kTableF16).  The scales are applied in
@@ -38,7 +46,7 @@ __device__ int g_attention_error;
 
 constexpr int kMaxWorkers = 320;      // of W / 2 warps
 constexpr int kRounds = 4;            // pieces a worker gets in long calls
-constexpr int kLongUnits = 16;        // units a warp up to which a call is one piece a worker
+constexpr int kLongUnits = 16;        // units a warp: a piece of a call that is cut into several a worker
 constexpr int kFanIn = 24;            // partial results joined at a time
 constexpr int kSlots = 2 * kMaxWorkers * kRounds + 2;  // partial results (see slot0)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -180,8 +188,10 @@ struct Shape {
     static constexpr int KS = FMT != kKvBf16 && NT == 1 && D <= 128 ? 2 : 1;
     static constexpr int kBlock = 32 * VB + 2 * SB;              // 16 keys, K and V
     static constexpr int kStage = KS * kBlock;
-    // Warps and stages: enough warps to issue the decoding (16 for the quantised formats where their
-    // registers allow it), and about 100 KB in flight an SM.
+    // Warps and stages.  bf16: 8 warps with 8 KB stages are 128 KB in flight an SM.  Decoding wants more warps, and
+    // registers: 12 warps at 168 (NF4, 32 sequences up to 16384: 95 us; 16 at 128 work the addresses out again
+    // for every unit: 107; 8: 130), except where a warp's state alone takes more (8 warps; NT = 2 at 12: 295 us
+    // against 250).
     static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : D == 256 || NT == 2 ? 8 : 12;
     static constexpr int kRingMost = FMT == kKvNf4 ? (W == 12 ? 8704 : 20480) : 230400 / W / 16 * 16;
     static constexpr int kStagesFit = kRingMost / kStage;
@@ -737,6 +747,14 @@ __device__ __forceinline__ void store_partial(float* slot, const Joined& r, int 
     }
 }
 
+// Counts up to `last` and wraps to 0; the old count.  Releases what this thread has seen (the worker's stores, by
+// the barrier before) and acquires what the others released.
+__device__ __forceinline__ uint32_t ticket_inc(uint32_t* at, uint32_t last) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(last) : "memory");
+    return old;
+}
+
 // Barrier of a worker's warps (barrier 0 is the CTA's).
 __device__ __forceinline__ void worker_barrier(int group, int warps) {
     if (warps == 1)
@@ -1184,12 +1202,8 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         }
         // joins `count` slots, `step` apart, once `tickets` says that all of them are there; whether it did
         auto join_slots = [&](uint32_t* ticket, int from, int step, int count, bool last) {
-            worker_barrier(group, wg);  // every thread's stores, then one fence and the ticket
-            if (tid == 0) {
-                __threadfence();
-                s_word[group][1] = atomicInc(ticket, count - 1) == static_cast<unsigned>(count - 1);
-                __threadfence();
-            }
+            worker_barrier(group, wg);  // every thread's stores come before the ticket, and its loads after it
+            if (tid == 0) s_word[group][1] = ticket_inc(ticket, count - 1) == static_cast<uint32_t>(count - 1);
             worker_barrier(group, wg);
             if (!s_word[group][1]) return false;
             auto piece = [&](int j) { return slot(from + j * step); };
@@ -1236,7 +1250,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     // the last worker leaves the tickets as it found them
     if (tid == 0 && plan.count > plan.workers) {
         const uint32_t last = plan.workers - 1;
-        if (atomicInc(a.tickets + 1, last) == last) a.tickets[0] = 0;
+        if (ticket_inc(a.tickets + 1, last) == last) a.tickets[0] = 0;
     }
 }
 
