@@ -34,6 +34,7 @@
 // cp.async stages and no barrier; their results are joined in shared memory.  The pieces of a segment leave
 // partial results in the workspace; the worker that finishes the last of them joins them in their
 // order (24 at a time, then the joined ones), so results do not depend on timing.
+#include <algorithm>
 #include <mutex>
 
 #include "nf4_kv.cuh"
@@ -960,14 +961,14 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     __shared__ Before s_blocks[kBlocks];
     const int lane = threadIdx.x % 32;
     const uint32_t base = smem_u32(smem);
-    if (FMT == kKvNf4) {
-        for (int i = threadIdx.x; i < 256 * 32; i += S::W * 32) {
+    // the table, by all warps but the one that plans, and before the previous kernel has finished
+    if (FMT == kKvNf4 && threadIdx.x >= 32) {
+        for (int i = threadIdx.x - 32; i < 256 * 32; i += S::W * 32 - 32) {
             const int v = i >> 5;
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(kTableAt + v * 256 + (i & 31) * 4),
                          "r"(pack_f16(kTableF16[v & 15], kTableF16[v >> 4]))
                          : "memory");
         }
-        __syncthreads();
     }
     pdl_launch_dependents();
     pdl_wait();
@@ -1268,10 +1269,12 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
                                         S::kSmem);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    // as many CTAs as SMs, or fewer where the longest possible sequences leave less than that to do
-    const int64_t most = a.B * static_cast<int64_t>(a.c.kv_heads) * a.chunks * ((a.max_pages * a.c.page_size + 16 * S::KS - 1) / (16 * S::KS));
-    int64_t grid = num_sms < kMaxWorkers / 2 ? num_sms : kMaxWorkers / 2;
-    if (grid > (most + S::W - 1) / S::W) grid = (most + S::W - 1) / S::W;
+    // as many CTAs as SMs, or fewer where there are fewer segments and the longest possible sequences leave less to do
+    const int64_t segments = static_cast<int64_t>(a.B) * a.c.kv_heads * a.chunks;
+    const int64_t units = segments * ((a.max_pages * a.c.page_size + 16 * S::KS - 1) / (16 * S::KS));
+    const int64_t useful = std::max(segments, (units + S::W - 1) / S::W);
+    int64_t grid = std::min(num_sms, kMaxWorkers / 2);
+    if (grid > useful) grid = useful;
     if (grid < 1) grid = 1;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
