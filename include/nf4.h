@@ -303,7 +303,7 @@ nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t 
  * is in page page_table[b][j / page_size].  A sequence with nothing to attend to gives zeros.  The
  * new token's own key and value are in the cache before the call.
  *   q           in   bf16 bits [B][q_heads][head_dim]; q_heads a multiple of kv_heads
- *   page_table  in   int32 [B][max_pages]; entries past a sequence's length are not read
+ *   page_table  in   int32 [B][max_pages]; entries past a sequence's length do not matter
  *   lengths     in   int32 [B]; a negative length counts as 0.  A length past max_pages * page_size is
  *                    cut there, and a needed page outside [0, pages) is left out of the sum; both
  *                    record code 43 in the device error word.

@@ -843,33 +843,30 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     // (the second bound keeps the workspace's slots enough when workers of few warps are many)
     uint32_t low = max(divide_up(total, rounds * p.workers), divide_up(total, kRounds * gridDim.x * 2));
     low = max(low, 2 * p.warps);
+    const uint32_t most = rounds * p.workers;
+    if (segments <= most / 2 && B <= 32) {
+        // lane i tries low + i low / 31; the last one fits: total / cut + segments <= most
+        // (ceilings in floating point: a cut that is off by one costs nothing but balance)
+        const uint32_t tried = low + (low * lane + 30) / 31, mine = lane < B ? units(lane) : 0;
+        const float inverse = 1.0f / static_cast<float>(tried);
+        float pieces = 0.0f;
+        for (int b = 0; b < B; b++)
+            pieces += ceilf(static_cast<float>(__shfl_sync(0xFFFFFFFFu, mine, b)) * inverse);
+        const uint32_t fits = __ballot_sync(0xFFFFFFFFu, pieces * segs <= static_cast<float>(most));
+        low = __shfl_sync(0xFFFFFFFFu, tried, fits ? __ffs(fits) - 1 : 31);
+    } else if (segments <= most / 2 && count_pieces(units, B, segs, low, lane) > most) {
+        uint32_t high = 2 * low + 1;  // fits
+        while (high - low > 1 + (low >> 5)) {
+            const uint32_t mid = low + (high - low) / 2;
+            if (count_pieces(units, B, segs, mid, lane) > most)
+                low = mid;
+            else
+                high = mid;
+        }
+        low = high;
+    }
     p.cut = low;
     p.count = count_pieces(units, B, segs, low, lane);
-    const uint32_t most = rounds * p.workers;
-    if (p.count > most && segments <= most / 2) {
-        // at twice the cut and a unit they fit: total / cut + segments <= most
-        uint32_t high = 2 * low + 1;
-        if (B <= 32) {  // lane i tries low + i low / 32
-            // (ceilings in floating point: a cut that is off by one costs nothing but balance)
-            const uint32_t tried = low + (low * (lane + 1) + 31) / 32, mine = lane < B ? units(lane) : 0;
-            const float inverse = 1.0f / static_cast<float>(tried);
-            float pieces = 0.0f;
-            for (int b = 0; b < B; b++)
-                pieces += ceilf(static_cast<float>(__shfl_sync(0xFFFFFFFFu, mine, b)) * inverse);
-            const uint32_t fits = __ballot_sync(0xFFFFFFFFu, pieces * segs <= static_cast<float>(most));
-            if (fits) high = __shfl_sync(0xFFFFFFFFu, tried, __ffs(fits) - 1);
-        } else {  // bisection
-            while (high - low > 1 + (low >> 5)) {
-                const uint32_t mid = low + (high - low) / 2;
-                if (count_pieces(units, B, segs, mid, lane) > most)
-                    low = mid;
-                else
-                    high = mid;
-            }
-        }
-        p.cut = high;
-        p.count = count_pieces(units, B, segs, high, lane);
-    }
     return p;
 }
 
