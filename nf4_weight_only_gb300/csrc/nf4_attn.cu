@@ -181,6 +181,7 @@ constexpr uint32_t kTableAt = 65536, kTableEnd = 131072;
 template <int FMT, int D, int NT>
 struct Shape {
     static constexpr bool kBf = FMT == kKvBf16;
+    static constexpr bool kLine = FMT != kKvFp8;                 // long segments are cut by line (see make_plan)
     static constexpr int VB = kv_vector_bytes(FMT, D);           // bytes of a vector
     static constexpr int SB = 16 * kv_scale_bytes(FMT, D);       // bytes of 16 keys' scales of one side
     static constexpr int GR = FMT == kKvNf4 ? D / 64 : 1;        // scale groups of a vector
@@ -774,6 +775,11 @@ struct Plan {
     uint64_t total;           // units
 };
 
+// (a 64-bit division takes longer than what follows it)
+__device__ __forceinline__ uint32_t quotient(uint64_t a, uint32_t d) {
+    return a < (uint64_t{1} << 32) ? static_cast<uint32_t>(a) / d : static_cast<uint32_t>(a / d);
+}
+
 __device__ __forceinline__ uint32_t divide_up(uint64_t a, uint32_t d) {  // at most 2^30
     if (a < (uint64_t{1} << 31)) return (static_cast<uint32_t>(a) + d - 1) / d;
     const uint64_t q = (a + d - 1) / d;
@@ -832,7 +838,7 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     const uint32_t share = divide_up(total, p.workers);
     p.cut = 0;
     if (LINE && p.warps >= W / 2 && (share >= 2 * kLongUnits * p.warps || segments > p.workers / 2) &&
-        total >= 8 * p.warps * segments) {
+        total >= 8 * p.warps * segments && share < (1u << 30)) {  // (what divide_up gives is not less than the share)
         p.cell = share;
         p.count = p.workers;
         return p;
@@ -870,14 +876,10 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     return p;
 }
 
-// By line: the first unit of a cell, and the cell of a unit.
+// By line: the first unit of a cell.
 __device__ __forceinline__ uint64_t cell_start(const volatile Plan& p, uint32_t cell) {
     const uint64_t x = static_cast<uint64_t>(cell) * p.cell;
     return x < p.total ? x : p.total;
-}
-__device__ __forceinline__ uint32_t cell_of(const volatile Plan& p, uint64_t x) {
-    const uint32_t size = p.cell;
-    return x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / size : static_cast<uint32_t>(x / size);
 }
 
 // A sequence among the others, and what precedes it.
@@ -985,7 +987,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     if (threadIdx.x < 32) {
         const uint32_t mine = a.B <= 32 && lane < a.B ? units_of(lane) : 0;
         auto kept = [&](int b) { return a.B <= 32 ? mine : b < kUnitsKept ? s_units[b] : units_of(b); };
-        const Plan p = make_plan<S::W, FMT == kKvNf4>(kept, a.B, segs, lane);
+        const Plan p = make_plan<S::W, S::kLine>(kept, a.B, segs, lane);
         if (lane == 0) s_plan = p;
         if (a.B > 32 && a.B <= 32 * kBlocks) make_blocks(kept, a.B, p.cut, lane, s_blocks);
     }
@@ -1007,13 +1009,12 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     uint64_t x = 0, stop = 0;  // by line: what is left of the cell
     while (id < plan.count) {
         const uint32_t cut = plan.cut;
-        const bool by_line = FMT == kKvNf4 && cut == 0;
+        const bool by_line = S::kLine && cut == 0;
         if (x == stop) {
             if (by_line) {
                 x = cell_start(plan, id), stop = cell_start(plan, id + 1);
                 if (x == stop) break;
-                at = locate(units_of, a.B, at, s_blocks, x < (uint64_t{1} << 32) ? static_cast<uint32_t>(x) / segs
-                                                                       : static_cast<uint32_t>(x / segs), 0, lane);
+                at = locate(units_of, a.B, at, s_blocks, quotient(x, segs), 0, lane);
             } else {
                 at = locate(units_of, a.B, at, s_blocks, id / segs, cut, lane);
             }
@@ -1037,7 +1038,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                 at.b++;
                 continue;
             }
-            seg = static_cast<int>(in_seq < (uint64_t{1} << 32) ? static_cast<uint32_t>(in_seq) / n : in_seq / n);
+            seg = static_cast<int>(quotient(in_seq, n));
             u0 = static_cast<int>(in_seq - static_cast<uint64_t>(seg) * n);
             u1 = static_cast<int>(left < n - u0 ? u0 + left : n);
             x += u1 - u0;
@@ -1172,24 +1173,21 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         worker_barrier(group, wg);
         uint2* out = reinterpret_cast<uint2*>(a.out + row0 * D);
         const int columns = heads * (D / 4);
-        // The slots of a segment's pieces.  By line: two a cell, for the piece that begins a segment and for one
-        // that goes on with it.  By segment: segments that are cut have more than `cut` units, so the runs of
-        // slots from twice their first unit's quotient are disjoint.
+        // The slots of a segment's pieces, one after the other.  By segment: those that are cut have more than `cut`
+        // units, so the runs of slots from twice their first unit's quotient are disjoint.  By line: from twice the
+        // cell they begin in, since the next one that is cut begins in the cell where this one ends, or later.
         int slot0 = 0;
         if (!whole) {
             const uint64_t first_unit = static_cast<uint64_t>(at.units_before) * segs + static_cast<uint64_t>(seg) * n;
-            if (!by_line) {
-                slot0 = 2 * static_cast<int>(first_unit < (uint64_t{1} << 32) ? static_cast<uint32_t>(first_unit) / cut
-                                                                              : first_unit / cut);
-            } else {
-                const uint32_t cell0 = cell_of(plan, first_unit);
-                slot0 = 2 * cell0 + 1;
-                parts = cell_of(plan, first_unit + n - 1) - cell0 + 1;
-                part = id - cell0;
+            const uint32_t size = by_line ? plan.cell : cut;
+            const uint32_t at_first = quotient(first_unit, size);
+            slot0 = 2 * static_cast<int>(at_first);
+            if (by_line) {
+                parts = quotient(first_unit + n - 1, size) - at_first + 1;
+                part = id - at_first;
             }
         }
-        auto slot_index = [&](int i) { return slot0 + (by_line ? 2 * i - (i > 0) : i); };
-        auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot_index(i)) * a.slot_floats; };
+        auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot0 + i) * a.slot_floats; };
         for (int i = alone ? columns : tid; i < columns; i += threads) {
             const Joined r = join<D, 4, true, true>(
                 area, [&](int w) { return s_ml + (group * wg + w) * (2 * NT * 8); }, joiners, heads, i);
@@ -1231,7 +1229,7 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         if (!whole) {
             const int from = static_cast<int>(part) / kFanIn * kFanIn, batches = (parts + kFanIn - 1) / kFanIn;
             const int count = min(kFanIn, static_cast<int>(parts) - from);
-            if (join_slots(a.joins + slot_index(from), from, 1, count, batches == 1) && batches > 1)
+            if (join_slots(a.joins + slot0 + from, from, 1, count, batches == 1) && batches > 1)
                 join_slots(a.joins + kSlots + slot0, 0, kFanIn, batches, true);
         }
         if (x == stop) id = s_word[group][0];
