@@ -12,11 +12,11 @@
 // for 12 to 20% of the time as it is.
 //
 // What bounds it, measured on GB300 (DRAM copy rate 6774 GB/s): with a bf16 cache the memory (64 sequences up to
-// 8192, 8 kv heads: 184 us, 97% of that rate) and, for one sequence of 131071, the SMs' unequal shares of it (93 us,
-// 85%); with fp8 the latency of a ring of two stages (109 us, 85%); with NF4 the decoding: 64 table lookups of
-// 81 shared-memory reads and 340 instructions for 16 keys, 53% of the issue slots (32 sequences up to 16384:
-// 83 us, 57%); short calls the chain of dependent loads (lengths, page table, data, partial results): 5 us
-// for one sequence of 128 tokens, 12 us for 8 of up to 4095.
+// 8192, 8 kv heads: 182 us, 99% of that rate; one of 131071: 85 us, 94%); with fp8 the same for many sequences
+// (98 us, 95%) and the latency of a ring of two stages for one (48 us, 86%); with NF4 the decoding: 64 table
+// lookups of 81 shared-memory reads and 340 instructions for 16 keys (32 sequences up to 16384: 76 us, 62%;
+// one of 131071: 39 us, 54%); short calls the chain of dependent loads (lengths, page table, data, partial
+// results): 5 us for one sequence of 128 tokens, 12 us for 8 of up to 4095.
 //
 // Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte
 // (two codes) indexes a table of fp16 pairs in shared memory (see kTableF16).  The scales are applied in
@@ -26,14 +26,13 @@
 // 2^-8, would cost as much as the output's own rounding).  S, m, l and O are fp32 throughout.
 //
 // Work.  A unit is 16 or 32 keys of one sequence and kv head (or of one group of at most 16 of its query
-// heads): a segment.  Segments are cut into pieces of about equal size by a rule on the lengths alone, which
-// the kernel works out for itself (no plan from the host), so ragged batches, one long sequence and
-// thousands of short ones load the SMs alike.  A worker is a group of warps, two to a CTA and SM, so that
-// one streams while the other starts or joins a piece.  It takes its first piece by its number and
-// further ones by a ticket.  Inside a piece its warps take units in turn, each with its own ring of
-// cp.async stages and no barrier; their results are joined in shared memory.  The pieces of a segment leave
-// partial results in the workspace; the worker that finishes the last of them joins them in their
-// order (24 at a time, then the joined ones), so results do not depend on timing.
+// heads): a segment.  Segments are cut into pieces by a rule on the lengths alone (make_plan), which the
+// kernel works out for itself (no plan from the host), so ragged batches, one long sequence and thousands
+// of short ones load the SMs alike.  A worker is a group of warps, two to a CTA and SM, so that one
+// streams while the other starts or joins a piece.  Inside a piece its warps take units in turn, each with
+// its own ring of cp.async stages and no barrier; their results are joined in shared memory.  The pieces
+// of a segment leave partial results in the workspace; the worker that finishes the last of them joins
+// them in their order (24 at a time, then the joined ones), so results do not depend on timing.
 #include <algorithm>
 #include <mutex>
 
@@ -46,8 +45,9 @@ namespace {
 __device__ int g_attention_error;
 
 constexpr int kMaxWorkers = 320;      // of W / 2 warps
-constexpr int kRounds = 4;            // pieces a worker gets in long calls
-constexpr int kLongUnits = 16;        // units a warp: a piece of a call that is cut into several a worker
+constexpr int kRounds = 4;            // pieces a worker gets where workers are few warps
+constexpr int kLongUnits = 32;        // units a warp to do, from which a few segments, too, are cut by line
+constexpr int kStartRounds = 3;       // units a warp: what a segment's start and join count for in a line
 constexpr int kFanIn = 24;            // partial results joined at a time
 constexpr int kSlots = 2 * kMaxWorkers * kRounds + 2;  // partial results (see slot0)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -142,7 +142,7 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool liv
 }
 
 // What a long call reads of the cache is read once and leaves the L2 (129 MB) first: partial results, page tables
-// and the next kernels' data stay (64 sequences up to 8192, fp8: 110 -> 108 us; one of 131071: 52 -> 50).  A
+// and the next kernels' data stay (NF4, 64 sequences up to 2000: 48.0 -> 46.3 us; fp8, one of 131071: 49.8 -> 47.2).  A
 // short call's may stay: it may still be there when the layer comes round again (8 ragged sequences, fp8, 23 MB:
 // 12.3 -> 11.7 us).
 constexpr int64_t kStreamBytes = 32 << 20;
@@ -181,7 +181,6 @@ constexpr uint32_t kTableAt = 65536, kTableEnd = 131072;
 template <int FMT, int D, int NT>
 struct Shape {
     static constexpr bool kBf = FMT == kKvBf16;
-    static constexpr bool kLine = FMT != kKvFp8;                 // long segments are cut by line (see make_plan)
     static constexpr int VB = kv_vector_bytes(FMT, D);           // bytes of a vector
     static constexpr int SB = 16 * kv_scale_bytes(FMT, D);       // bytes of 16 keys' scales of one side
     static constexpr int GR = FMT == kKvNf4 ? D / 64 : 1;        // scale groups of a vector
@@ -766,13 +765,13 @@ __device__ __forceinline__ void worker_barrier(int group, int warps) {
 }
 
 // How the work is cut.  By segment: every segment into pieces of at most `cut` units, as equal as they come.
-// By line (cut = 0): the units of all segments end to end into one cell of `cell` units a worker, a cell's
-// part of a segment being a piece.
+// By line (cut = 0): the units of all segments end to end, each segment's behind `start` units that stand for the
+// time its start and join take, into one cell of `cell` units a worker; a cell's part of a segment is a piece.
 struct Plan {
     uint32_t warps, workers;  // warps of a worker; workers of the grid
     uint32_t count;           // pieces, or cells
-    uint32_t cut, cell;
-    uint64_t total;           // units
+    uint32_t cut, cell, start;
+    uint64_t total;           // units (by line: with the starts)
 };
 
 // (a 64-bit division takes longer than what follows it)
@@ -798,19 +797,20 @@ __device__ __forceinline__ uint32_t count_pieces(const Units& units, int B, uint
 // W / 2 of them, so that a CTA has one that streams while the other starts or joins a piece, except
 //  - all W, when there is at most a segment for each CTA and little to do (no second piece to overlap with), or
 //    a segment for eight CTAs (half as many partial results to join; one bf16 sequence of 131071 keys and 8
-//    heads: 92 us, 98 with halves);
+//    heads: 84 us, 87 with halves);
 //  - fewer, when there are many segments too short to keep W / 2 warps busy.
-// Sequences of up to 8 units a warp are not cut: the join of partial results costs 3 us, about what these
-// units do.  The rest is cut by segment: one piece a worker where there are few segments and less than
-// 2 kLongUnits units a warp to do, else up to four, taken by ticket, since the SMs' shares of the memory's
-// rate differ by 20% (one bf16 sequence of 131071 keys and 8 kv heads, in two: 102 us; in four, 110; in equal
-// runs laid end to end, 118).  Rounding up the pieces of each segment must not start
-// another round, so `cut` grows until they fit, unless the segments alone fill the rounds.
-// LINE: where decoding, not the memory, bounds the SM (NF4), SMs are equally fast, and long segments (8 units
-// a warp on average) are cut by line: the same work for every worker (32 sequences up to 16384: 89 us;
-// by segment 95), which shorter ones would pay for with a start and a join for each (64 sequences up
-// to 2000: 60 us; by segment 46).
-template <int W, bool LINE, typename Units>
+// Then, the figures being of bf16, fp8 and NF4 caches with 8 kv heads:
+//  - Sequences of up to 8 units a warp (4, where there are more segments than workers, so that a worker's pieces even
+//    out) are not cut: the join of partial results costs 3 us, about what these units do.
+//  - Many segments, and long ones, are cut by line: every worker does the same, whatever the lengths.  A segment's
+//    start and join (and units that do not fill a round of the worker's warps) take as long as about three units a
+//    warp, so the line counts that many more for each (64 sequences of 200 to 4000 tokens: 88, 50, 47 us; without it
+//    97, 71, 70; cut by segment into up to four pieces a worker: 94, 61, 61.  One of 131071: 85, 47, 39; by
+//    segment 93, 47, 40).
+//  - The rest, a few segments with little to do, by segment: the pieces of each are as equal as they come and their
+//    count fits the workers, so `cut` grows until it does.  So are many segments too short for W / 2 warps, into
+//    up to kRounds pieces a worker, taken by ticket.
+template <int W, typename Units>
 __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t segs, int lane) {
     uint32_t sum = 0, live = 0, longest = 0;
     for (int b = lane; b < B; b += 32) {
@@ -824,28 +824,28 @@ __device__ __forceinline__ Plan make_plan(const Units& units, int B, uint32_t se
     longest = __reduce_max_sync(0xFFFFFFFFu, longest);
     const uint64_t segments = static_cast<uint64_t>(live) * segs, total = static_cast<uint64_t>(sum) * segs;
     Plan p;
-    p.total = total;
+    p.total = total, p.start = 0;
     p.warps = W / 2;
     if (segments * 8 <= gridDim.x || (segments <= gridDim.x && total <= static_cast<uint64_t>(8 * W) * gridDim.x))
         p.warps = W;
     while (p.warps > 1 && segments >= 2 * gridDim.x * (W / p.warps) && total < 4 * p.warps * segments) p.warps /= 2;
     p.workers = gridDim.x * (W / p.warps);
-    if (longest <= 8 * p.warps) {
-        p.cut = 8 * p.warps;
+    const uint32_t uncut = (p.warps >= W / 2 && segments > p.workers ? 4 : 8) * p.warps;
+    if (longest <= uncut) {
+        p.cut = uncut;
         p.count = static_cast<uint32_t>(segments);
         return p;
     }
     const uint32_t share = divide_up(total, p.workers);
-    p.cut = 0;
-    if (LINE && p.warps >= W / 2 && (share >= 2 * kLongUnits * p.warps || segments > p.workers / 2) &&
-        total >= 8 * p.warps * segments && share < (1u << 30)) {  // (what divide_up gives is not less than the share)
-        p.cell = share;
+    if (p.warps >= W / 2 && (segments > p.workers / 2 || share >= kLongUnits * p.warps) && share < (1u << 29)) {
+        p.cut = 0;
+        p.start = kStartRounds * p.warps;
+        p.total = total + segments * p.start;
+        p.cell = divide_up(p.total, p.workers);
         p.count = p.workers;
         return p;
     }
-    const uint32_t rounds = segments > p.workers / 2 || share >= 4 * kLongUnits * p.warps ? kRounds
-                            : share >= 2 * kLongUnits * p.warps                           ? 2
-                                                                                          : 1;
+    const uint32_t rounds = segments > p.workers / 2 ? kRounds : 1;
     // (the second bound keeps the workspace's slots enough when workers of few warps are many)
     uint32_t low = max(divide_up(total, rounds * p.workers), divide_up(total, kRounds * gridDim.x * 2));
     low = max(low, 2 * p.warps);
@@ -898,23 +898,24 @@ constexpr int kUnitsKept = 4096;  // sequences whose units are kept while the pl
 
 // The whole warp calls it.
 template <typename Units>
-__device__ __forceinline__ void make_blocks(const Units& units, int B, uint32_t cut, int lane, Before* blocks) {
+__device__ __forceinline__ void make_blocks(const Units& units, int B, uint32_t cut, uint32_t start, int lane,
+                                            Before* blocks) {
     Before sum{0, 0};
     for (int i = 0; i * 32 < B; i++) {
         if (lane == 0) blocks[i] = sum;
         const int b = i * 32 + lane;
         const uint32_t n = b < B ? units(b) : 0;
-        sum.units += __reduce_add_sync(0xFFFFFFFFu, n);
+        sum.units += __reduce_add_sync(0xFFFFFFFFu, n ? n + start : 0);
         sum.pieces += __reduce_add_sync(0xFFFFFFFFu, cut ? (n + cut - 1) / cut : 0);
     }
 }
 
 // The sequence in which number `id` falls (there is one): of the pieces of one segment of each sequence,
-// ceil(n / cut) for n units, or (cut = 0) of its units.  Searched from its block of 32 on, or, with more
+// ceil(n / cut) for n units, or (cut = 0) of its units with its start.  Searched from its block of 32 on, or, with more
 // sequences than the blocks cover, from the last place found.  The whole warp calls it.
 template <typename Units>
 __device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, const Before* blocks, uint32_t id,
-                                        uint32_t cut, int lane) {
+                                        uint32_t cut, uint32_t start, int lane) {
     if (B == 1) return at;
     if (B > 32 && B <= 32 * kBlocks) {
         int block = -1;  // the last one that nothing past `id` precedes
@@ -928,7 +929,8 @@ __device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, 
     for (;;) {
         const int b = at.b + lane;
         const uint32_t n = b < B ? units_of(b) : 0, p = cut ? (n + cut - 1) / cut : 0;
-        uint32_t sum = p, units = n;
+        const uint32_t line = n ? n + start : 0;
+        uint32_t sum = p, units = line;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, sum, o), up_units = __shfl_up_sync(0xFFFFFFFFu, units, o);
@@ -939,7 +941,7 @@ __device__ __forceinline__ Place locate(const Units& units_of, int B, Place at, 
         if (past) {
             const int f = __ffs(past) - 1;
             at.b += f;
-            at.units_before += __shfl_sync(0xFFFFFFFFu, units - n, f);
+            at.units_before += __shfl_sync(0xFFFFFFFFu, units - line, f);
             at.pieces_before += __shfl_sync(0xFFFFFFFFu, sum - p, f);
             return at;
         }
@@ -987,9 +989,9 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     if (threadIdx.x < 32) {
         const uint32_t mine = a.B <= 32 && lane < a.B ? units_of(lane) : 0;
         auto kept = [&](int b) { return a.B <= 32 ? mine : b < kUnitsKept ? s_units[b] : units_of(b); };
-        const Plan p = make_plan<S::W, S::kLine>(kept, a.B, segs, lane);
+        const Plan p = make_plan<S::W>(kept, a.B, segs, lane);
         if (lane == 0) s_plan = p;
-        if (a.B > 32 && a.B <= 32 * kBlocks) make_blocks(kept, a.B, p.cut, lane, s_blocks);
+        if (a.B > 32 && a.B <= 32 * kBlocks) make_blocks(kept, a.B, p.cut, p.start, lane, s_blocks);
     }
     __syncthreads();
     // (the plan is read where it is needed: it does not live in registers)
@@ -1009,14 +1011,14 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
     uint64_t x = 0, stop = 0;  // by line: what is left of the cell
     while (id < plan.count) {
         const uint32_t cut = plan.cut;
-        const bool by_line = S::kLine && cut == 0;
+        const bool by_line = cut == 0;
         if (x == stop) {
             if (by_line) {
                 x = cell_start(plan, id), stop = cell_start(plan, id + 1);
                 if (x == stop) break;
-                at = locate(units_of, a.B, at, s_blocks, quotient(x, segs), 0, lane);
+                at = locate(units_of, a.B, at, s_blocks, quotient(x, segs), 0, plan.start, lane);
             } else {
-                at = locate(units_of, a.B, at, s_blocks, id / segs, cut, lane);
+                at = locate(units_of, a.B, at, s_blocks, id / segs, cut, 0, lane);
             }
             if (tid == 0) next = plan.count > plan.workers ? atomicAdd(a.tickets, 1u) + plan.workers : 0xFFFFFFFFu;
         }
@@ -1032,14 +1034,21 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
             part = in_seq - seg * parts;
             u0 = static_cast<int>(part * len), u1 = static_cast<int>(min(n, part * len + len));
         } else {
-            const uint64_t in_seq = x - static_cast<uint64_t>(at.units_before) * segs, left = stop - x;
-            if (n == 0 || in_seq >= static_cast<uint64_t>(n) * segs) {  // on to the next sequence
-                at.units_before += n;
+            const uint32_t start = plan.start, line = n ? n + start : 0;
+            const uint64_t in_seq = x - static_cast<uint64_t>(at.units_before) * segs;
+            if (in_seq >= static_cast<uint64_t>(line) * segs) {  // on to the next sequence
+                at.units_before += line;
                 at.b++;
                 continue;
             }
-            seg = static_cast<int>(quotient(in_seq, n));
-            u0 = static_cast<int>(in_seq - static_cast<uint64_t>(seg) * n);
+            seg = static_cast<int>(quotient(in_seq, line));
+            uint32_t from = static_cast<uint32_t>(in_seq - static_cast<uint64_t>(seg) * line);
+            if (from < start) {
+                x += start - from, from = start;
+                if (x >= stop) break;  // (a worker has one cell)
+            }
+            const uint64_t left = stop - x;
+            u0 = static_cast<int>(from - start);
             u1 = static_cast<int>(left < n - u0 ? u0 + left : n);
             x += u1 - u0;
         }
@@ -1178,13 +1187,16 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         // cell they begin in, since the next one that is cut begins in the cell where this one ends, or later.
         int slot0 = 0;
         if (!whole) {
-            const uint64_t first_unit = static_cast<uint64_t>(at.units_before) * segs + static_cast<uint64_t>(seg) * n;
-            const uint32_t size = by_line ? plan.cell : cut;
-            const uint32_t at_first = quotient(first_unit, size);
-            slot0 = 2 * static_cast<int>(at_first);
-            if (by_line) {
-                parts = quotient(first_unit + n - 1, size) - at_first + 1;
-                part = id - at_first;
+            const uint64_t before = static_cast<uint64_t>(at.units_before) * segs;
+            if (!by_line) {
+                slot0 = 2 * static_cast<int>(quotient(before + static_cast<uint64_t>(seg) * n, cut));
+            } else {
+                const uint32_t start = plan.start, size = plan.cell;
+                const uint64_t first_unit = before + static_cast<uint64_t>(seg) * (n + start) + start;
+                const uint32_t first_cell = quotient(first_unit, size);
+                slot0 = 2 * static_cast<int>(first_cell);
+                parts = quotient(first_unit + n - 1, size) - first_cell + 1;
+                part = id - first_cell;
             }
         }
         auto slot = [&](int i) { return a.partials + static_cast<int64_t>(slot0 + i) * a.slot_floats; };

@@ -76,3 +76,32 @@ def test_one_workspace_for_every_cut():
     for _ in range(3):
         for (c, q, t, n), want in zip(cases, own):
             assert torch.equal(nf4.attention_decode(c, q, t, n, shared), want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("batch,heads,group,low,high", [
+    (1, 8, 5, 120001, 120002),   # few segments, long
+    (33, 4, 2, 1, 9000),         # found by block
+    (64, 8, 1, 90, 4000),        # cells of one long segment's part, and of many short segments
+    (2100, 1, 2, 700, 1100),     # more sequences than are found by block
+    (4200, 1, 1, 800, 1000),     # more than are kept while the plan is made
+])
+def test_line(fmt, batch, heads, group, low, high):
+    """Segments laid end to end, some of them empty, with cells that end anywhere in them."""
+    page, dim = 64, 64
+    lengths = torch.randint(low, high, (batch,), generator=torch.Generator().manual_seed(batch)).tolist()
+    for i in range(5, batch, 11):
+        lengths[i] = 0
+    need = sum(-(-n // page) for n in lengths)
+    c = new_cache(fmt, need, heads, page, dim, seed=27)
+    table = paged(lengths, page, need, -(-max(lengths) // page), 28)
+    q = randn((batch, heads * group, dim), 29)
+    n = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    ws = nf4.attention_workspace(c, batch, heads * group)
+    first = nf4.attention_decode(c, q, table.to(DEV), n, ws)
+    assert torch.equal(nf4.attention_decode(c, q, table.to(DEV), n, ws), first)
+    assert nf4.nf4_check_device_error() == 0
+    some = sorted(set(range(0, batch, max(1, batch // 60))) | {batch - 1})
+    want, tol = reference(c, q[some], table[some], [lengths[i] for i in some], dim ** -0.5, 0)
+    assert bool(((first[some].double() - want).abs() <= tol).all())
+    assert not first[[i for i, m in enumerate(lengths) if m == 0]].any()
