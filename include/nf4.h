@@ -22,14 +22,16 @@
  *     16 bytes.  bf16 and fp16 values travel as their 16-bit patterns (uint16_t).
  *   - Calls are asynchronous on `stream` (0 = the legacy default stream).  No call synchronises
  *     the device, allocates memory or keeps state beyond a per-device capability check, except the
- *     ring calls of the overflow-streaming section, which own explicitly created state.
+ *     ring calls of the overflow-streaming section, which own explicitly created state.  (The
+ *     attention keeps counters in the workspace that its caller passes.)
  *   - Arguments are checked on the host before anything is launched; on an error nothing is
  *     launched and no output is written.  A failed launch returns NF4_ERR_CUDA and leaves the CUDA
  *     error state cleared.
  *   - Shapes: N and M may be 0 (nothing is launched, NF4_OK); K must be a positive multiple of 64;
  *     M, N and K must each be at most 2^31 - 1.
  *   - Non-finite inputs are outside the contract: results are unspecified, but no call faults.
- *   - The same inputs give the same output bytes on every call (no atomics, fixed reduction order).
+ *   - The same inputs give the same output bytes on every call (fixed reduction order; atomics only
+ *     hand out the attention's work).
  *   - Every call may be captured into a CUDA graph (the kernels build their constant tables in
  *     shared memory at launch; no call needs one-time device work), except the first call of
  *     nf4_linear_host_noalloc on a device (see there).
@@ -365,9 +367,9 @@ nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
  * see nf4_diag_set_wait_limit); a wait that runs out records a nonzero code (1..39; 39 is
  * nf4_diag_bounded_wait's), and the kernel drains and exits instead of hanging, leaving its outputs
  * unspecified.  nf4_embed records 41 for an id outside the table, the cache calls 42 for a slot
- * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds (44: a shared-memory layout that its
- * kernel does not know).  *code receives the first
- * recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
+ * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds (44: a
+ * shared-memory layout that its kernel does not know; nothing is computed then).  *code receives the
+ * first recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
  */
 nf4_status nf4_check_device_error(int* code);
 

@@ -147,10 +147,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
 // ---------------------------------------------------------------------------------------------
 // Residual RMS norm
 // ---------------------------------------------------------------------------------------------
-// Two forms.  rmsnorm_kernel, for few rows or very wide ones: one CTA a row.  h = x + residual stays in registers (CH pieces of eight values a thread; CH = 0, for
-// rows too wide for that, reads the row again), one block reduction gives sum(h^2) and max |h w| at once:
-// max |y| = rsqrt(...) * max |h w|, so the 8-bit scale needs no second one.  With many rows its CTAs spend
-// their time waiting for their loads (8192 x 5120, 8 bits out: 58 us, 75% of the measured copy rate).
+// Two forms.  rmsnorm_kernel, for few rows, narrow or very wide ones: one CTA a row.  h = x + residual stays in
+// registers (CH pieces of eight values a thread; CH = 0, for rows too wide for that, reads the row again), one
+// block reduction gives sum(h^2) and max |h w| at once: max |y| = rsqrt(...) * max |h w|, so the 8-bit scale
+// needs no second one.  With many rows its CTAs spend their time waiting for their loads (8192 x 5120, 8 bits
+// out: 58 us, 75% of the measured copy rate).
 // rmsnorm_ring_kernel, for those: persistent CTAs whose next two rows are on their way into shared memory;
 // each thread copies what it will read itself, so the ring needs no barrier.
 __device__ __forceinline__ float2 block_sum_max(float2 v, float2* part) {
