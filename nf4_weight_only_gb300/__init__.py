@@ -7,6 +7,7 @@ torch tensors (device memory and streams) into the C calls of the same names and
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import importlib.machinery
@@ -319,6 +320,16 @@ def _current(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream):
+    """Where results are allocated: on the stream that computes them.  (torch may hand out memory that the current
+    stream still uses.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    if hasattr(stream, "cuda_stream"):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream())
+
+
 class KVCache:
     """A paged key-value cache over the caller's tensors (include/nf4.h, nf4_kv_cache).
 
@@ -407,9 +418,11 @@ def nf4_attention_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> i
     return n
 
 
-def attention_workspace(cache: KVCache, batch: int, q_heads: int) -> torch.Tensor:
-    """A zeroed workspace for nf4_attention_decode with this cache, up to this batch and these heads."""
-    return torch.zeros(nf4_attention_workspace_bytes(cache, batch, q_heads), dtype=torch.uint8, device=cache.device)
+def attention_workspace(cache: KVCache, batch: int, q_heads: int, stream=None) -> torch.Tensor:
+    """A workspace for nf4_attention_decode with this cache and these heads, allocated and zeroed on `stream`: calls
+    on another stream wait for that first."""
+    with _on(stream):
+        return torch.zeros(nf4_attention_workspace_bytes(cache, batch, q_heads), dtype=torch.uint8, device=cache.device)
 
 
 def nf4_attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
@@ -492,29 +505,33 @@ def nf4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
 # Convenience wrappers that allocate the outputs with torch.
 def kv_read(cache: KVCache, slots: torch.Tensor, stream=None):
     shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=slots.device) for _ in range(2))
+    with _on(stream):
+        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=slots.device) for _ in range(2))
     nf4_kv_read(cache, slots, k, v, stream)
     return k, v
 
 
 def attention_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
                      workspace: torch.Tensor, scale: Optional[float] = None, window: int = 0, stream=None):
-    out = torch.empty_like(q)
+    with _on(stream):
+        out = torch.empty_like(q)
     nf4_attention_decode(cache, q, page_table, lengths, out, workspace, scale, window, stream)
     return out
 
 
 def rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, sections=None,
          interleaved: bool = False, magnitude: float = 1.0, stream=None):
-    q_out, k_out = torch.empty_like(q), torch.empty_like(k)
+    with _on(stream):
+        q_out, k_out = torch.empty_like(q), torch.empty_like(k)
     nf4_rope(q, k, positions, inv_freq, q_out, k_out, sections, interleaved, magnitude, stream)
     return q_out, k_out
 
 
 def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None, stream=None):
     """y, or (y, x + residual) with a residual."""
-    y = torch.empty_like(x)
-    r = None if residual is None else torch.empty_like(x)
+    with _on(stream):
+        y = torch.empty_like(x)
+        r = None if residual is None else torch.empty_like(x)
     nf4_rmsnorm(x, weight, eps, residual=residual, residual_out=r, y=y, stream=stream)
     return y if residual is None else (y, r)
 
