@@ -14,7 +14,7 @@
 // What bounds it, measured on GB300 (DRAM copy rate 6774 GB/s): with a bf16 cache the memory (64 sequences up to
 // 8192, 8 kv heads: 182 us, 99% of that rate; one of 131071: 85 us, 94%); with fp8 the same for many sequences
 // (98 us, 95%) and the latency of a ring of two stages for one (48 us, 86%); with NF4 the decoding: 64 table
-// lookups of 81 shared-memory reads and 340 instructions for 16 keys (32 sequences up to 16384: 76 us, 62%;
+// lookups of 81 shared-memory reads and 340 instructions for 16 keys (32 sequences up to 16384: 75 us, 63%;
 // one of 131071: 39 us, 54%); short calls the chain of dependent loads (lengths, page table, data, partial
 // results): 5 us for one sequence of 128 tokens, 12 us for 8 of up to 4095.
 //
@@ -513,18 +513,27 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
                 for (int c = 0; c < GR; c++)
                     if (!on(b, r)) vs[b][r][c] = 0.0f;
     }
+    float widest = 0.0f;  // the largest V scale
     if (FMT != kKvBf16) {
-        // V scales in fp16 range: the largest times vn stays below 2^7
-        float top = 0.0f;
 #pragma unroll
         for (int b = 0; b < KS; b++)
 #pragma unroll
             for (int r = 0; r < 2; r++)
 #pragma unroll
-                for (int c = 0; c < GR; c++) top = fmaxf(top, vs[b][r][c]);
-        if (__any_sync(0xFFFFFFFFu, top > s.vlim)) {
-            top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-            const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 7), 254);
+                for (int c = 0; c < GR; c++) widest = fmaxf(widest, vs[b][r][c]);
+    }
+#pragma unroll
+    for (int b = 0; b < KS; b++)
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) most = fmaxf(most, x[b][nt][j]);
+    // rare, and one vote for both (two: 1.5% slower with NF4): V's scales leave the fp16 range (the largest times vn
+    // stays below 2^7), or the maxima move
+    if (__any_sync(0xFFFFFFFFu, (FMT != kKvBf16 && widest > s.vlim) || most > kLazy)) {
+        if (FMT != kKvBf16 && __any_sync(0xFFFFFFFFu, widest > s.vlim)) {
+            widest = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(widest)));
+            const int e = min(max(static_cast<int>(__float_as_uint(widest) >> 23), 7), 254);
             const float vn = __uint_as_float(static_cast<uint32_t>(260 - e) << 23), f = vn / s.vn;
             s.vn = vn;
             s.vlim = __uint_as_float(static_cast<uint32_t>(min(e + 1, 254)) << 23);
@@ -535,37 +544,31 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
 #pragma unroll
                     for (int j = 0; j < 4; j++) s.o[nt][i][j] *= f;
         }
-    }
+        if (__any_sync(0xFFFFFFFFu, most > kLazy)) {
 #pragma unroll
-    for (int b = 0; b < KS; b++)
+            for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+                for (int j = 0; j < 2; j++) {
+                    float top = s.m[nt][j];
 #pragma unroll
-            for (int j = 0; j < 4; j++) most = fmaxf(most, x[b][nt][j]);
-    if (__any_sync(0xFFFFFFFFu, most > kLazy)) {
+                    for (int b = 0; b < KS; b++)
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+                        for (int r = 0; r < 2; r++) {
+                            float& z = x[b][nt][j + 2 * r];
+                            z = z == -INFINITY ? z : y[b][nt][j + 2 * r] * s.mul[nt][j];
+                            top = fmaxf(top, z);
+                        }
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                float top = s.m[nt][j];
+                    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    const float f = exp2_approx(s.m[nt][j] - top);
+                    s.m[nt][j] = top;
+                    s.l[nt][j] *= f;
 #pragma unroll
-                for (int b = 0; b < KS; b++)
+                    for (int i = 0; i < D / 16; i++) s.o[nt][i][j] *= f, s.o[nt][i][j + 2] *= f;
 #pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        float& z = x[b][nt][j + 2 * r];
-                        z = z == -INFINITY ? z : y[b][nt][j + 2 * r] * s.mul[nt][j];
-                        top = fmaxf(top, z);
-                    }
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                const float f = exp2_approx(s.m[nt][j] - top);
-                s.m[nt][j] = top;
-                s.l[nt][j] *= f;
-#pragma unroll
-                for (int i = 0; i < D / 16; i++) s.o[nt][i][j] *= f, s.o[nt][i][j + 2] *= f;
-#pragma unroll
-                for (int b = 0; b < KS; b++) x[b][nt][j] -= top, x[b][nt][j + 2] -= top;
-            }
+                    for (int b = 0; b < KS; b++) x[b][nt][j] -= top, x[b][nt][j + 2] -= top;
+                }
+        }
     }
     // weights, and p^T fragments
     constexpr int PB = FMT == kKvBf16 ? 2 : GR;  // bf16: p's high and low part; else one for each scale group
