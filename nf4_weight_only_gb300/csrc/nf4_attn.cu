@@ -21,8 +21,8 @@
 // Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte
 // (two codes) indexes a table of fp16 pairs in shared memory (see kTableF16).  The scales are applied in
 // fp32: K's to S, V's to p.  q in fp16 is scaled by a power of two a head (exact except for elements
-// below 2^-28 of the head's largest); p * scale is rounded to fp16 (2^-11), times a power of two a warp
-// that follows the largest scale.  With a bf16 cache p goes in as the sum of two bf16 numbers (one alone,
+// below 2^-28 of the head's largest); p * scale is rounded to fp16, times a power of two a warp that follows the
+// largest scale of V it has met (the error is 2^-11 of the product or 2^-31 of that scale, whichever is larger).  With a bf16 cache p goes in as the sum of two bf16 numbers (one alone,
 // 2^-8, would cost as much as the output's own rounding).  S, m, l and O are fp32 throughout.
 //
 // Work.  A unit is 16 or 32 keys of one sequence and kv head (or of one group of at most 16 of its query
