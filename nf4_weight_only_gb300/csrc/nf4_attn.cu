@@ -18,12 +18,13 @@
 // one of 131071: 39 us, 54%); short calls the chain of dependent loads (lengths, page table, data, partial
 // results): 5 us for one sequence of 128 tokens, 12 us for 8 of up to 4095.
 //
-// Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte
-// (two codes) indexes a table of fp16 pairs in shared memory (see kTableF16).  The scales are applied in
-// fp32: K's to S, V's to p.  q in fp16 is scaled by a power of two a head (exact except for elements
-// below 2^-28 of the head's largest); p * scale is rounded to fp16, times a power of two a warp that follows the
-// largest scale of V it has met (the error is 2^-11 of the product or 2^-31 of that scale, whichever is larger).  With a bf16 cache p goes in as the sum of two bf16 numbers (one alone,
-// 2^-8, would cost as much as the output's own rounding).  S, m, l and O are fp32 throughout.
+// Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte (two
+// codes) indexes a table of fp16 pairs in shared memory (see kTableF16).  The scales are applied in fp32: K's to
+// S, V's to p.  q in fp16 is scaled by a power of two a head (exact except for elements below 2^-28 of the
+// head's largest); p * scale is rounded to fp16, times a power of two a warp that follows the largest scale of V
+// it has met (the error is 2^-11 of the product or 2^-31 of that scale, whichever is larger).  With a bf16 cache
+// p goes in as the sum of two bf16 numbers (one alone, 2^-8, would cost as much as the output's own rounding).
+// S, m, l and O are fp32 throughout.
 //
 // Work.  A unit is 16 or 32 keys of one sequence and kv head (or of one group of at most 16 of its query
 // heads): a segment.  Segments are cut into pieces by a rule on the lengths alone (make_plan), which the
@@ -144,7 +145,7 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool liv
 // What a long call reads of the cache is read once and leaves the L2 (129 MB) first: partial results, page tables
 // and the next kernels' data stay (NF4, 64 sequences up to 2000: 48.0 -> 46.3 us; fp8, one of 131071: 49.8 -> 47.2).  A
 // short call's may stay: it may still be there when the layer comes round again (8 ragged sequences, fp8, 23 MB:
-// 12.3 -> 11.7 us).
+// 12.3 -> 12.0 us).
 constexpr int64_t kStreamBytes = 32 << 20;
 __device__ __forceinline__ uint64_t l2_policy(bool stream) {
     uint64_t first, normal;
@@ -190,9 +191,9 @@ struct Shape {
     static constexpr int kBlock = 32 * VB + 2 * SB;              // 16 keys, K and V
     static constexpr int kStage = KS * kBlock;
     // Warps and stages.  bf16: 8 warps with 8 KB stages are 128 KB in flight an SM.  Decoding wants more warps, and
-    // registers: 12 warps at 168 (NF4, 32 sequences up to 16384: 95 us; 16 at 128 work the addresses out again
-    // for every unit: 107; 8: 130), except where a warp's state alone takes more (8 warps; NT = 2 at 12: 295 us
-    // against 250).
+    // registers: 12 warps at 168 (NF4, 32 sequences up to 16384: 75 us; 16 at 128 work the addresses out again
+    // for every unit: 79; 8: 81), except where a warp's state alone takes more (8 warps: NT = 2 uses 254; in 12
+    // warps it was 18% slower).
     static constexpr int W = FMT == kKvBf16 ? (D == 256 ? 4 : 8) : D == 256 || NT == 2 ? 8 : 12;
     static constexpr int kRingMost = FMT == kKvNf4 ? (W == 12 ? 8704 : 20480) : 230400 / W / 16 * 16;
     static constexpr int kStagesFit = kRingMost / kStage;
@@ -1105,7 +1106,8 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
                     for (int b = 0; b < KS; b++) {
                         const int64_t at_b = KS > 1 && b ? place[KS - 1] : place[0];
                         bad |= at_b == -1 ? 1u << b : 0u;
-                        copy_edge_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, at_b, lo - 16 * b, hi - 16 * b, lane, policy);
+                        copy_edge_block<FMT, D, NT>(a.c, in_buf + b * S::kBlock, at_b, lo - 16 * b, hi - 16 * b, lane,
+                                                    policy);
                     }
                 }
                 in_buf = in_buf + S::kStage == ring + S::kRing ? ring : in_buf + S::kStage;
@@ -1256,7 +1258,8 @@ __global__ void __launch_bounds__(Shape<FMT, D, NT>::W * 32, 1) attention_kernel
         if (lane == 0 && a.lengths[b] > a.max_pages * a.c.page_size) atomicCAS(&g_attention_error, 0, 43);
         if (span_of(a, b).units<KEYS>() == 0)
             for (int i = lane; i < a.q_heads * (D / 8); i += 32)
-                reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * (D / 8)) + i] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4*>(a.out)[static_cast<int64_t>(b) * (a.q_heads * (D / 8)) + i] =
+                    make_uint4(0, 0, 0, 0);
     }
     // the last worker leaves the tickets as it found them
     if (tid == 0 && plan.count > plan.workers) {

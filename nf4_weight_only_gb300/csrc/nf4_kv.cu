@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(256) append_kernel(KvCache c, const uint16_t* 
     uint32_t t = i0 / c.kv_heads;
     const int h = static_cast<int>(i0 - t * c.kv_heads);
     // whole warps stay in the loop: the shuffles take all 32 lanes
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (256 / L); base < walk.items; base += walk.width, t += walk.tokens) {
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * (256 / L); base < walk.items;
+         base += walk.width, t += walk.tokens) {
         const int64_t i = base + threadIdx.x / L;
         uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
         int64_t at = -1;

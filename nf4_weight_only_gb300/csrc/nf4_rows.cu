@@ -103,9 +103,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a, in
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int i = 8 * c + j;
-            const int32_t p = i < a.section_end[0] ? pos[0] : i < a.section_end[1] ? pos[1] : i < a.section_end[2] ? pos[2] : pos[3];
+            const int32_t p = i < a.section_end[0]   ? pos[0]
+                              : i < a.section_end[1] ? pos[1]
+                              : i < a.section_end[2] ? pos[2]
+                                                     : pos[3];
             const uint64_t at = turn_fraction(a.inv_freq[i]) * static_cast<uint64_t>(static_cast<int64_t>(p));
-            const float angle = static_cast<float>(static_cast<int32_t>(at >> 32)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+            constexpr float kTurn = 1.4629180792671596e-9f;  // 2 pi / 2^32
+            const float angle = static_cast<float>(static_cast<int32_t>(at >> 32)) * kTurn;
             r.s[j] = __sinf(angle) * a.magnitude;
             r.c[j] = __cosf(angle) * a.magnitude;
         }
@@ -403,7 +407,8 @@ cudaError_t launch_rope(const RopeArgs& a, int num_sms, cudaStream_t stream) {
     }
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = pdl_config(grid, kRopeThreads, stream, &attr);
-    return walk > 1 ? cudaLaunchKernelEx(&cfg, rope_kernel<4>, a, step) : cudaLaunchKernelEx(&cfg, rope_kernel<1>, a, step);
+    return walk > 1 ? cudaLaunchKernelEx(&cfg, rope_kernel<4>, a, step)
+                    : cudaLaunchKernelEx(&cfg, rope_kernel<1>, a, step);
 }
 
 cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t T, int64_t H,
