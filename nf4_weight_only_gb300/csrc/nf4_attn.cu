@@ -677,8 +677,8 @@ __device__ __forceinline__ void attend_unit(WarpState<FMT, D, NT>& s, uint32_t b
 struct Span {
     int start, end;  // keys [start, end) of a sequence
     template <int KEYS>
-    __device__ int units() const {  // of KEYS keys each, aligned
-        return end > start ? (end + KEYS - 1) / KEYS - start / KEYS : 0;
+    __device__ int units() const {  // of KEYS keys each, aligned (`end` may be within KEYS of 2^31)
+        return end > start ? static_cast<int>((static_cast<uint32_t>(end) + (KEYS - 1)) / KEYS) - start / KEYS : 0;
     }
 };
 
