@@ -316,8 +316,9 @@ nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t 
  *               workspace each; one workspace serves calls of different sizes as long as it is large
  *               enough for each.
  * Values in places that are not attended to (past a length, before the window) do not matter, NaN
- * and infinities included.  NF4_ERR_SHAPE also for B > 65535, B * q_heads > 2^30, max_pages * page_size
- * >= 2^31, B * max_pages * page_size > 2^35 and for a workspace_bytes below the need.
+ * and infinities included.  NF4_ERR_SHAPE also for B > 65535, q_heads > 65535, B * q_heads > 2^30,
+ * max_pages * page_size >= 2^31, B * max_pages * page_size > 2^35 and for a workspace_bytes below the
+ * need.  nf4_attention_workspace_bytes gives -1 for a cache, B or q_heads that the call refuses so.
  */
 int64_t nf4_attention_workspace_bytes(const nf4_kv_cache* cache, int64_t B, int64_t q_heads);
 nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, const int32_t* page_table,

@@ -98,6 +98,11 @@ bool overlaps_cache(const Ranges& r, const void* p, int64_t bytes) {
     return false;
 }
 
+bool attention_sizes_ok(const nf4_kv_cache* c, int64_t B, int64_t q_heads) {
+    return B >= 0 && B <= 65535 && q_heads >= 1 && q_heads <= 65535 && q_heads % c->kv_heads == 0 &&
+           B * q_heads <= (int64_t{1} << 30);
+}
+
 nf4::KvCache device_cache(const nf4_kv_cache* c) {
     return {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), static_cast<uint8_t*>(c->k_scales),
             static_cast<uint8_t*>(c->v_scales), c->pages, c->kv_heads, c->page_size, c->head_dim, c->format};
@@ -322,7 +327,7 @@ nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t 
 }
 
 int64_t nf4_attention_workspace_bytes(const nf4_kv_cache* cache, int64_t B, int64_t q_heads) {
-    if (!cache || check_cache(cache) == NF4_ERR_SHAPE || B < 0 || q_heads < 1 || q_heads % cache->kv_heads != 0) return -1;
+    if (!cache || check_cache(cache) == NF4_ERR_SHAPE || !attention_sizes_ok(cache, B, q_heads)) return -1;
     return nf4::attention_workspace_bytes(cache->kv_heads, cache->head_dim, B, q_heads);
 }
 
@@ -332,8 +337,7 @@ nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, co
                                 cudaStream_t stream) {
     nf4_status st = check_cache(cache);
     if (st != NF4_OK) return st;
-    if (B < 0 || B > 65535 || q_heads < 1 || q_heads > 65535 || q_heads % cache->kv_heads != 0) return NF4_ERR_SHAPE;
-    if (B * q_heads > (int64_t{1} << 30)) return NF4_ERR_SHAPE;
+    if (!attention_sizes_ok(cache, B, q_heads)) return NF4_ERR_SHAPE;
     if (max_pages < 0 || max_pages > kMaxDim || max_pages * cache->page_size > kMaxDim || window < 0) return NF4_ERR_SHAPE;
     if (max_pages > 0 && B > (int64_t{1} << 35) / (max_pages * cache->page_size)) return NF4_ERR_SHAPE;
     if (B == 0) return NF4_OK;

@@ -1,0 +1,16 @@
+"""Host-side checks of the cache, attention, rotary and norm calls at the ends of their ranges (no GPU)."""
+import ctypes
+
+import pytest
+
+from test_layer_ops_host import E, F, SHAPE, cache, lib  # noqa: F401 (lib is a fixture)
+
+
+@pytest.mark.parametrize("batch,q_heads", [(1, 65536), (1, 1 << 31), (1, 1 << 32), (1, 3 << 32), (65536, 1), (32768, 65535)])
+def test_workspace_of_sizes_that_the_attention_refuses(lib, batch, q_heads):  # noqa: F811
+    c = cache(heads=1)
+    p = ctypes.addressof(c)
+    assert lib.nf4_attention_workspace_bytes(p, batch, q_heads) == -1
+    assert lib.nf4_attention_decode(p, E, F, 4, F + 4096, batch, q_heads, 1.0, 0, E + 65536, F + (1 << 30), 1 << 30,
+                                    None) == SHAPE
+    assert lib.nf4_attention_workspace_bytes(p, 65535, 16384) > 0 and lib.nf4_attention_workspace_bytes(p, 0, 65535) > 0
