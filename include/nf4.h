@@ -268,7 +268,7 @@ typedef struct nf4_kv_cache {
     void* k_scales; /* device: NULL (BF16), float [pages][kv_heads][page_size] (FP8) or
                        fp16 bits [pages][kv_heads][page_size][head_dim/64] (NF4) */
     void* v_scales;
-    int64_t pages;     /* 0 .. 2^31-1 */
+    int64_t pages;     /* 0 .. 2^31-1, and pages * kv_heads * page_size at most 2^40 */
     int32_t kv_heads;  /* 1 .. 65535 */
     int32_t page_size; /* tokens a page: a multiple of 16, up to 65536 */
     int32_t head_dim;  /* 64, 128 or 256 */

@@ -18,6 +18,7 @@ constexpr int kMaxDevices = 64;
 // The last CUDA error this host thread saw inside the library (read by nf4_last_cuda_error).
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
 constexpr int64_t kMaxDim = 0x7FFFFFFF;
+constexpr int64_t kMaxVectors = int64_t{1} << 40;  // of one side of a cache
 
 // Per-device cache: 0 = unknown, -1 = unsupported, otherwise the SM count of a 10.3 device.
 std::atomic<int> g_device_sms[kMaxDevices];
@@ -73,6 +74,8 @@ nf4_status check_cache(const nf4_kv_cache* c) {
     if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return NF4_ERR_SHAPE;
     if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16 != 0) return NF4_ERR_SHAPE;
     if (c->kv_heads < 1 || c->kv_heads > 65535 || c->pages < 0 || c->pages > kMaxDim) return NF4_ERR_SHAPE;
+    // (at 32 bytes a vector or more no memory holds that many; the byte counts below fit 64 bits)
+    if (c->pages > kMaxVectors / (static_cast<int64_t>(c->kv_heads) * c->page_size)) return NF4_ERR_SHAPE;
     if (c->pages == 0) return NF4_OK;
     const bool scaled = c->format != NF4_KV_BF16;
     if (!c->k || !c->v || (scaled && (!c->k_scales || !c->v_scales))) return NF4_ERR_NULL;
