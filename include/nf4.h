@@ -351,7 +351,10 @@ nf4_status nf4_rope(const uint16_t* q, int64_t q_heads, const uint16_t* k, int64
  * nf4_rmsnorm - root-mean-square norm with the residual's addition: h = x + residual in fp32 (h = x
  * without one), residual_out = bf16_rn(h), y = h * rsqrt(mean(h^2) + eps) * weight in fp32, written as
  * bf16 (y, what nf4_linear reads) and / or in 8 bits: y8 = e4m3_rn(y / s) saturated at +-448 with one
- * fp32 scale s = max |y| / 448 a row (an all-zero row: s = 0, codes 0).
+ * fp32 scale s = max |y| / 448 a row.  An all-zero row gives zeros, s = 0 and codes 0, for eps = 0 too.
+ * The squares are summed in fp32 and max |y| is found as max |h * weight| times the row's factor, so rows
+ * with |h| past 2^63 / sqrt(H), or with |h * weight| past fp32's range, are outside the contract.  (The 8-bit
+ * output is for a caller's own 8-bit product: nf4_linear reads bf16.)
  *   x, residual    in   bf16 bits [T][H], H a positive multiple of 8; residual may be NULL
  *   weight         in   bf16 bits [H]
  *   residual_out   out  bf16 bits [T][H] or NULL; may be residual or x itself

@@ -177,6 +177,12 @@ __device__ __forceinline__ float2 block_sum_max(float2 v, float2* part) {
     return r;
 }
 
+// 1 / sqrt(mean square + eps); 0 for a zero row without an eps, so that it gives zeros and not 0 * inf.
+__device__ __forceinline__ float row_rstd(float square_sum, float inv_h, float eps) {
+    const float v = square_sum * inv_h + eps;
+    return v == 0.0f ? 0.0f : 1.0f / sqrtf(v);
+}
+
 struct NormArgs {
     const uint4 *x, *residual, *weight;
     uint4 *residual_out, *y;
@@ -283,8 +289,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
         }
     }
     acc = block_sum_max(acc, part);
-    const float rstd = 1.0f / sqrtf(acc.x * a.inv_h + a.eps);
-    const RowScale scale(acc.y * rstd / kFp8Max);
+    const float rstd = row_rstd(acc.x, a.inv_h, a.eps);
+    const RowScale scale(a.y8 ? acc.y * rstd / kFp8Max : 0.0f);
     if (a.y8 && threadIdx.x == 0) a.y8_scales[blockIdx.x] = scale.scale;
     if (CH) {
 #pragma unroll
@@ -375,8 +381,8 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_ring_kernel(const NormArgs a, 
         }
         issue(row + static_cast<int64_t>(kNormStages - 1) * gridDim.x);
         acc = block_sum_max(acc, part[flip]);
-        const float rstd = 1.0f / sqrtf(acc.x * a.inv_h + a.eps);
-        const RowScale scale(acc.y * rstd / kFp8Max);
+        const float rstd = row_rstd(acc.x, a.inv_h, a.eps);
+        const RowScale scale(a.y8 ? acc.y * rstd / kFp8Max : 0.0f);
         if (a.y8 && threadIdx.x == 0) a.y8_scales[row] = scale.scale;
 #pragma unroll
         for (int c = 0; c < kNormPieces; c++) {

@@ -38,3 +38,18 @@ def test_norm_scale_below_its_reciprocals_range(rows, width, top, eps):
     slack = 2.0 ** -18 * ratio.abs() + 2.0 ** -149 / s.t.double()[:, None]
     step = torch.maximum(2.0 ** -4 * ratio.abs(), torch.full_like(ratio, 2.0 ** -10))
     assert bool(((codes - ratio.clamp(-448, 448)).abs() <= step + slack).all())
+
+
+@pytest.mark.parametrize("rows,width", [(4, 64), (700, 2056), (2, 40000)])
+def test_norm_of_zero_rows_without_eps(rows, width):
+    """An all-zero row gives zeros, scale 0 and codes 0 for any eps, 0 too."""
+    x, w = randn((rows, width), 1), randn((width,), 2)
+    x[1] = 0
+    y, y8 = Guarded(x.shape, torch.bfloat16), Guarded(x.shape, torch.float8_e4m3fn)
+    s = Guarded((rows,), torch.float32)
+    nf4.nf4_rmsnorm(x, w, 0.0, y=y.t, y8=y8.t, y8_scales=s.t)
+    assert y.canaries_intact() and y8.canaries_intact() and s.canaries_intact()
+    assert not y.t[1].any() and not y8.t[1].float().any() and float(s.t[1]) == 0.0
+    h = x.double()
+    want = h / (h * h).mean(-1, keepdim=True).sqrt().clamp_min(1e-300) * w.double()
+    assert bool(((y.t.double() - want).abs() <= 2.0 ** -8 * want.abs()).all())
