@@ -337,7 +337,7 @@ nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, co
  *                       be 0 (its pointers are not used)
  *   positions      in   int32 [axes][T]
  *   sections       in   host array of `axes` (1..4) counts of pairs, each >= 0, sum rotary_dim / 2
- *   inv_freq       in   float [rotary_dim / 2] (finite)
+ *   inv_freq       in   float [rotary_dim / 2], any finite values
  *   rotary_dim     a multiple of 16, at most head_dim and 256; head_dim a multiple of 16, and
  *                  (q_heads + k_heads) * head_dim at most 2^24
  *   q_out, k_out   out  the same shapes; each may be its own input (in place), no other overlap

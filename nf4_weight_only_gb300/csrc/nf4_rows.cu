@@ -18,8 +18,8 @@ namespace {
 // held as a 64-bit binary fraction F of a turn; F * position modulo 2^64 is then the fraction of the product,
 // exactly, by integer wrap-around.  With inv_freq = m 2^e (m of 24 bits) F is the product of m and 2^64 / (2 pi),
 // shifted by e, all in integers (double precision here runs at a sixty-fourth of the single rate and took
-// half of the kernel's time); F's error, 2^-63 below inv_freq = 1, times the position is below 2^-31 turn.
-// The upper 32 bits of F * position, as a signed number, are an angle in [-pi, pi), where the hardware sine and
+// half of the kernel's time); F's error, 2^-63 below inv_freq = 1 (2^-55 below 256, 2^-64 above), times the position
+// is below 2^-31 turn (2^-24).  The upper 32 bits of F * position, as a signed number, are an angle in [-pi, pi), where the hardware sine and
 // cosine have an absolute error near 2^-21, far below the 2^-9 of the bf16 result.
 constexpr int kRopeThreads = 256;
 
@@ -27,10 +27,19 @@ struct Turn {
     float c[8], s[8];
 };
 
+// 1 / (2 pi) in binary, 32 bits a word, behind a word of zeros.
+__device__ __constant__ const uint32_t kInverseTwoPi[8] = {0x00000000u, 0x28BE60DBu, 0x9391054Au, 0x7F09D5F4u,
+                                                           0x7D4D3770u, 0x36D8A566u, 0x4F10E410u, 0x7F9458EAu};
+
+// |f| = m 2^e from 256 on, e in [-15, 104] (the reduction of Payne and Hanek, 1983): of 1 / (2 pi), the bits before
+// 2^-e give whole turns, and the 96 bits from there, times m, the fraction to 2^-64.
 // (Kept out of line: inlined, the compiler computes it for every pair and selects.)
-__device__ __noinline__ uint64_t turn_fraction_large(float f) {
-    const double turns = static_cast<double>(f) * 0.15915494309189533577;
-    return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
+__device__ __noinline__ uint64_t turn_fraction_large(uint32_t m, int e) {
+    const int word = (e + 32) >> 5, bit = (e + 32) & 31;
+    uint32_t g[3];
+#pragma unroll
+    for (int i = 0; i < 3; i++) g[i] = __funnelshift_l(kInverseTwoPi[word + i + 1], kInverseTwoPi[word + i], bit);
+    return m * ((static_cast<uint64_t>(g[0]) << 32) | g[1]) + ((static_cast<uint64_t>(m) * g[2]) >> 32);
 }
 
 // The fraction of a turn, times 2^64, that one position moves a pair of angular frequency f.
@@ -44,7 +53,7 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
         const int shift = e + 24;
         frac = shift >= 0 ? high << shift : shift > -64 ? high >> -shift : 0;
     } else {
-        frac = turn_fraction_large(__uint_as_float(bits));
+        frac = turn_fraction_large(static_cast<uint32_t>(m), e);
     }
     return f < 0.0f ? 0 - frac : frac;
 }

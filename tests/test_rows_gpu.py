@@ -53,3 +53,49 @@ def test_norm_of_zero_rows_without_eps(rows, width):
     h = x.double()
     want = h / (h * h).mean(-1, keepdim=True).sqrt().clamp_min(1e-300) * w.double()
     assert bool(((y.t.double() - want).abs() <= 2.0 ** -8 * want.abs()).all())
+
+
+def two_pi_inverse():
+    """floor(2^400 / (2 pi)), by Machin's formula for pi."""
+    bits = 700
+
+    def arctan_inverse(n):  # 2^bits * arctan(1 / n)
+        total, power, k = 0, (1 << bits) // n, 0
+        while power:
+            total += (-1) ** k * (power // (2 * k + 1))
+            power //= n * n
+            k += 1
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    return (1 << (400 + bits)) // (2 * pi)
+
+
+def turn(position, frequency):
+    """position * frequency radians as a fraction of a turn in [0, 1), in integers."""
+    n, d = float(frequency).as_integer_ratio()  # d: a power of two
+    return (position * n * two_pi_inverse() // d) % (1 << 400) / (1 << 400)
+
+
+FREQUENCIES = [255.0, 255.99998, 256.0, 257.5, 511.0, 1000.0, 65535.0, 1e6, 3.3e7, 1e10, 1e19, 1e25, 1e30, 2.0 ** 104, 1e38,
+               2.0 ** 127, 3.4028234e38, -256.0, -1e6, -3.4e38, 1.0, 0.0, 1e-30, 1e-45, -0.75, 2.0 ** 24 - 1, 16777215.0 * 64,
+               300.25, 1e3 / 3, 2e4, 7e8, 5e14]
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_of_large_frequencies(inter):
+    """The angle is the real product at any frequency and position: against integers of 400 bits."""
+    assert len(FREQUENCIES) == 32
+    positions = [0, 1, -1, 2, 3, 1000, 131071, 2 ** 31 - 1, -(2 ** 31), -98765]
+    inv = torch.tensor(FREQUENCIES, dtype=torch.float32)
+    angle = torch.tensor([[turn(p, f) for f in inv.tolist()] for p in positions], dtype=torch.float64, device=DEV)
+    cos, sin = (angle * 2 * torch.pi).cos()[:, None], (angle * 2 * torch.pi).sin()[:, None]
+    q, k = randn((len(positions), 3, 64), 1), randn((len(positions), 1, 64), 2)
+    at = torch.tensor([positions], dtype=torch.int32, device=DEV)
+    for x, got in zip((q, k), nf4.rope(q, k, at, inv.to(DEV), interleaved=inter)):
+        x, got = x.double(), got.double()
+        first, second = (slice(0, 64, 2), slice(1, 64, 2)) if inter else (slice(0, 32), slice(32, 64))
+        a, b = x[..., first], x[..., second]
+        slack = 2.0 ** -18 * (a.abs() + b.abs())
+        for want, part in ((a * cos - b * sin, first), (b * cos + a * sin, second)):
+            assert bool(((got[..., part] - want).abs() <= 2.0 ** -8 * want.abs() + slack).all())
