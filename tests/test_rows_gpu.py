@@ -99,3 +99,48 @@ def test_rope_of_large_frequencies(inter):
         slack = 2.0 ** -18 * (a.abs() + b.abs())
         for want, part in ((a * cos - b * sin, first), (b * cos + a * sin, second)):
             assert bool(((got[..., part] - want).abs() <= 2.0 ** -8 * want.abs() + slack).all())
+
+
+SMS = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 152
+
+
+@pytest.mark.parametrize("rows", [4 * SMS, 4 * SMS + 1, 9 * SMS + 5, 13 * SMS - 3])
+@pytest.mark.parametrize("width", [2048, 2056, 3080, 5120, 5128, 8184, 8192, 8200])
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_of_many_rows(rows, width, residual):
+    """Rows that go through persistent CTAs (more than 4 an SM, more than 2048 and up to 8192 wide), several a CTA with
+    an uneven last turn, and the neighbours of these limits: every output alone, all of them, and in place."""
+    x, w = randn((rows, width), 1), (1 + 0.2 * randn((width,), 2).float()).to(torch.bfloat16)
+    r = randn((rows, width), 3, 4.0) if residual else None
+    size = torch.exp2(((torch.arange(rows, device=DEV) * 7) % 19 - 9).float())[:, None]  # no two rows in turn alike
+    x = (x.float() * size).to(torch.bfloat16)
+    x[5] = 0
+    if residual:
+        r = (r.float() * size).to(torch.bfloat16)
+        r[5] = 0
+    h32 = x.float() + r.float() if residual else x.float()
+    h, eps = h32.double(), 1e-6
+    want = h / torch.sqrt((h * h).mean(-1, keepdim=True) + eps) * w.double()
+    s64 = want.abs().amax(-1) / 448
+    ro, y = Guarded(x.shape, torch.bfloat16), Guarded(x.shape, torch.bfloat16)
+    y8, sc = Guarded(x.shape, torch.float8_e4m3fn), Guarded((rows,), torch.float32)
+    nf4.nf4_rmsnorm(x, w, eps, residual=r, residual_out=ro.t, y=y.t, y8=y8.t, y8_scales=sc.t)
+    assert all(g.canaries_intact() for g in (ro, y, y8, sc))
+    assert torch.equal(ro.t, h32.to(torch.bfloat16))
+    # bf16's rounding, and 2^-20 for the fp32 sum, root and products
+    assert bool(((y.t.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want.abs()).all())
+    assert bool(((sc.t.double() - s64).abs() <= 2.0 ** -20 * s64).all())
+    step = torch.maximum(2.0 ** -4 * want.abs(), 2.0 ** -10 * s64[:, None])
+    assert bool(((y8.t.float().double() * sc.t.double()[:, None] - want).abs() <= step * (1 + 2.0 ** -10)).all())
+    # alone, and in place: the same bytes
+    one, one8, ones = torch.empty_like(x), torch.empty_like(y8.t), torch.empty_like(sc.t)
+    nf4.nf4_rmsnorm(x, w, eps, residual=r, y=one)
+    assert torch.equal(one, y.t)
+    nf4.nf4_rmsnorm(x, w, eps, residual=r, y8=one8, y8_scales=ones)
+    assert torch.equal(one8.view(torch.uint8), y8.t.view(torch.uint8)) and torch.equal(ones, sc.t)
+    a, b = x.clone(), None if r is None else r.clone()
+    nf4.nf4_rmsnorm(a, w, eps, residual=b, residual_out=b, y=a)
+    assert torch.equal(a, y.t) and (b is None or torch.equal(b, ro.t))
+    a = x.clone()
+    nf4.nf4_rmsnorm(a, w, eps, residual=r, residual_out=a, y8=one8, y8_scales=ones)
+    assert torch.equal(a, ro.t) and torch.equal(one8.view(torch.uint8), y8.t.view(torch.uint8))
