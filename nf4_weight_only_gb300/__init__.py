@@ -13,6 +13,7 @@ import functools
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 from typing import Optional
 
 import torch
@@ -115,11 +116,19 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
 _calls = None
 
 
+class _NoCalls:
+    """In the compiled calls' place where they were not built: every call goes through ctypes."""
+    append = read = attention = rope = rmsnorm = staticmethod(lambda *args: None)
+
+
 def _load_calls(lib: ctypes.CDLL) -> None:
     """The compiled short way into `lib` for the calls of a decode loop (csrc/nf4_python.c)."""
     global _calls
     if not os.path.exists(_build.CALLS_PATH):
-        raise RuntimeError(f"{_build.CALLS_PATH} is missing: build it with nf4_weight_only_gb300.build.build()")
+        warnings.warn(f"{_build.CALLS_PATH} was not built: cache, attention, rope and norm calls go through ctypes, "
+                      "which takes some microseconds more of the host's time", RuntimeWarning, stacklevel=3)
+        _calls = _NoCalls
+        return
     loader = importlib.machinery.ExtensionFileLoader("nf4_calls", _build.CALLS_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("nf4_calls", loader))
     loader.exec_module(module)
@@ -297,7 +306,7 @@ class _KvCacheStruct(ctypes.Structure):
 
 def _ready():
     """The compiled calls.  Each returns a status, or None for tensors that it does not take: the wrappers then go
-    through their own checks, which say what is wrong."""
+    through their own checks, which say what is wrong, and through ctypes."""
     if _calls is None:
         _load_calls(load())
     return _calls

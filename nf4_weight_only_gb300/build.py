@@ -1,12 +1,14 @@
 """Build libnf4.so (the CUDA kernels and the C ABI) in-tree for sm_103a with nvcc, and the binding's compiled
-calls (csrc/nf4_python.c) with the host compiler."""
+calls (csrc/nf4_python.c) with the host compiler, for the interpreter that runs this.  Where there is no C compiler or
+no Python.h, the library is built without them: the binding then makes the same calls through ctypes."""
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
-from typing import List
+from typing import List, Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -14,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libnf4.so")
-CALLS_PATH = os.path.join(BUILD_DIR, "nf4_calls.so")
+CALLS_PATH = os.path.join(BUILD_DIR, "nf4_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["nf4_api.cu", "nf4_quant.cu", "nf4_gemv.cu", "nf4_ring.cu", "nf4_kv.cu", "nf4_attn.cu",
            "nf4_rows.cu"]
@@ -35,10 +37,19 @@ def _inputs() -> List[str]:
     return files
 
 
+def _calls_command(out: str) -> Optional[List[str]]:
+    """What compiles the binding's calls, or None without a C compiler or Python's headers."""
+    cc, include = shutil.which(os.environ.get("CC", "gcc")), sysconfig.get_paths()["include"]
+    if cc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    return [cc, "-O2", "-shared", "-fPIC", "-I", include, os.path.join(CSRC, "nf4_python.c"), "-lm", "-o", out]
+
+
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
+    built = [LIB_PATH] + ([CALLS_PATH] if _calls_command(CALLS_PATH) else [])
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -50,9 +61,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
     nvcc = _nvcc()
     procs, objs = [], []
     calls_tmp = CALLS_PATH + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
-           os.path.join(CSRC, "nf4_python.c"), "-lm", "-o", calls_tmp]
-    procs.append(("nf4_python.c", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    calls = _calls_command(calls_tmp)
+    if calls:
+        procs.append(("nf4_python.c",
+                      subprocess.Popen(calls, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    else:
+        print("no C compiler or no Python.h: the binding's compiled calls are left out", file=sys.stderr)
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
@@ -72,7 +86,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB_PATH)
-    os.replace(calls_tmp, CALLS_PATH)
+    if calls:
+        os.replace(calls_tmp, CALLS_PATH)
     return LIB_PATH
 
 
