@@ -19,7 +19,7 @@
  *
  * Common rules for every entry point:
  *   - Pointers are device pointers owned by the caller, row-major and contiguous, each aligned to
- *     16 bytes.  bf16 and fp16 values travel as their 16-bit patterns (uint16_t).
+ *     16 bytes where nothing else is said.  bf16 and fp16 values travel as their 16-bit patterns (uint16_t).
  *   - Calls are asynchronous on `stream` (0 = the legacy default stream).  No call synchronises
  *     the device, allocates memory or keeps state beyond a per-device capability check, except the
  *     ring calls of the overflow-streaming section, which own explicitly created state.  (The
@@ -62,7 +62,7 @@ typedef enum nf4_status {
     NF4_OK = 0,
     NF4_ERR_NULL = 1,               /* a required pointer is NULL */
     NF4_ERR_SHAPE = 2,              /* negative size, K not a positive multiple of 64, or > 2^31-1 */
-    NF4_ERR_ALIGN = 3,              /* a pointer is not 16-byte aligned */
+    NF4_ERR_ALIGN = 3,              /* a pointer is not aligned as its call asks (16 bytes) */
     NF4_ERR_ALIAS = 4,              /* an output range overlaps an input range */
     NF4_ERR_UNSUPPORTED_DEVICE = 5, /* the current device is not compute capability 10.3 (sm_103) */
     NF4_ERR_CUDA = 6,               /* a CUDA runtime call or kernel launch failed */
@@ -306,6 +306,7 @@ nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t 
  * new token's own key and value are in the cache before the call.
  *   q           in   bf16 bits [B][q_heads][head_dim]; q_heads a multiple of kv_heads
  *   page_table  in   int32 [B][max_pages]; entries past a sequence's length do not matter
+ *                    (page_table and lengths need the alignment of an int32 only: a batch may be cut)
  *   lengths     in   int32 [B]; a negative length counts as 0.  A length past max_pages * page_size is
  *                    cut there, and a needed page outside [0, pages) is left out of the sum; both
  *                    record code 43 in the device error word.
@@ -335,7 +336,7 @@ nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, co
  * bf16; elements past rotary_dim are copied.
  *   q, k           in   bf16 bits [T][q_heads][head_dim], [T][k_heads][head_dim]; either head count may
  *                       be 0 (its pointers are not used)
- *   positions      in   int32 [axes][T]
+ *   positions      in   int32 [axes][T] (aligned to an int32)
  *   sections       in   host array of `axes` (1..4) counts of pairs, each >= 0, sum rotary_dim / 2
  *   inv_freq       in   float [rotary_dim / 2], any finite values
  *   rotary_dim     a multiple of 16, at most head_dim and 256; head_dim a multiple of 16, and

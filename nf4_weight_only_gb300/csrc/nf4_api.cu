@@ -24,6 +24,7 @@ constexpr int64_t kMaxVectors = int64_t{1} << 40;  // of one side of a cache
 std::atomic<int> g_device_sms[kMaxDevices];
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -345,8 +346,8 @@ nf4_status nf4_attention_decode(const nf4_kv_cache* cache, const uint16_t* q, co
     if (max_pages > 0 && B > (int64_t{1} << 35) / (max_pages * cache->page_size)) return NF4_ERR_SHAPE;
     if (B == 0) return NF4_OK;
     if (!q || !lengths || !out || !workspace || (max_pages > 0 && !page_table)) return NF4_ERR_NULL;
-    if (!aligned16(q) || !aligned16(lengths) || !aligned16(out) || !aligned16(workspace) || !aligned16(page_table))
-        return NF4_ERR_ALIGN;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return NF4_ERR_ALIGN;
+    if (!aligned4(lengths) || !aligned4(page_table)) return NF4_ERR_ALIGN;
     const int64_t need = nf4::attention_workspace_bytes(cache->kv_heads, cache->head_dim, B, q_heads);
     if (workspace_bytes < need) return NF4_ERR_SHAPE;
     const Ranges r = cache_ranges(cache);
@@ -389,8 +390,9 @@ nf4_status nf4_rope(const uint16_t* q, int64_t q_heads, const uint16_t* k, int64
     const void* ins[4] = {positions, inv_freq, q_heads ? q : nullptr, k_heads ? k : nullptr};
     const void* outs[2] = {q_heads ? q_out : nullptr, k_heads ? k_out : nullptr};
     const int64_t in_bytes[4] = {axes * T * 4, rotary_dim * 2, T * q_heads * head_dim * 2, T * k_heads * head_dim * 2};
-    for (const void* p : ins)
-        if (!aligned16(p)) return NF4_ERR_ALIGN;
+    if (!aligned4(positions)) return NF4_ERR_ALIGN;
+    for (int i = 1; i < 4; i++)
+        if (!aligned16(ins[i])) return NF4_ERR_ALIGN;
     for (const void* p : outs)
         if (!aligned16(p)) return NF4_ERR_ALIGN;
     for (int o = 0; o < 2; o++)
