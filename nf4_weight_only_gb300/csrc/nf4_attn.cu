@@ -1290,15 +1290,8 @@ cudaError_t launch(const AttnArgs& a, int num_sms, cudaStream_t stream) {
     if (grid > useful) grid = useful;
     if (grid < 1) grid = 1;
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(S::W * 32);
+    cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(grid)), S::W * 32, stream, &attr);
     cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attention_kernel<FMT, D, NT>, a);
 }
 

@@ -11,24 +11,12 @@ constexpr int kGroup = 64;  // weights per scale group (deep-fold README, format
 
 // The NormalFloat-4 table published with QLoRA (Dettmers et al., 2023, appendix), index 0..15.
 // The published literals are the definition; each is an exact binary32 number.
-__device__ __constant__ static const float kNF4[16] = {
-    -1.0f,
-    -0.6961928009986877f,
-    -0.5250730514526367f,
-    -0.39491748809814453f,
-    -0.28444138169288635f,
-    -0.18477343022823334f,
-    -0.09105003625154495f,
-    0.0f,
-    0.07958029955625534f,
-    0.16093020141124725f,
-    0.24611230194568634f,
-    0.33791524171829224f,
-    0.44070982933044434f,
-    0.5626170039176941f,
-    0.7229568362236023f,
-    1.0f,
-};
+#define NF4_TABLE_VALUES                                                                                  \
+    { -1.0f, -0.6961928009986877f, -0.5250730514526367f, -0.39491748809814453f,                           \
+      -0.28444138169288635f, -0.18477343022823334f, -0.09105003625154495f, 0.0f,                          \
+      0.07958029955625534f, 0.16093020141124725f, 0.24611230194568634f, 0.33791524171829224f,             \
+      0.44070982933044434f, 0.5626170039176941f, 0.7229568362236023f, 1.0f }
+__device__ __constant__ static const float kNF4[16] = NF4_TABLE_VALUES;
 
 // ---------------------------------------------------------------------------------------------
 // Thin PTX wrappers

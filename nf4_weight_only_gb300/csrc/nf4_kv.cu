@@ -27,11 +27,7 @@ constexpr float next_up(float x) {
     return up;
 }
 constexpr Thresholds nf4_thresholds() {
-    constexpr float table[16] = {-1.0f, -0.6961928009986877f, -0.5250730514526367f, -0.39491748809814453f,
-                                 -0.28444138169288635f, -0.18477343022823334f, -0.09105003625154495f, 0.0f,
-                                 0.07958029955625534f, 0.16093020141124725f, 0.24611230194568634f,
-                                 0.33791524171829224f, 0.44070982933044434f, 0.5626170039176941f,
-                                 0.7229568362236023f, 1.0f};
+    constexpr float table[16] = NF4_TABLE_VALUES;
     Thresholds r{};
     for (int i = 0; i < 15; i++) {
         const float lo = table[i], hi = table[i + 1];
@@ -294,18 +290,6 @@ __global__ void __launch_bounds__(256) read_kernel(KvCache c, const int64_t* __r
             __stcs(reinterpret_cast<uint4*>(out) + i * L + l, o);
         }
     }
-}
-
-cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
-    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr->val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
 }
 
 // Up to 8 CTAs an SM; more than one step only with a width that the heads divide.

@@ -1,4 +1,4 @@
-// The paged key-value cache's formats as the kernels see them (cache and attention kernels).
+// The paged key-value cache's formats as the kernels see them, and what the kernels around the linears share.
 #pragma once
 
 #include <cstdint>
@@ -39,6 +39,19 @@ __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+
+// A launch that may begin before the previous kernel of the stream has ended (its kernels wait before they read).
+inline cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 }  // namespace nf4

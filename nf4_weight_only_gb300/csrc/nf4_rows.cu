@@ -201,32 +201,23 @@ struct NormArgs {
     float inv_h, eps;
 };
 
-__device__ __forceinline__ void load_h(const NormArgs& a, int64_t at, float (&h)[8]) {
-    const uint4 x = a.x[at];
+__device__ __forceinline__ void unpack(const uint4& x, float (&h)[8]) {
     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const float2 f = bf16x2_to_f32x2(xs[j]);
         h[2 * j] = f.x, h[2 * j + 1] = f.y;
     }
-    if (a.residual) {
-        const uint4 r = a.residual[at];
-        const uint32_t rs[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = bf16x2_to_f32x2(rs[j]);
-            h[2 * j] += f.x, h[2 * j + 1] += f.y;
-        }
-    }
 }
 
-__device__ __forceinline__ void load_w(const NormArgs& a, int i, float (&w)[8]) {
-    const uint4 x = a.weight[i];
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+// x + residual of a piece.
+__device__ __forceinline__ void load_h(const NormArgs& a, int64_t at, float (&h)[8]) {
+    unpack(a.x[at], h);
+    if (a.residual) {
+        float r[8];
+        unpack(a.residual[at], r);
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float2 f = bf16x2_to_f32x2(xs[j]);
-        w[2 * j] = f.x, w[2 * j + 1] = f.y;
+        for (int j = 0; j < 8; j++) h[j] += r[j];
     }
 }
 
@@ -273,7 +264,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
     float2 acc = make_float2(0.0f, 0.0f);
     auto add = [&](const float (&v)[8], int i) {
         float w[8];
-        if (a.y8) load_w(a, i, w);
+        if (a.y8) unpack(a.weight[i], w);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             acc.x = fmaf(v[j], v[j], acc.x);
@@ -307,7 +298,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
             const int i = threadIdx.x + c * blockDim.x;
             if (i < a.vecs) {
                 float w[8];
-                load_w(a, i, w);
+                unpack(a.weight[i], w);
                 store_out(a, row + i, h[c], w, rstd, scale);
             }
         }
@@ -315,22 +306,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormArgs a) {
         for (int i = threadIdx.x; i < a.vecs; i += blockDim.x) {
             float w[8];
             load_h(a, row + i, h[0]);
-            load_w(a, i, w);
+            unpack(a.weight[i], w);
             store_out(a, row + i, h[0], w, rstd, scale);
         }
     }
 }
 
 constexpr int kNormStages = 3;
-
-__device__ __forceinline__ void unpack(const uint4& x, float (&h)[8]) {
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        const float2 f = bf16x2_to_f32x2(xs[j]);
-        h[2 * j] = f.x, h[2 * j + 1] = f.y;
-    }
-}
 
 constexpr int kNormPieces = 2;  // 16-byte pieces of a row a thread
 
@@ -402,18 +384,6 @@ __global__ void __launch_bounds__(512, 2) rmsnorm_ring_kernel(const NormArgs a, 
             store_out(a, row * a.vecs + i, h[c], v, rstd, scale);
         }
     }
-}
-
-cudaLaunchConfig_t pdl_config(dim3 grid, int threads, cudaStream_t stream, cudaLaunchAttribute* attr) {
-    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr->val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
 }
 
 }  // namespace
