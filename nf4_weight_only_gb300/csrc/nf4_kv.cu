@@ -141,8 +141,10 @@ __device__ __forceinline__ void quantise8(const uint4& w, uint32_t column, uint3
     for (int o = 1; o < (FMT == kKvNf4 ? 8 : D / 8); o <<= 1) s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, o));
     if (FMT == kKvFp8) {
         scale = s = __fdiv_rn(s, kFp8Max);
-        divide8(x, s);
-        const uint32_t keep = s > 0.0f ? 0xFFFFFFFFu : 0u;  // a scale of 0: every code is 0
+        // A scale of 0: every code is 0.  (Divided by, it would take the slow path of the division, in lanes without an
+        // item, too: one token 3.3 us, so 1.8; 4099 tokens of 8 heads 7.8 and 6.7.)
+        const uint32_t keep = s > 0.0f ? 0xFFFFFFFFu : 0u;
+        divide8(x, s > 0.0f ? s : 1.0f);
         out[0] = (f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16)) & keep;
         out[1] = (f32x2_to_e4m3x2(x[4], x[5]) | (f32x2_to_e4m3x2(x[6], x[7]) << 16)) & keep;
     } else {
