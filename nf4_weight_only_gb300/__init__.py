@@ -314,6 +314,8 @@ def _ready():
 
 def _expect(t: torch.Tensor, name: str, dtype, shape) -> int:
     """The address of a contiguous CUDA tensor of exactly this type and shape (or ValueError)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: want a tensor, got {type(t).__name__}")
     if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
         return t.data_ptr()
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():

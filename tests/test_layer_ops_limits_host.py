@@ -50,3 +50,22 @@ def test_integers_of_a_cut_batch(lib):  # noqa: F811
         assert rope(C + off) in (5, 6)
     for off in (1, 2, 6):
         assert attention(F + off, F + 4096) == ALIGN and attention(F, F + 4096 + off) == ALIGN and rope(C + off) == ALIGN
+
+
+def test_outputs_that_are_left_out(monkeypatch):
+    """A missing output is a ValueError that names it."""
+    import nf4_weight_only_gb300 as nf4
+    from nf4_weight_only_gb300 import build
+    build.build()
+    q, f = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(32)
+    positions = torch.zeros(1, 1, dtype=torch.int32)
+    real = nf4._expect
+    # CPU tensors pass, so that the missing one is what is met
+    monkeypatch.setattr(nf4, "_expect", lambda t, *a: 0 if isinstance(t, torch.Tensor) else real(t, *a))
+    with pytest.raises(ValueError, match="q_out: want a tensor"):
+        nf4.nf4_rope(q, None, positions, f, None, None)
+    with pytest.raises(ValueError, match="k_out: want a tensor"):
+        nf4.nf4_rope(None, q, positions, f, None, None)
+    with pytest.raises(ValueError, match="out: want a tensor"):
+        cache = type("Cache", (), {"_address": 0, "head_dim": 64})
+        nf4.nf4_attention_decode(cache, q, positions, positions[0], None, torch.zeros(16, dtype=torch.uint8))
