@@ -301,7 +301,7 @@ nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t 
  * nf4_attention_decode - attention of one new token a sequence over the cache:
  *   out[b][h] = sum_j p_j v_j,  p = softmax_j(scale * q[b][h] . k_j),
  * j over places max(0, lengths[b] - window) .. lengths[b] - 1 of sequence b (window = 0: from 0),
- * k_j and v_j the cache's values (not rounded to bf16) of kv head h / (q_heads / kv_heads); place j
+ * k_j and v_j the cache's values (not rounded to bf16; see below) of kv head h / (q_heads / kv_heads); place j
  * is in page page_table[b][j / page_size].  A sequence with nothing to attend to gives zeros.  The
  * new token's own key and value are in the cache before the call.
  *   q           in   bf16 bits [B][q_heads][head_dim]; q_heads a multiple of kv_heads
@@ -316,6 +316,14 @@ nf4_status nf4_kv_read(const nf4_kv_cache* cache, const int64_t* slots, int64_t 
  *               call leaves it fit for the next one.  Calls that may overlap on the GPU need a
  *               workspace each; one workspace serves calls of different sizes as long as it is large
  *               enough for each.
+ * Scores, softmax statistics and sums are fp32.  Rounded to fewer bits on the way:
+ *   bf16  p, to the sum of two bf16 numbers (2^-16 of it)
+ *   fp8   p * scale of V, to fp16 (2^-11 of it, or 2^-31 of the largest scale of V met, if that is more)
+ *   NF4   the same; and the 16 table values, of K and of V, to fp16: each within 6.4e-4 of its value,
+ *         rounded so that the errors cancel in a mean over values alike on both sides of zero (below 2.5e-6
+ *         of their mean size; up to 1.8e-4 of it for values all on one side, 6e-5 for skewed ones around
+ *         zero: nf4_kv_read has the values without that)
+ *   q, with fp8 and NF4: elements below 2^-28 of their head's largest
  * Values in places that are not attended to (past a length, before the window) do not matter, NaN
  * and infinities included.  NF4_ERR_SHAPE also for B > 65535, q_heads > 65535, B * q_heads > 2^30,
  * max_pages * page_size >= 2^31, B * max_pages * page_size > 2^35 and for a workspace_bytes below the

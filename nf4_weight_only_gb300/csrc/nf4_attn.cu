@@ -9,14 +9,20 @@
 // cache: the dims of a product's k axis may be permuted at will (q is permuted alike), and so may the
 // keys.  tcgen05 takes 64 or 128 rows from shared or tensor memory in canonical tiles; here the rows are in
 // pages of 16 and more, quantised, a tile would be used once, for eight columns, and the tensor pipe is busy
-// for 12 to 20% of the time as it is.
+// for 14 to 20% of the time as it is.
 //
-// What bounds it, measured on GB300 (DRAM copy rate 6774 GB/s): with a bf16 cache the memory (64 sequences up to
-// 8192, 8 kv heads: 182 us, 99% of that rate; one of 131071: 85 us, 94%); with fp8 the same for many sequences
-// (98 us, 95%) and the latency of a ring of two stages for one (48 us, 86%); with NF4 the decoding: 64 table
-// lookups of 81 shared-memory reads and 340 instructions for 16 keys (32 sequences up to 16384: 75 us, 63%;
-// one of 131071: 39 us, 54%); short calls the chain of dependent loads (lengths, page table, data, partial
-// results): 5 us for one sequence of 128 tokens, 12 us for 8 of up to 4095.
+// What bounds it, measured on GB300 (DRAM copy rate 6774 GB/s; 8 kv heads of 5 query heads, head_dim 128):
+//   bf16   the memory (64 sequences up to 8192: 183 us, 98% of that rate; one of 131071: 85 us, 93%)
+//   fp8    the same for many sequences (99 us, 94%), the latency of a ring of two stages for one (48 us, 86%)
+//   NF4    the latency of decoding, no pipe being full (LSU 60%, issue 54%, ALU 42%, tensor 20%): 340 instructions
+//          for 16 keys, 81 of them shared-memory reads, in a chain lookup, product, softmax, lookup, product, with three
+//          warps a scheduler to cover it (32 sequences up to 16384: 74 us, 63%; one of 131071: 39 us, 55%)
+//   short  one sequence of 517 tokens and 2 kv heads, bf16, 7.8 us: its segments are not cut, so two SMs read 265 KB
+//          each (2 us at 64 bytes a clock) in four rounds of their rings, after lengths and page table; 8
+//          sequences of up to 4095 in fp8 12 us: the longest one's pieces and their join
+// More than eight query heads a kv head (NT = 2) take 249 to 255 registers, so eight warps of fp8 and NF4 in place of
+// twelve: the 32 sequences with 12 heads take 114 us in NF4 (5 heads: 74), 107 in fp8 (96), 184 in bf16 (178).  With
+// head_dim 256 they also spill 248 to 304 bytes: 274 us (5 heads: 149), 222 (190), 372 (348).  The main fp8 form spills 8.
 //
 // Quantised formats stay codes until they are fragments.  fp8 codes convert to fp16 exactly; an NF4 byte (two
 // codes) indexes a table of fp16 pairs in shared memory (see kTableF16).  The scales are applied in fp32: K's to
@@ -159,7 +165,8 @@ __device__ __forceinline__ uint64_t l2_policy(bool stream) {
 // mean shows: 1% of the result at 131071 keys.  The unit and the direction of each entry's rounding are
 // therefore chosen together (enumerated over all fp16 units and all 2^13 directions) so that the mean error
 // is below 2.5e-6 of the values' size for normal, Laplace and uniform values of any width against their
-// group's maximum; each entry stays within one fp16 step (2^-10.6 relative), 2.8e-4 in the mean square.
+// group's maximum; each entry stays within one fp16 step (6.4e-4 relative), 2.8e-4 in the mean square.  For values
+// all on one side of zero it is up to 1.8e-4, for skewed ones around zero 6e-5 (exponential less its mean).
 constexpr float kTableUnit = 1307.0f / 2048.0f;
 __device__ __constant__ const float kTableF16[16] = {
     -0.63818359375f,   -0.4443359375f,    -0.335205078125f,  -0.251953125f,   -0.181640625f,  -0.117919921875f,
