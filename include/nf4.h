@@ -375,13 +375,120 @@ nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
                        cudaStream_t stream);
 
 /*
+ * Operators of a server that decodes for many requests at once: the indices of a step, made on the GPU from
+ * the requests' lengths; the requests' own low-rank adapters beside the packed projections; the choice of the
+ * next token.  With nf4_embed, the layers above and nf4_linear for the output head they close the loop:
+ * plan, embed, layers, head, sample, and the sampled tokens are the next step's ids.  The common rules hold.
+ */
+
+/*
+ * nf4_plan_step - the indices of a step: pages handed out and taken back, and the place, position and
+ * sequence of every new token.  Sequence b holds lengths[b] tokens in ceil(lengths[b] / page_size) pages and
+ * brings new_tokens[b] more: 1 when it decodes, a piece of its prompt, 0 when it waits; a negative number
+ * says that it is finished: its pages go back and its length becomes 0.  The new tokens are rows of the step's
+ * batch in the order of the sequences, starts[b] being the first of sequence b.
+ * Free pages are a ring of `pages` entries, free_in[0] the first one and free_in[1] how many there are.  Pages
+ * given back go to the ring's end, in order, and may be handed out in the same step; new pages come from its
+ * beginning, in the order of the sequences.  A sequence is refused (its length stays, its new tokens get no
+ * place) if its tokens pass row T, if its pages pass max_pages, or if it needs new pages and the ring does not
+ * hold all that it and the sequences before it need.
+ *   lengths      in   int32 [B]; a negative one counts as 0
+ *   new_tokens   in   int32 [B]
+ *   page_size    16 .. 65536, a multiple of 16 (nf4_kv_cache)
+ *   pages        entries of the ring and pages of the cache, 0 .. 2^31-1
+ *   page_table   in/out int32 [B][max_pages]: entries of new pages are written, no others; those of a
+ *                finished sequence stay as they are
+ *   free_pages   in/out int32 [pages]: entries behind the ring's end are written
+ *   free_in      in   int64 [2]
+ *   free_out     out  int64 [2]; may be free_in
+ *   lengths_out  out  int32 [B]; may be lengths
+ *   starts       out  int32 [B + 1]; starts[B] is the number of new tokens (which must be below 2^31)
+ *   slots        out  int64 [T], what nf4_kv_append takes: page * page_size + offset; -1 for the tokens of a
+ *                     refused sequence and for rows from starts[B] on
+ *   positions    out  int32 [T], lengths[b] + i for token i of sequence b; 0 from row starts[B] on
+ *   sequences    out  int32 [T], b; -1 from row starts[B] on
+ * All of them are aligned to their elements at least (not to 16 bytes).  B at most 8192, T at most 2^31 - 1, B *
+ * max_pages at most 2^40.  A page outside [0, pages) where a token goes gives the place -1, a ring's state outside
+ * the ring is cut to it, pages that the ring has no room for are lost: each records code 45 in the device error word.
+ */
+nf4_status nf4_plan_step(const int32_t* lengths, const int32_t* new_tokens, int64_t B, int64_t page_size, int64_t pages,
+                         int32_t* page_table, int64_t max_pages, int32_t* free_pages, const int64_t* free_in,
+                         int64_t* free_out, int32_t* lengths_out, int32_t* starts, int64_t T, int64_t* slots,
+                         int32_t* positions, int32_t* sequences, cudaStream_t stream);
+
+/*
+ * nf4_lora_plan - the tokens of a step, listed adapter by adapter.  Made once for all nf4_lora calls with the same
+ * tokens (every projection of every layer).
+ *   ids        in   int32 [T], the adapter of each token; negative: none.  With `sequences`: int32 [S], the
+ *                   adapter of each sequence
+ *   sequences  in   NULL, or int32 [T], the sequence of each token (as nf4_plan_step gives it); negative: no
+ *                   adapter
+ *   T          0 .. 2^24;  adapters  0 .. 8192 that are loaded
+ *   plan       out  nf4_lora_plan_bytes(T, adapters) bytes on the device, 16-byte aligned
+ * An id >= adapters, or a sequence >= S, counts as none and records code 46 in the device error word.
+ * nf4_lora_plan_bytes gives -1 for sizes that are refused.
+ */
+int64_t nf4_lora_plan_bytes(int64_t T, int64_t adapters);
+nf4_status nf4_lora_plan(const int32_t* ids, const int32_t* sequences, int64_t S, int64_t T, int64_t adapters, void* plan,
+                         int64_t plan_bytes, cudaStream_t stream);
+
+/*
+ * nf4_lora - low-rank adapters of many requests beside up to 8 projections that share their input:
+ *   ys[i][t] = bf16_rn(bases[i][t] + scales[a] * sum_r b[i][a][:, r] h_r),  h_r = sum_k a[i][a][r, k] x[t, k]
+ * for a token t with adapter a; without one, ys[i][t] = bases[i][t] (rows that are in place are not touched).
+ *   x          in   bf16 bits [T][K], K a positive multiple of 64
+ *   plan       in   from nf4_lora_plan with the same T and adapters
+ *   rank       of all adapters: a multiple of 8, 8 .. 128 (pad a smaller one with zeros)
+ *   scales     in   float [adapters]
+ *   count      1 .. 8
+ *   a          host array of count device pointers; a[i]: bf16 bits [adapters][rank][K]
+ *   b          host array; b[i]: bf16 bits [adapters][Ns[i]][rank]
+ *   bases      host array; bases[i]: bf16 bits [T][Ns[i]] (what nf4_linear_grouped gave); NULL: ys
+ *   ys         host array; ys[i]: bf16 bits [T][Ns[i]]; may be its own base, no other overlap
+ *   workspace  nf4_lora_workspace_bytes(T, adapters, rank, count) bytes on the device; needs no set-up.  Calls that
+ *              may overlap on the GPU need one each
+ * Sums are fp32; scales[a] * h_r goes into the second product as the sum of two bf16 numbers (2^-16 of it).  The
+ * host arrays are read before the call returns.  A plan of other sizes records code 47, and nothing is computed.
+ */
+int64_t nf4_lora_workspace_bytes(int64_t T, int64_t adapters, int64_t rank, int64_t count);
+nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, int64_t plan_bytes, int64_t adapters,
+                    int64_t rank, const float* scales, int count, const uint16_t* const* a, const uint16_t* const* b,
+                    const uint16_t* const* bases, uint16_t* const* ys, const int64_t* Ns, void* workspace,
+                    int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * nf4_sample - the next token of every row of logits, from a given random number.  With l the row's logits and T
+ * its temperature, token i has the weight w_i = exp((l_i - max l) / T).  Tokens are ordered by l, equal ones by
+ * index.  Of that order are kept: the first top_k; of these the smallest number whose weights reach top_p of
+ * theirs; of these the ones with w_i >= min_p; the first token always.  The token drawn is the first i, in order of
+ * index, for which the kept weights up to i pass random * (their sum).  T = 0 (or below 2^-100): the first of
+ * the largest logits.
+ *   logits       in   [B][stride], the first V of a row used; bf16 bits (logits_bf16 != 0; what nf4_linear gives) or
+ *                     float
+ *   temperature  in   float [B], NULL: 1
+ *   top_k        in   int32 [B]; 0 or less, V or more: all.  NULL: all
+ *   top_p        in   float [B]; 1 or more: all.  NULL: all
+ *   min_p        in   float [B]; 0 or less: all.  NULL: all
+ *   random       in   float [B] in [0, 1)
+ *   tokens       out  int32 [B]
+ *   logprobs     out  float [B] or NULL: log softmax(l) of the token, before temperature and cuts
+ * V in 1 .. 262144, stride >= V, B at most 2^24; everything is aligned to its elements (rows may start anywhere).
+ * Logits of -inf (masked) and NaN have no weight; a row with nothing else gives token -1 and logprob -inf.  Weights
+ * are whole multiples of 2^-40 (each within 2^-37), so sums are exact and the drawn token does not depend on their order.
+ */
+nf4_status nf4_sample(const void* logits, int logits_bf16, int64_t B, int64_t V, int64_t stride, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p, const float* random, int32_t* tokens,
+                      float* logprobs, cudaStream_t stream);
+
+/*
  * nf4_check_device_error - diagnostics: read and clear the device-side error words of the current
  * device.  The linear kernels bound every pipeline wait (one second of wall-clock time per wait,
  * see nf4_diag_set_wait_limit); a wait that runs out records a nonzero code (1..39; 39 is
  * nf4_diag_bounded_wait's), and the kernel drains and exits instead of hanging, leaving its outputs
  * unspecified.  nf4_embed records 41 for an id outside the table, the cache calls 42 for a slot
  * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds (44: a
- * shared-memory layout that its kernel does not know; nothing is computed then).  *code receives the
+ * shared-memory layout that its kernel does not know; nothing is computed then), nf4_plan_step 45,
+ * nf4_lora_plan 46 and nf4_lora 47 (see there).  *code receives the
  * first recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
  */
 nf4_status nf4_check_device_error(int* code);

@@ -32,7 +32,8 @@ STATUS_NAMES = {0: "NF4_OK", 1: "NF4_ERR_NULL", 2: "NF4_ERR_SHAPE", 3: "NF4_ERR_
 # Every symbol include/nf4.h declares.
 EXPORTED = ("nf4_quantize", "nf4_dequant", "nf4_linear", "nf4_linear_grouped", "nf4_embed",
             "nf4_kv_append", "nf4_kv_read", "nf4_attention_workspace_bytes", "nf4_attention_decode", "nf4_rope",
-            "nf4_rmsnorm", "nf4_ring_create", "nf4_ring_run", "nf4_ring_destroy", "nf4_linear_host_noalloc",
+            "nf4_rmsnorm", "nf4_plan_step", "nf4_lora_plan_bytes", "nf4_lora_plan", "nf4_lora_workspace_bytes",
+            "nf4_lora", "nf4_sample", "nf4_ring_create", "nf4_ring_run", "nf4_ring_destroy", "nf4_linear_host_noalloc",
             "nf4_check_device_error", "nf4_diag_bounded_wait", "nf4_diag_set_wait_limit", "nf4_status_str",
             "nf4_abi_version", "nf4_noalloc_slot_bytes", "nf4_last_cuda_error")
 
@@ -86,6 +87,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.nf4_rope.restype = ci
     lib.nf4_rmsnorm.argtypes = [vp, vp, vp, i64, i64, cf, vp, vp, vp, vp, vp]
     lib.nf4_rmsnorm.restype = ci
+    lib.nf4_plan_step.argtypes = [vp, vp, i64, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp]
+    lib.nf4_plan_step.restype = ci
+    lib.nf4_lora_plan_bytes.argtypes = [i64, i64]
+    lib.nf4_lora_plan_bytes.restype = i64
+    lib.nf4_lora_plan.argtypes = [vp, vp, i64, i64, i64, vp, i64, vp]
+    lib.nf4_lora_plan.restype = ci
+    lib.nf4_lora_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.nf4_lora_workspace_bytes.restype = i64
+    lib.nf4_lora.argtypes = [vp, i64, i64, vp, i64, i64, i64, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.nf4_lora.restype = ci
+    lib.nf4_sample.argtypes = [vp, ci, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.nf4_sample.restype = ci
     lib.nf4_ring_create.argtypes = [i64, ctypes.POINTER(ctypes.c_void_p)]
     lib.nf4_ring_create.restype = ci
     lib.nf4_ring_run.argtypes = [vp, vp, i64, vp]
@@ -118,7 +131,7 @@ _calls = None
 
 class _NoCalls:
     """In the compiled calls' place where they were not built: every call goes through ctypes."""
-    append = read = attention = rope = rmsnorm = staticmethod(lambda *args: None)
+    append = read = attention = rope = rmsnorm = plan_step = lora_plan = lora = sample = staticmethod(lambda *args: None)
 
 
 def _load_calls(lib: ctypes.CDLL) -> None:
@@ -132,7 +145,8 @@ def _load_calls(lib: ctypes.CDLL) -> None:
     loader = importlib.machinery.ExtensionFileLoader("nf4_calls", _build.CALLS_PATH)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("nf4_calls", loader))
     loader.exec_module(module)
-    functions = (lib.nf4_kv_append, lib.nf4_kv_read, lib.nf4_attention_decode, lib.nf4_rope, lib.nf4_rmsnorm)
+    functions = (lib.nf4_kv_append, lib.nf4_kv_read, lib.nf4_attention_decode, lib.nf4_rope, lib.nf4_rmsnorm,
+                 lib.nf4_plan_step, lib.nf4_lora_plan, lib.nf4_lora, lib.nf4_sample)
     module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in functions), torch.bfloat16, torch.float8_e4m3fn,
                 torch.float32, torch.int32, torch.int64, torch.uint8, _raw_stream, _current_device)
     _calls = module
@@ -513,7 +527,148 @@ def nf4_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Opt
                               _current(stream)), "nf4_rmsnorm")
 
 
+# ---------------------------------------------------------------------------------------------
+# Operators of a server that decodes for many requests at once
+# ---------------------------------------------------------------------------------------------
+def _maybe(t: Optional[torch.Tensor], name: str, dtype, shape) -> Optional[int]:
+    return None if t is None else _expect(t, name, dtype, shape)
+
+
+def nf4_plan_step(lengths: torch.Tensor, new_tokens: torch.Tensor, page_size: int, page_table: torch.Tensor,
+                  free_pages: torch.Tensor, free_state: torch.Tensor, free_out: torch.Tensor, lengths_out: torch.Tensor,
+                  starts: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor, sequences: torch.Tensor,
+                  stream=None) -> None:
+    """The indices of a step: int32 lengths, new_tokens [B] (negative: finished) -> lengths_out [B], starts [B + 1] and
+    for every row int64 slots [T], int32 positions, sequences [T].  page_table int32 [B, max_pages] gets the new
+    pages from the ring free_pages int32 [pages], whose int64 state [2] = (first, count) goes to free_out;
+    lengths_out and free_out may be their inputs."""
+    status = _ready().plan_step(lengths, new_tokens, page_size, page_table, free_pages, free_state, free_out, lengths_out,
+                                starts, slots, positions, sequences, stream)
+    if status is not None:
+        return _check(status, "nf4_plan_step")
+    i32, i64 = torch.int32, torch.int64
+    (b,), (pages,), (t,), max_pages = lengths.shape, free_pages.shape, slots.shape, page_table.shape[-1]
+    _check(load().nf4_plan_step(
+        _expect(lengths, "lengths", i32, (b,)), _expect(new_tokens, "new_tokens", i32, (b,)), b, page_size, pages,
+        _expect(page_table, "page_table", i32, (b, max_pages)), max_pages, _expect(free_pages, "free_pages", i32, (pages,)),
+        _expect(free_state, "free_state", i64, (2,)), _expect(free_out, "free_out", i64, (2,)),
+        _expect(lengths_out, "lengths_out", i32, (b,)), _expect(starts, "starts", i32, (b + 1,)), t,
+        _expect(slots, "slots", i64, (t,)), _expect(positions, "positions", i32, (t,)),
+        _expect(sequences, "sequences", i32, (t,)), _current(stream)), "nf4_plan_step")
+
+
+def free_ring(pages: int, device="cuda"):
+    """(free_pages, free_state) of a pool in which every page is free."""
+    return (torch.arange(pages, dtype=torch.int32, device=device),
+            torch.tensor([0, pages], dtype=torch.int64, device=device))
+
+
+def nf4_lora_plan_bytes(tokens: int, adapters: int) -> int:
+    n = load().nf4_lora_plan_bytes(tokens, adapters)
+    if n < 0:
+        raise NF4Error(2, "nf4_lora_plan_bytes")
+    return n
+
+
+def lora_plan_buffer(tokens: int, adapters: int, device="cuda") -> torch.Tensor:
+    """Room for nf4_lora_plan's plan of `tokens` tokens and `adapters` loaded adapters."""
+    return torch.empty(nf4_lora_plan_bytes(tokens, adapters), dtype=torch.uint8, device=device)
+
+
+def nf4_lora_plan(ids: torch.Tensor, adapters: int, plan: torch.Tensor, sequences: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """The tokens of a step, listed by adapter, for nf4_lora: int32 ids [T] of the tokens, or ids [S] of the sequences
+    and int32 sequences [T]; negative: no adapter."""
+    status = _ready().lora_plan(ids, sequences, adapters, plan, stream)
+    if status is not None:
+        return _check(status, "nf4_lora_plan")
+    (s,), (size,) = ids.shape, plan.shape
+    t = s if sequences is None else sequences.shape[0]
+    _check(load().nf4_lora_plan(_expect(ids, "ids", torch.int32, (s,)),
+                                _maybe(sequences, "sequences", torch.int32, (t,)), s, t, adapters,
+                                _expect(plan, "plan", torch.uint8, (size,)), size, _current(stream)), "nf4_lora_plan")
+
+
+def nf4_lora_workspace_bytes(tokens: int, adapters: int, rank: int, count: int) -> int:
+    n = load().nf4_lora_workspace_bytes(tokens, adapters, rank, count)
+    if n < 0:
+        raise NF4Error(2, "nf4_lora_workspace_bytes")
+    return n
+
+
+def lora_workspace(tokens: int, adapters: int, rank: int, count: int, device="cuda") -> torch.Tensor:
+    """A workspace for nf4_lora with these sizes (or smaller ones of the same rank and count)."""
+    return torch.empty(nf4_lora_workspace_bytes(tokens, adapters, rank, count), dtype=torch.uint8, device=device)
+
+
+def nf4_lora(x: torch.Tensor, plan: torch.Tensor, scales: torch.Tensor, a, b, ys, workspace: torch.Tensor, bases=None,
+             stream=None) -> None:
+    """ys[i] = bases[i] + scale * B (A x) with each token's adapter: x bf16 [T, K], scales fp32 [adapters], lists (up to
+    8) of a bf16 [adapters, rank, K], b bf16 [adapters, N_i, rank], ys and bases bf16 [T, N_i]; bases None: ys."""
+    status = _ready().lora(x, plan, scales, a, b, ys, workspace, bases, stream)
+    if status is not None:
+        return _check(status, "nf4_lora")
+    n, bf16, u8 = len(a), torch.bfloat16, torch.uint8
+    if not (len(b) == len(ys) == n and (bases is None or len(bases) == n)):
+        raise ValueError("a, b, ys and bases must have the same length")
+    if not 1 <= n <= 8:
+        raise ValueError(f"want 1 to 8 projections, got {n}")
+    (t, k), (adapters,), (size,), (room,) = x.shape, scales.shape, plan.shape, workspace.shape
+    rank = a[0].shape[1]
+    arr = ctypes.c_void_p * n
+
+    def addresses(ts, name, shape):
+        return ctypes.cast(arr(*[_expect(u, f"{name}[{i}]", bf16, shape(i)) for i, u in enumerate(ts)]), ctypes.c_void_p)
+
+    ns = [u.shape[1] for u in b]
+    _check(load().nf4_lora(
+        _expect(x, "x", bf16, (t, k)), t, k, _expect(plan, "plan", u8, (size,)), size, adapters, rank,
+        _expect(scales, "scales", torch.float32, (adapters,)), n, addresses(a, "a", lambda i: (adapters, rank, k)),
+        addresses(b, "b", lambda i: (adapters, ns[i], rank)),
+        None if bases is None else addresses(bases, "bases", lambda i: (t, ns[i])),
+        addresses(ys, "ys", lambda i: (t, ns[i])), ctypes.cast((ctypes.c_int64 * n)(*ns), ctypes.c_void_p),
+        _expect(workspace, "workspace", u8, (room,)), room, _current(stream)), "nf4_lora")
+
+
+def nf4_sample(logits: torch.Tensor, random: torch.Tensor, tokens: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+               top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+               min_p: Optional[torch.Tensor] = None, vocab: Optional[int] = None,
+               logprobs: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The next token of every row of logits bf16 or fp32 [B, stride] (the first `vocab` of a row; default: all), drawn
+    with fp32 random [B] in [0, 1): int32 tokens [B] and fp32 logprobs [B].  fp32 temperature (0: the largest),
+    int32 top_k (0: all), fp32 top_p (1: all), fp32 min_p (0: all), each [B] or None."""
+    status = _ready().sample(logits, random, tokens, temperature, top_k, top_p, min_p, vocab, logprobs, stream)
+    if status is not None:
+        return _check(status, "nf4_sample")
+    b, width = logits.shape
+    bf16, f32, i32 = logits.dtype == torch.bfloat16, torch.float32, torch.int32
+    _check(load().nf4_sample(
+        _expect(logits, "logits", torch.bfloat16 if bf16 else f32, (b, width)), int(bf16), b,
+        width if vocab is None else vocab, width, _maybe(temperature, "temperature", f32, (b,)),
+        _maybe(top_k, "top_k", i32, (b,)), _maybe(top_p, "top_p", f32, (b,)), _maybe(min_p, "min_p", f32, (b,)),
+        _expect(random, "random", f32, (b,)), _expect(tokens, "tokens", i32, (b,)),
+        _maybe(logprobs, "logprobs", f32, (b,)), _current(stream)), "nf4_sample")
+
+
 # Convenience wrappers that allocate the outputs with torch.
+def lora_plan(ids: torch.Tensor, adapters: int, sequences: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    with _on(stream):
+        plan = lora_plan_buffer((ids if sequences is None else sequences).shape[0], adapters, ids.device)
+    nf4_lora_plan(ids, adapters, plan, sequences, stream)
+    return plan
+
+
+def sample(logits: torch.Tensor, random: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, vocab: Optional[int] = None, stream=None):
+    """(tokens, logprobs)"""
+    with _on(stream):
+        tokens = torch.empty(logits.shape[0], dtype=torch.int32, device=logits.device)
+        logprobs = torch.empty(logits.shape[0], dtype=torch.float32, device=logits.device)
+    nf4_sample(logits, random, tokens, temperature, top_k, top_p, min_p, vocab, logprobs, stream)
+    return tokens, logprobs
+
+
 def kv_read(cache: KVCache, slots: torch.Tensor, stream=None):
     shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
     with _on(stream):

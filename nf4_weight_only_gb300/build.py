@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libnf4.so")
 CALLS_PATH = os.path.join(BUILD_DIR, "nf4_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["nf4_api.cu", "nf4_quant.cu", "nf4_gemv.cu", "nf4_ring.cu", "nf4_kv.cu", "nf4_attn.cu",
-           "nf4_rows.cu"]
+           "nf4_rows.cu", "nf4_plan.cu", "nf4_lora.cu", "nf4_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                      "-Xptxas", "-warn-spills"]

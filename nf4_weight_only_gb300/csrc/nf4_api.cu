@@ -24,6 +24,7 @@ constexpr int64_t kMaxVectors = int64_t{1} << 40;  // of one side of a cache
 std::atomic<int> g_device_sms[kMaxDevices];
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
@@ -106,6 +107,11 @@ bool attention_sizes_ok(const nf4_kv_cache* c, int64_t B, int64_t q_heads) {
     return B >= 0 && B <= 65535 && q_heads >= 1 && q_heads <= 65535 && q_heads % c->kv_heads == 0 &&
            B * q_heads <= (int64_t{1} << 30);
 }
+
+bool lora_sizes_ok(int64_t T, int64_t adapters) {
+    return T >= 0 && T <= nf4::kLoraMaxTokens && adapters >= 0 && adapters <= nf4::kLoraMaxAdapters;
+}
+bool lora_rank_ok(int64_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 
 nf4::KvCache device_cache(const nf4_kv_cache* c) {
     return {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), static_cast<uint8_t*>(c->k_scales),
@@ -204,12 +210,14 @@ nf4_status nf4_check_device_error(int* code) {
     int dev = 0, sms = 0;
     nf4_status st = current_device(&dev, &sms);
     if (st != NF4_OK) return st;
-    int linear = 0, embed = 0, kv = 0, attention = 0;
+    int linear = 0, embed = 0, kv = 0, attention = 0, plan = 0, lora = 0;
     if ((st = from_cuda(nf4::read_and_clear_error(&linear))) != NF4_OK) return st;
     if ((st = from_cuda(nf4::read_and_clear_embed_error(&embed))) != NF4_OK) return st;
     if ((st = from_cuda(nf4::read_and_clear_kv_error(&kv))) != NF4_OK) return st;
     if ((st = from_cuda(nf4::read_and_clear_attention_error(&attention))) != NF4_OK) return st;
-    *code = linear ? linear : embed ? embed : kv ? kv : attention;
+    if ((st = from_cuda(nf4::read_and_clear_plan_error(&plan))) != NF4_OK) return st;
+    if ((st = from_cuda(nf4::read_and_clear_lora_error(&lora))) != NF4_OK) return st;
+    *code = linear ? linear : embed ? embed : kv ? kv : attention ? attention : plan ? plan : lora;
     return NF4_OK;
 }
 
@@ -430,6 +438,149 @@ nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
     nf4_status st = current_device(&dev, &sms);
     if (st != NF4_OK) return st;
     return from_cuda(nf4::launch_rmsnorm(x, residual, weight, T, H, eps, residual_out, y, y8, y8_scales, sms, stream));
+}
+
+nf4_status nf4_plan_step(const int32_t* lengths, const int32_t* new_tokens, int64_t B, int64_t page_size, int64_t pages,
+                         int32_t* page_table, int64_t max_pages, int32_t* free_pages, const int64_t* free_in,
+                         int64_t* free_out, int32_t* lengths_out, int32_t* starts, int64_t T, int64_t* slots,
+                         int32_t* positions, int32_t* sequences, cudaStream_t stream) {
+    if (B < 0 || B > nf4::kPlanMaxBatch || T < 0 || T > kMaxDim || pages < 0 || pages > kMaxDim) return NF4_ERR_SHAPE;
+    if (page_size < 16 || page_size > 65536 || page_size % 16 != 0) return NF4_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > kMaxDim || B * max_pages > (int64_t{1} << 40)) return NF4_ERR_SHAPE;
+    if (!free_in || !free_out || !starts || (B > 0 && (!lengths || !new_tokens || !lengths_out))) return NF4_ERR_NULL;
+    if ((T > 0 && (!slots || !positions || !sequences)) || (B * max_pages > 0 && !page_table) || (pages > 0 && !free_pages))
+        return NF4_ERR_NULL;
+    if (!aligned8(free_in) || !aligned8(free_out) || !aligned8(slots)) return NF4_ERR_ALIGN;
+    const void* words[8] = {lengths, new_tokens, page_table, free_pages, lengths_out, starts, positions, sequences};
+    for (const void* p : words)
+        if (!aligned4(p)) return NF4_ERR_ALIGN;
+    // three inputs, eight outputs (two of which may be their inputs)
+    const void* at[11] = {lengths,  new_tokens, free_in, lengths_out, free_out, page_table,
+                          free_pages, starts,     slots,   positions,   sequences};
+    const int64_t n[11] = {B * 4, B * 4, 16, B * 4, 16, B * max_pages * 4, pages * 4, (B + 1) * 4, T * 8, T * 4, T * 4};
+    for (int o = 3; o < 11; o++)
+        for (int i = 0; i < o; i++) {
+            const bool same = at[o] == at[i] && ((o == 3 && i == 0) || (o == 4 && i == 2));  // in place
+            if (!same && overlap(at[o], n[o], at[i], n[i])) return NF4_ERR_ALIAS;
+        }
+    int dev = 0, sms = 0;
+    nf4_status st = current_device(&dev, &sms);
+    if (st != NF4_OK) return st;
+    nf4::PlanArgs a{};
+    a.lengths = lengths, a.new_tokens = new_tokens, a.page_table = page_table, a.free_pages = free_pages;
+    a.free_in = free_in, a.free_out = free_out, a.lengths_out = lengths_out, a.starts = starts;
+    a.slots = slots, a.positions = positions, a.sequences = sequences;
+    a.T = T, a.max_pages = max_pages, a.pages = pages, a.B = static_cast<int>(B);
+    a.page_size = static_cast<uint32_t>(page_size);
+    return from_cuda(nf4::launch_plan(a, stream));
+}
+
+int64_t nf4_lora_plan_bytes(int64_t T, int64_t adapters) {
+    return lora_sizes_ok(T, adapters) ? nf4::lora_plan_bytes(T, adapters) : -1;
+}
+
+nf4_status nf4_lora_plan(const int32_t* ids, const int32_t* sequences, int64_t S, int64_t T, int64_t adapters, void* plan,
+                         int64_t plan_bytes, cudaStream_t stream) {
+    if (!lora_sizes_ok(T, adapters) || (sequences && (S < 0 || S > kMaxDim))) return NF4_ERR_SHAPE;
+    if (!plan || (T > 0 && !ids && (!sequences || S > 0))) return NF4_ERR_NULL;
+    if (!aligned16(plan) || !aligned4(ids) || !aligned4(sequences)) return NF4_ERR_ALIGN;
+    const int64_t need = nf4::lora_plan_bytes(T, adapters);
+    if (plan_bytes < need) return NF4_ERR_SHAPE;
+    if (overlap(plan, need, ids, (sequences ? S : T) * 4) || overlap(plan, need, sequences, sequences ? T * 4 : 0))
+        return NF4_ERR_ALIAS;
+    int dev = 0, sms = 0;
+    nf4_status st = current_device(&dev, &sms);
+    if (st != NF4_OK) return st;
+    return from_cuda(nf4::launch_lora_plan(ids, sequences, S, T, adapters, plan, stream));
+}
+
+int64_t nf4_lora_workspace_bytes(int64_t T, int64_t adapters, int64_t rank, int64_t count) {
+    if (!lora_sizes_ok(T, adapters) || !lora_rank_ok(rank) || count < 1 || count > nf4::kMaxGroupedLinears) return -1;
+    return nf4::lora_workspace_bytes(T, adapters, rank, count);
+}
+
+nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, int64_t plan_bytes, int64_t adapters,
+                    int64_t rank, const float* scales, int count, const uint16_t* const* a, const uint16_t* const* b,
+                    const uint16_t* const* bases, uint16_t* const* ys, const int64_t* Ns, void* workspace,
+                    int64_t workspace_bytes, cudaStream_t stream) {
+    if (!lora_sizes_ok(T, adapters) || !lora_rank_ok(rank)) return NF4_ERR_SHAPE;
+    if (count < 1 || count > nf4::kMaxGroupedLinears) return NF4_ERR_SHAPE;
+    nf4_status st = check_k(K);
+    if (st != NF4_OK) return st;
+    if (!a || !b || !ys || !Ns) return NF4_ERR_NULL;
+    int64_t rows = 0;
+    for (int i = 0; i < count; i++) {
+        if (Ns[i] < 0 || Ns[i] > kMaxDim) return NF4_ERR_SHAPE;
+        rows += Ns[i];
+    }
+    if (rows > kMaxDim) return NF4_ERR_SHAPE;
+    if (T == 0 || rows == 0) return NF4_OK;
+    if (!x || !plan || !workspace || (adapters > 0 && !scales)) return NF4_ERR_NULL;
+    if (!aligned16(x) || !aligned16(plan) || !aligned16(workspace) || !aligned4(scales)) return NF4_ERR_ALIGN;
+    const int64_t need = nf4::lora_workspace_bytes(T, adapters, rank, count), pb = nf4::lora_plan_bytes(T, adapters);
+    if (workspace_bytes < need || plan_bytes < pb) return NF4_ERR_SHAPE;
+    nf4::LoraArgs args{};
+    for (int i = 0; i < count; i++) {  // empty projections are dropped, the order stays
+        if (Ns[i] == 0) continue;
+        const uint16_t* base = bases ? bases[i] : ys[i];
+        if (!ys[i] || !base || (adapters > 0 && (!a[i] || !b[i]))) return NF4_ERR_NULL;
+        if (!aligned16(ys[i]) || !aligned16(base) || !aligned16(a[i]) || !aligned16(b[i])) return NF4_ERR_ALIGN;
+        const int k = args.count++;
+        args.a[k] = a[i], args.b[k] = b[i], args.base[k] = base, args.y[k] = ys[i], args.N[k] = Ns[i];
+    }
+    // every output against everything: inputs, the other outputs, the workspace
+    const int64_t xb = T * K * 2, ab = adapters * rank * K * 2;
+    if (overlap(workspace, need, x, xb) || overlap(workspace, need, plan, pb) ||
+        overlap(workspace, need, scales, adapters * 4))
+        return NF4_ERR_ALIAS;
+    for (int i = 0; i < args.count; i++) {
+        const int64_t yb = T * args.N[i] * 2;
+        if (overlap(args.y[i], yb, x, xb) || overlap(args.y[i], yb, plan, pb) || overlap(args.y[i], yb, workspace, need) ||
+            overlap(args.y[i], yb, scales, adapters * 4) || overlap(workspace, need, args.a[i], ab) ||
+            overlap(workspace, need, args.b[i], adapters * args.N[i] * rank * 2) ||
+            overlap(workspace, need, args.base[i], yb))
+            return NF4_ERR_ALIAS;
+        for (int j = 0; j < args.count; j++) {
+            const int64_t other = T * args.N[j] * 2;
+            if (overlap(args.y[i], yb, args.a[j], ab) ||
+                overlap(args.y[i], yb, args.b[j], adapters * args.N[j] * rank * 2) ||
+                (j != i && overlap(args.y[i], yb, args.y[j], other)) ||
+                (!(j == i && args.y[i] == args.base[i]) && overlap(args.y[i], yb, args.base[j], other)))
+                return NF4_ERR_ALIAS;
+        }
+    }
+    int dev = 0, sms = 0;
+    if ((st = current_device(&dev, &sms)) != NF4_OK) return st;
+    args.x = x, args.plan = static_cast<const int32_t*>(plan), args.scales = scales;
+    args.h = static_cast<float*>(workspace);
+    args.T = T, args.K = K, args.adapters = adapters, args.rank = static_cast<int>(rank);
+    return from_cuda(nf4::launch_lora(args, sms, stream));
+}
+
+nf4_status nf4_sample(const void* logits, int logits_bf16, int64_t B, int64_t V, int64_t stride, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p, const float* random, int32_t* tokens,
+                      float* logprobs, cudaStream_t stream) {
+    if (B < 0 || B > (1 << 24) || V < 1 || V > nf4::kSampleMaxVocab || stride < V || stride > kMaxDim) return NF4_ERR_SHAPE;
+    if (B == 0) return NF4_OK;
+    if (!logits || !random || !tokens) return NF4_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(logits) % (logits_bf16 ? 2 : 4) != 0) return NF4_ERR_ALIGN;
+    const void* at[7] = {temperature, top_k, top_p, min_p, random, tokens, logprobs};
+    for (const void* p : at)
+        if (!aligned4(p)) return NF4_ERR_ALIGN;
+    const int64_t lb = ((B - 1) * stride + V) * (logits_bf16 ? 2 : 4);
+    for (int o = 5; o < 7; o++) {
+        if (!at[o]) continue;
+        if (overlap(at[o], B * 4, logits, lb)) return NF4_ERR_ALIAS;
+        for (int i = 0; i < o; i++)
+            if (at[i] && overlap(at[o], B * 4, at[i], B * 4)) return NF4_ERR_ALIAS;
+    }
+    int dev = 0, sms = 0;
+    nf4_status st = current_device(&dev, &sms);
+    if (st != NF4_OK) return st;
+    nf4::SampleArgs a{};
+    a.logits = logits, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.random = random;
+    a.tokens = tokens, a.logprobs = logprobs, a.B = B, a.V = V, a.stride = stride, a.bf16 = logits_bf16 != 0;
+    return from_cuda(nf4::launch_sample(a, sms, stream));
 }
 
 }  // extern "C"

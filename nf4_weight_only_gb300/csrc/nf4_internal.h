@@ -78,6 +78,59 @@ cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const ui
                            float eps, uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y8_scales, int num_sms,
                            cudaStream_t stream);
 
+// A step's indices (nf4_plan_step); every CTA keeps four int32 a sequence in shared memory.
+constexpr int kPlanMaxBatch = 8192, kPlanThreads = 1024;
+struct PlanArgs {
+    const int32_t *lengths, *new_tokens;
+    int32_t* page_table;
+    int32_t* free_pages;
+    const int64_t* free_in;
+    int64_t* free_out;
+    int32_t *lengths_out, *starts;
+    int64_t* slots;
+    int32_t *positions, *sequences;
+    int64_t T, max_pages, pages;
+    int B;
+    uint32_t page_size;
+};
+cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
+// Error words: 45, a page or a ring's state outside the pool; 46, an adapter or a row outside its list; 47, a plan
+// of other sizes.
+cudaError_t read_and_clear_plan_error(int* code);
+
+// Low-rank adapters of many requests.
+constexpr int64_t kLoraMaxAdapters = 8192, kLoraMaxTokens = 1 << 24;
+int64_t lora_plan_bytes(int64_t T, int64_t adapters);
+int64_t lora_workspace_bytes(int64_t T, int64_t adapters, int64_t rank, int64_t count);
+cudaError_t launch_lora_plan(const int32_t* ids, const int32_t* sequences, int64_t S, int64_t T, int64_t adapters,
+                             void* plan, cudaStream_t stream);
+struct LoraArgs {
+    const uint16_t* x;
+    const int32_t* plan;
+    const float* scales;
+    float* h;  // the workspace
+    const uint16_t *a[kMaxGroupedLinears], *b[kMaxGroupedLinears], *base[kMaxGroupedLinears];
+    uint16_t* y[kMaxGroupedLinears];
+    int64_t N[kMaxGroupedLinears];
+    int64_t T, K, adapters;
+    int rank, count;
+};
+cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t read_and_clear_lora_error(int* code);
+
+// The next token of every row.
+struct SampleArgs {
+    const void* logits;
+    const float *temperature, *top_p, *min_p, *random;
+    const int32_t* top_k;
+    int32_t* tokens;
+    float* logprobs;
+    int64_t B, V, stride;
+    int bf16;
+};
+constexpr int64_t kSampleMaxVocab = 262144;
+cudaError_t launch_sample(const SampleArgs& a, int num_sms, cudaStream_t stream);
+
 // The C-ABI layer's device check (an nf4_status value): the current device and its SM count.
 int abi_current_device(int* device, int* sms);
 // Records a CUDA error for nf4_last_cuda_error (no-op for cudaSuccess).

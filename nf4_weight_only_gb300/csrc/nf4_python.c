@@ -23,6 +23,13 @@ static int (*p_rope)(const void*, int64_t, const void*, int64_t, int64_t, int64_
                      const void*, int64_t, int, float, void*, void*, cudaStream);
 static int (*p_rmsnorm)(const void*, const void*, const void*, int64_t, int64_t, float, void*, void*, void*, void*,
                         cudaStream);
+static int (*p_plan_step)(const void*, const void*, int64_t, int64_t, int64_t, void*, int64_t, void*, const void*, void*,
+                          void*, void*, int64_t, void*, void*, void*, cudaStream);
+static int (*p_lora_plan)(const void*, const void*, int64_t, int64_t, int64_t, void*, int64_t, cudaStream);
+static int (*p_lora)(const void*, int64_t, int64_t, const void*, int64_t, int64_t, int64_t, const void*, int, void* const*,
+                     void* const*, void* const*, void* const*, const int64_t*, void*, int64_t, cudaStream);
+static int (*p_sample)(const void*, int, int64_t, int64_t, int64_t, const void*, const void*, const void*, const void*,
+                       const void*, void*, void*, cudaStream);
 
 enum { BF16, FP8, F32, I32, I64, U8, TYPES };
 static PyObject* g_types[TYPES];
@@ -210,23 +217,122 @@ static PyObject* rmsnorm(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
     CALL(p_rmsnorm(x, r, w, shape[0], shape[1], (float)eps, ro, y, y8, scales, stream));
 }
 
-/* init(addresses of the five functions, the six types, raw-stream and current-device functions) */
+/* plan_step(lengths, new_tokens, page_size, page_table, free_pages, free_state, free_out, lengths_out, starts, slots,
+ *           positions, sequences, stream) */
+static PyObject* plan_step(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
+    (void)self;
+    ARGS(13)
+    int64_t b[1] = {-1}, table[2] = {0, -1}, pages[1] = {-1}, two[1] = {2}, more[1], t[1] = {-1};
+    void *lengths, *new_tokens, *page_table, *ring, *in, *out, *lengths_out, *starts, *slots, *positions, *sequences;
+    cudaStream stream;
+    if (!tensor(a[0], I32, 1, b, &lengths)) Py_RETURN_NONE;
+    table[0] = b[0], more[0] = b[0] + 1;
+    if (!tensor(a[1], I32, 1, b, &new_tokens) || !tensor(a[3], I32, 2, table, &page_table) ||
+        !tensor(a[4], I32, 1, pages, &ring) || !tensor(a[5], I64, 1, two, &in) || !tensor(a[6], I64, 1, two, &out) ||
+        !tensor(a[7], I32, 1, b, &lengths_out) || !tensor(a[8], I32, 1, more, &starts) ||
+        !tensor(a[9], I64, 1, t, &slots) || !tensor(a[10], I32, 1, t, &positions) ||
+        !tensor(a[11], I32, 1, t, &sequences))
+        Py_RETURN_NONE;
+    const int64_t page_size = PyLong_AsLongLong(a[2]);
+    if (PyErr_Occurred() || !stream_of(a[12], &stream)) return NULL;
+    CALL(p_plan_step(lengths, new_tokens, b[0], page_size, pages[0], page_table, table[1], ring, in, out, lengths_out,
+                     starts, t[0], slots, positions, sequences, stream));
+}
+
+/* lora_plan(ids, sequences or None, adapters, plan, stream) */
+static PyObject* lora_plan(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
+    (void)self;
+    ARGS(5)
+    int64_t s[1] = {-1}, t[1] = {-1}, size[1] = {-1};
+    void *ids, *sequences, *plan;
+    cudaStream stream;
+    if (!tensor(a[0], I32, 1, s, &ids) || !maybe(a[1], I32, 1, t, &sequences) || !tensor(a[3], U8, 1, size, &plan))
+        Py_RETURN_NONE;
+    const int64_t adapters = PyLong_AsLongLong(a[2]);
+    if (PyErr_Occurred() || !stream_of(a[4], &stream)) return NULL;
+    CALL(p_lora_plan(ids, sequences, s[0], a[1] == Py_None ? s[0] : t[0], adapters, plan, size[0], stream));
+}
+
+/* The tensors of a list, at most eight of them: 0 if one is not of that type, number of dims and (where dims is not
+ * negative) shape; dims[i] receives their shapes. */
+static int tensors(PyObject* list, int type, int nd, Py_ssize_t n, int64_t (*dims)[3], void** at) {
+    if (!PyList_Check(list) && !PyTuple_Check(list)) return 0;
+    if (PySequence_Fast_GET_SIZE(list) != n) return 0;
+    for (Py_ssize_t i = 0; i < n; i++)
+        if (!tensor(PySequence_Fast_GET_ITEM(list, i), type, nd, dims[i], &at[i])) return 0;
+    return 1;
+}
+
+/* lora(x, plan, scales, a, b, ys, workspace, bases or None, stream) */
+static PyObject* lora(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+    (void)self;
+    ARGS(9)
+    int64_t shape[2] = {-1, -1}, size[1] = {-1}, adapters[1] = {-1}, room[1] = {-1};
+    int64_t da[8][3], db[8][3], dy[8][3], ns[8];
+    void *x, *plan, *scales, *workspace, *a[8], *b[8], *ys[8], *bases[8];
+    cudaStream stream;
+    if (!tensor(args[0], BF16, 2, shape, &x) || !tensor(args[1], U8, 1, size, &plan) ||
+        !tensor(args[2], F32, 1, adapters, &scales) || !tensor(args[6], U8, 1, room, &workspace))
+        Py_RETURN_NONE;
+    if (!PyList_Check(args[3]) && !PyTuple_Check(args[3])) Py_RETURN_NONE;
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(args[3]);
+    if (n < 1 || n > 8) Py_RETURN_NONE;
+    for (Py_ssize_t i = 0; i < n; i++) da[i][0] = adapters[0], da[i][1] = -1, da[i][2] = shape[1];
+    if (!tensors(args[3], BF16, 3, n, da, a)) Py_RETURN_NONE;
+    for (Py_ssize_t i = 0; i < n; i++) db[i][0] = adapters[0], db[i][1] = -1, db[i][2] = da[0][1];
+    if (!tensors(args[4], BF16, 3, n, db, b)) Py_RETURN_NONE;
+    for (Py_ssize_t i = 0; i < n; i++) {
+        if (da[i][1] != da[0][1]) Py_RETURN_NONE;
+        dy[i][0] = shape[0], dy[i][1] = ns[i] = db[i][1];
+    }
+    if (!tensors(args[5], BF16, 2, n, dy, ys) || (args[7] != Py_None && !tensors(args[7], BF16, 2, n, dy, bases)))
+        Py_RETURN_NONE;
+    if (!stream_of(args[8], &stream)) return NULL;
+    CALL(p_lora(x, shape[0], shape[1], plan, size[0], adapters[0], da[0][1], scales, (int)n, a, b,
+                args[7] == Py_None ? NULL : bases, ys, ns, workspace, room[0], stream));
+}
+
+/* sample(logits, random, tokens, temperature, top_k, top_p, min_p, vocab or None, logprobs, stream) */
+static PyObject* sample(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
+    (void)self;
+    ARGS(10)
+    int64_t shape[2] = {-1, -1};
+    void *logits, *random, *tokens, *temperature, *top_k, *top_p, *min_p, *logprobs;
+    cudaStream stream;
+    const int bf16 = tensor(a[0], BF16, 2, shape, &logits);
+    if (!bf16) shape[0] = shape[1] = -1;
+    if ((!bf16 && !tensor(a[0], F32, 2, shape, &logits)) || !tensor(a[1], F32, 1, shape, &random) ||
+        !tensor(a[2], I32, 1, shape, &tokens) || !maybe(a[3], F32, 1, shape, &temperature) ||
+        !maybe(a[4], I32, 1, shape, &top_k) || !maybe(a[5], F32, 1, shape, &top_p) ||
+        !maybe(a[6], F32, 1, shape, &min_p) || !maybe(a[8], F32, 1, shape, &logprobs))
+        Py_RETURN_NONE;
+    const int64_t vocab = a[7] == Py_None ? shape[1] : PyLong_AsLongLong(a[7]);
+    if (PyErr_Occurred() || !stream_of(a[9], &stream)) return NULL;
+    CALL(p_sample(logits, bf16, shape[0], vocab, shape[1], temperature, top_k, top_p, min_p, random, tokens, logprobs,
+                  stream));
+}
+
+/* init(addresses of the nine functions, the six types, raw-stream and current-device functions) */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
     (void)self;
-    ARGS(5 + TYPES + 2)
-    void* f[5];
-    for (int i = 0; i < 5; i++) f[i] = PyLong_AsVoidPtr(a[i]);
+    enum { CALLS = 9 };
+    ARGS(CALLS + TYPES + 2)
+    void* f[CALLS];
+    for (int i = 0; i < CALLS; i++) f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return NULL;
     p_append = f[0], p_read = f[1], p_attention = f[2], p_rope = f[3], p_rmsnorm = f[4];
-    for (int i = 0; i < TYPES; i++) Py_XSETREF(g_types[i], Py_NewRef(a[5 + i]));
-    Py_XSETREF(g_raw_stream, Py_NewRef(a[5 + TYPES]));
-    Py_XSETREF(g_current_device, Py_NewRef(a[6 + TYPES]));
+    p_plan_step = f[5], p_lora_plan = f[6], p_lora = f[7], p_sample = f[8];
+    for (int i = 0; i < TYPES; i++) Py_XSETREF(g_types[i], Py_NewRef(a[CALLS + i]));
+    Py_XSETREF(g_raw_stream, Py_NewRef(a[CALLS + TYPES]));
+    Py_XSETREF(g_current_device, Py_NewRef(a[CALLS + TYPES + 1]));
     Py_RETURN_NONE;
 }
 
 #define METHOD(name, f) {name, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD("init", init), METHOD("append", append), METHOD("read", read_),
                                 METHOD("attention", attention), METHOD("rope", rope), METHOD("rmsnorm", rmsnorm),
+                                METHOD("plan_step", plan_step), METHOD("lora_plan", lora_plan), METHOD("lora", lora),
+                                METHOD("sample", sample),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "nf4_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
