@@ -14,6 +14,7 @@
 // is exchanged through distributed shared memory.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "nf4_kv.cuh"
@@ -24,10 +25,12 @@ namespace nf4 {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 1024;
+constexpr int kBins = 1024;  // two a thread
 constexpr int kMaxCluster = 8;
-constexpr int kOne = 40;           // a weight of 1 is 2^40
-constexpr float kFarthest = 41.0f; // in powers of 2: what lies further from the top has no weight
+constexpr int kList = 2048;            // candidates that a row's cut is found among
+constexpr int kFewest = 128;           // top_k up to this may take the short way
+constexpr int kOne = 40;               // a weight of 1 is 2^40
+constexpr float kFarthest = 41.0f;     // in powers of 2: what lies further from the top has no weight
 constexpr float kColdest = 0x1p-100f;  // a temperature below counts as 0
 
 // 2^(40 - j / 1024), rounded.  exp by its series, in double precision at compile time.
@@ -106,28 +109,29 @@ __device__ __forceinline__ uint64_t fraction_of(float f, uint64_t s, bool up) {
     return whole + (up && rest ? 1 : 0);
 }
 
-struct Slot {
-    unsigned long long a, b;
+// What a CTA tells the others: its largest logit, its sum of exp(l - that), and an index or a count; then sums.
+struct Note {
+    float top, sum;
+    int32_t at, count;
 };
-
-struct Shared {
+struct alignas(16) Shared {  // the slice follows, in 16-byte pieces
     unsigned long long table[1024];
-    unsigned long long weights[2][kBins];  // of the bins, one for each of two rounds that follow one another
-    uint32_t counts[2][kBins];
-    Slot slot[2];          // what this CTA tells the others
-    Slot part[kWarps];
-    unsigned long long found[4];
+    uint32_t low[kBins], high[kBins];  // of the bins: counts, or weights in two words
+    unsigned long long list[kList];    // candidates: key and index, or keys
+    Note notes[2][kMaxCluster];
+    unsigned long long sums[kMaxCluster][2];
+    unsigned long long part[kWarps][2];
+    float fpart[kWarps][2];
+    unsigned long long found[2];
+    uint32_t count;
     Row row;
 };
+
+static_assert(sizeof(Shared) % 16 == 0, "the slice's pieces are aligned");
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
-__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max(v, static_cast<uint64_t>(__shfl_xor_sync(0xFFFFFFFFu, v, o)));
     return v;
 }
 __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {  // inclusive
@@ -138,23 +142,81 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t v, int lane) {  // inclus
     }
     return v;
 }
+__device__ __forceinline__ float logit_of(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
 
+constexpr uint32_t kNothing = 0x007FFFFFu;  // the key of -inf
+__device__ __forceinline__ float minus_inf() { return __uint_as_float(0xFF800000u); }
+
+// Slices hold no NaN (loading makes them -inf).
 template <bool BF16>
 __device__ __forceinline__ float value_at(const void* values, int i) {
     if (BF16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(values)[i]) << 16);
     return static_cast<const float*>(values)[i];
 }
 
+// 16 bytes of logits: without NaN, their maximum, and each as a float.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, int per) {
-    extern __shared__ __align__(16) uint8_t slice[];
-    __shared__ Shared sh;
+struct Piece {
+    uint32_t w[4];
+    __device__ __forceinline__ explicit Piece(const uint4& u) : w{u.x, u.y, u.z, u.w} {}
+    __device__ __forceinline__ static uint32_t larger(uint32_t a, uint32_t b) {
+        uint32_t r;
+        if (BF16)
+            asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        else
+            asm("max.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static constexpr uint32_t kLeast = BF16 ? 0xFF80FF80u : 0xFF800000u;
+    __device__ __forceinline__ void clean() {
+#pragma unroll
+        for (int j = 0; j < 4; j++) w[j] = larger(w[j], kLeast);
+    }
+    __device__ __forceinline__ uint32_t top() const { return larger(larger(w[0], w[1]), larger(w[2], w[3])); }
+    __device__ __forceinline__ static float single(uint32_t m) {
+        return BF16 ? fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u)) : __uint_as_float(m);
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if (!BF16) return __uint_as_float(w[j]);
+        return __uint_as_float((j & 1) ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    }
+};
+
+// sums += exp({a, b} - top), both at a time: subtract, multiply by log2(e), two powers of 2, add.
+__device__ __forceinline__ void add_exponentials(float2& sums, float a, float b, float top) {
+    asm("{\n\t.reg .b64 v, t, s;\n\t.reg .f32 x, y;\n\t"
+        "mov.b64 v, {%2, %3};\n\t"
+        "mov.b64 t, {%4, %4};\n\t"
+        "add.rn.f32x2 v, v, t;\n\t"
+        "mov.b64 t, {%5, %5};\n\t"
+        "mul.rn.f32x2 v, v, t;\n\t"
+        "mov.b64 {x, y}, v;\n\t"
+        "ex2.approx.ftz.f32 x, x;\n\t"
+        "ex2.approx.ftz.f32 y, y;\n\t"
+        "mov.b64 v, {x, y};\n\t"
+        "mov.b64 s, {%0, %1};\n\t"
+        "add.rn.f32x2 s, s, v;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "+f"(sums.x), "+f"(sums.y)
+        : "f"(a), "f"(b), "f"(-top), "f"(1.4426950408889634f));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int per) {
+    extern __shared__ __align__(16) uint8_t memory[];
+    Shared& sh = *reinterpret_cast<Shared*>(memory);
+    uint8_t* slice = memory + sizeof(Shared);
     constexpr int E = BF16 ? 2 : 4, VEC = 16 / E;
+    using P = Piece<BF16>;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t b = blockIdx.x / ranks;
-    for (int i = tid; i < 1024; i += kThreads) sh.table[i] = kPowers.e[i];
+    for (int i = tid; i < kBins; i += kThreads) sh.low[i] = 0;
+    if (tid == 0) sh.count = 0;
+    cluster.barrier_arrive();  // no CTA writes to another before that one has begun
     pdl_launch_dependents();
     pdl_wait();
 
@@ -163,291 +225,527 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
     const int e1 = static_cast<int>(min(a.V, static_cast<int64_t>(e0) + per));
     const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (b * a.stride + e0) * E;
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E;
-    const int places = e1 > e0 ? (off + (e1 - e0) + VEC - 1) / VEC * VEC : 0;
-    uint64_t best = 0;  // the largest key, and the lowest index that has it
-    for (int v = tid; v < places / VEC; v += kThreads) {
-        const int p0 = v * VEC;
-        union {
-            uint4 u;
-            uint16_t h[8];
-            float f[4];
-        } x;
-        if (p0 >= off && p0 + VEC <= off + (e1 - e0)) {
-            x.u = __ldcs(reinterpret_cast<const uint4*>(src + (p0 - off) * E));
-        } else {
+    const int places = e1 > e0 ? (off + (e1 - e0) + VEC - 1) / VEC * VEC : 0, pieces = places / VEC;
+    const float heat = a.temperature ? a.temperature[b] : 1.0f;
+    const int k = a.top_k ? a.top_k[b] : 0;
+    float mine;  // the largest of this thread's pieces: tid, tid + kThreads, ...
+    {
+        uint32_t best = P::kLeast;
+        auto keep = [&](int v, const uint4& u) {
+            P p(u);
+            p.clean();
+            best = P::larger(best, p.top());
+            reinterpret_cast<uint4*>(slice)[v] = make_uint4(p.w[0], p.w[1], p.w[2], p.w[3]);
+        };
+        const int v0 = off ? 1 : 0, v1 = (off + (e1 - e0)) / VEC;  // whole pieces
+        const uint4* whole = reinterpret_cast<const uint4*>(src - off * E);
+        int v = v0 + tid;
+        for (; v + 3 * kThreads < v1; v += 4 * kThreads) {
+            uint4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) u[j] = __ldcs(whole + v + j * kThreads);
+#pragma unroll
+            for (int j = 0; j < 4; j++) keep(v + j * kThreads, u[j]);
+        }
+        for (; v < v1; v += kThreads) keep(v, __ldcs(whole + v));
+        // the pieces at the ends, where the row begins or ends inside one
+        for (int end = 0; end < 2; end++) {
+            const int at = end ? v1 : 0;
+            if (tid != end || at >= pieces || (at >= v0 && at < v1) || (end && at == 0)) continue;
+            uint32_t w[4] = {P::kLeast, P::kLeast, P::kLeast, P::kLeast};
 #pragma unroll
             for (int j = 0; j < VEC; j++) {
-                const int i = p0 + j - off;
-                const bool in = i >= 0 && i < e1 - e0;
+                const int i = at * VEC + j - off;
+                if (i < 0 || i >= e1 - e0) continue;
                 if (BF16)
-                    x.h[j] = in ? reinterpret_cast<const uint16_t*>(src)[i] : 0xFF80u;
+                    w[j / 2] = (w[j / 2] & (j & 1 ? 0x0000FFFFu : 0xFFFF0000u)) |
+                               (static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[i]) << (16 * (j & 1)));
                 else
-                    x.f[j] = in ? reinterpret_cast<const float*>(src)[i] : __uint_as_float(0xFF800000u);
+                    w[j] = reinterpret_cast<const uint32_t*>(src)[i];
+            }
+            keep(at, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        mine = P::single(best);
+    }
+    // the slice's largest logit, and the least of the threads' largest ones
+    float top_here, least_here;
+    auto block_ends = [&](float hi, float lo, float* out_hi, float* out_lo) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        }
+        if (lane == 0) sh.fpart[warp][0] = hi, sh.fpart[warp][1] = lo;
+        __syncthreads();
+        hi = sh.fpart[lane % kWarps][0], lo = sh.fpart[lane % kWarps][1];
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        }
+        *out_hi = hi, *out_lo = lo;
+        __syncthreads();
+    };
+    block_ends(mine, mine == minus_inf() ? __uint_as_float(0x7F800000u) : mine, &top_here, &least_here);
+    const bool cold = !(heat >= kColdest);
+    const bool few = !cold && k > 0 && k <= kFewest && k < a.V;
+    // The bin in which the counts in sh.low (and sh.high) pass `want`; kBins if they do not.  All threads have
+    // written their counts.
+    auto passed = [&](uint64_t v0, uint64_t v1, uint64_t want, uint64_t* before) {
+        const uint64_t both = v0 + v1, upto = warp_scan(both, lane);
+        if (lane == 31) sh.part[warp][0] = upto;
+        if (tid == 0) sh.found[0] = kBins, sh.found[1] = 0;
+        __syncthreads();
+        uint64_t ahead = upto - both;
+        for (int w = 0; w < warp; w++) ahead += sh.part[w][0];
+        if (ahead < want && ahead + both >= want) {
+            const int j = ahead + v0 >= want ? 0 : 1;
+            sh.found[0] = 2 * tid + j;
+            sh.found[1] = ahead + (j ? v0 : 0);
+        }
+        __syncthreads();
+        *before = sh.found[1];
+        const int bin = static_cast<int>(sh.found[0]);
+        __syncthreads();
+        return bin;
+    };
+    // Short way, for small top_k: at least k of the threads' largest logits reach `cut`, so the k largest of the
+    // slice do; few others do.
+    float cut_here = minus_inf();
+    if (few && top_here > minus_inf() && top_here < 3.4e38f) {
+        const float spread = fmaxf(top_here - least_here, 1e-30f), to_bin = (kBins - 0.5f) / spread;
+        const int bin = mine == minus_inf() ? kBins : min(kBins - 1, static_cast<int>((top_here - mine) * to_bin));
+        if (bin < kBins) atomicAdd(&sh.low[bin], 1u);
+        __syncthreads();
+        uint64_t unused;
+        const int last = passed(sh.low[2 * tid], sh.low[2 * tid + 1], static_cast<uint64_t>(k), &unused);
+        float ignored;
+        block_ends(0.0f, bin <= last && bin < kBins ? mine : __uint_as_float(0x7F800000u), &ignored, &cut_here);
+        if (last == kBins) cut_here = minus_inf();  // fewer than k threads have a logit
+    }
+    cluster.barrier_wait();
+    const int room = kList / ranks;  // of the list, for each CTA
+    float2 sums = make_float2(0.0f, 0.0f);
+    int first = 0x7FFFFFFF;
+    if (top_here > minus_inf()) {
+        const bool wants_sum = a.logprobs != nullptr;
+        unsigned long long* list = cluster.map_shared_rank(sh.list, 0) + rank * room;
+        const float line = cold ? top_here : few ? cut_here : __uint_as_float(0x7F800000u);
+        for (int v = tid; v < pieces; v += kThreads) {
+            const P p(reinterpret_cast<const uint4*>(slice)[v]);
+            if (wants_sum) {
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) add_exponentials(sums, p[j], p[j + 1], top_here);
+            }
+            if (P::single(p.top()) >= line) {
+#pragma unroll
+                for (int j = 0; j < VEC; j++) {
+                    if (!(p[j] >= line) || p[j] == minus_inf()) continue;
+                    const int i = e0 + v * VEC + j - off;
+                    if (cold) {
+                        first = min(first, i);
+                    } else {
+                        const uint32_t at = atomicAdd(&sh.count, 1u);
+                        if (at < static_cast<uint32_t>(room))
+                            list[at] = (static_cast<unsigned long long>(key_of(p[j])) << 32) | (0xFFFFFFFFu - i);
+                    }
+                }
             }
         }
-        reinterpret_cast<uint4*>(slice)[v] = x.u;
+    }
+    {
+        float sum = sums.x + sums.y;
 #pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            const float l = BF16 ? __uint_as_float(static_cast<uint32_t>(x.h[j]) << 16) : x.f[j];
-            const uint64_t at = (static_cast<uint64_t>(key_of(l)) << 32) | (0xFFFFFFFFu - (e0 + p0 + j - off));
-            best = max(best, at);
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            first = min(first, __shfl_xor_sync(0xFFFFFFFFu, first, o));
+        }
+        if (lane == 0) sh.fpart[warp][0] = sum, sh.fpart[warp][1] = __int_as_float(first);
+        __syncthreads();
+        if (tid < ranks) {
+            sum = 0.0f;
+            for (int w = 0; w < kWarps; w++) {
+                sum += sh.fpart[w][0];
+                first = min(first, __float_as_int(sh.fpart[w][1]));
+            }
+            cluster.map_shared_rank(&sh, tid)->notes[0][rank] = {top_here, sum, first, static_cast<int32_t>(sh.count)};
         }
     }
-    // sums over the row: every CTA's in two buffers by turns, one barrier each
-    int turn = 0;
-    auto reduce = [&](uint64_t x, uint64_t y, bool maximum, uint64_t* total_x, uint64_t* total_y) {
-        x = maximum ? warp_max(x) : warp_sum(x);
-        y = maximum ? warp_max(y) : warp_sum(y);
-        if (lane == 0) sh.part[warp] = {x, y};
+    cluster.sync();
+    float top = minus_inf(), all = 0.0f;
+    bool fits = true;
+    int arg = 0x7FFFFFFF, candidates = 0;
+    for (int r = 0; r < ranks; r++) {
+        const Note n = sh.notes[0][r];
+        if (n.top > top) top = n.top, arg = n.at;
+        fits &= n.count <= room;
+        candidates += n.count;
+    }
+    if (a.logprobs)
+        for (int r = 0; r < ranks; r++) {
+            const Note n = sh.notes[0][r];
+            if (n.top > minus_inf()) all += n.sum * exp2f((n.top - top) * 1.4426950408889634f);
+        }
+    const float log_sum = logf(all);
+    auto finish = [&](int token, float logit) {
+        a.tokens[b] = token;
+        if (a.logprobs) a.logprobs[b] = token < 0 ? minus_inf() : (logit - top) - log_sum;
+    };
+    if (top == minus_inf() || cold) {  // no token, or the first of the largest
+        if (rank == 0 && tid == 0) finish(top == minus_inf() ? -1 : arg, top);
+        return;
+    }
+    if (top == __uint_as_float(0x7F800000u)) {  // the first of the infinite ones
+        int at = 0x7FFFFFFF;
+        for (int i = tid; i < places; i += kThreads)
+            if (value_at<BF16>(slice, i) == top) at = min(at, e0 + i - off);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(0xFFFFFFFFu, at, o));
+        if (lane == 0) sh.fpart[warp][0] = __int_as_float(at);
         __syncthreads();
-        if (warp == 0) {
-            Slot s = lane < kWarps ? sh.part[lane] : Slot{0, 0};
-            const uint64_t sx = maximum ? warp_max(s.a) : warp_sum(s.a), sy = maximum ? warp_max(s.b) : warp_sum(s.b);
-            if (lane == 0) sh.slot[turn] = {sx, sy};
+        if (tid < ranks) {
+            for (int w = 0; w < kWarps; w++) at = min(at, __float_as_int(sh.fpart[w][0]));
+            cluster.map_shared_rank(&sh, tid)->notes[1][rank].at = at;
         }
         cluster.sync();
-        uint64_t rx = 0, ry = 0;
-        for (int r = 0; r < ranks; r++) {
-            const Slot s = *cluster.map_shared_rank(&sh.slot[turn], r);
-            rx = maximum ? max(rx, static_cast<uint64_t>(s.a)) : rx + s.a;
-            ry = maximum ? max(ry, static_cast<uint64_t>(s.b)) : ry + s.b;
+        if (rank == 0 && tid == 0) {
+            for (int r = 0; r < ranks; r++) at = min(at, sh.notes[1][r].at);
+            finish(at, top);
         }
-        turn ^= 1;
-        *total_x = rx;
-        if (total_y) *total_y = ry;
-    };
-    uint64_t top, unused;
-    reduce(best, 0, true, &top, &unused);
-    const uint32_t top_key = static_cast<uint32_t>(top >> 32);
-    const int top_at = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(top));
-    const float top_l = __uint_as_float((top_key & 0x80000000u) ? top_key ^ 0x80000000u : ~top_key);
-    const float heat = a.temperature ? a.temperature[b] : 1.0f;
-    // no logit above -inf: no token; +inf, or no heat: the first of the largest
-    const bool none = top_key <= 0x007FFFFFu, greedy = !(heat >= kColdest) || top_l > 3.4028235e38f;
-    int token = none ? -1 : top_at;
-    float log_sum = 0.0f;
-    if (a.logprobs && !none) {
-        float sum = 0.0f;
-        for (int i = tid; i < places; i += kThreads) sum += exp2f(fmaxf(value_at<BF16>(slice, i) - top_l, -1e30f) * 1.4426950408889634f);
-        uint64_t total;
-        reduce(static_cast<uint64_t>(static_cast<double>(sum) * 0x1p44), 0, false, &total, nullptr);
-        log_sum = logf(static_cast<float>(static_cast<double>(total) * 0x1p-44));
+        return;
     }
-    if (!none && !greedy) {
-        if (tid == 0) {
-            const double c = 1.4426950408889634 / static_cast<double>(heat);
-            sh.row.top = top_l;
-            sh.row.c_hi = static_cast<float>(c);
-            sh.row.c_lo = static_cast<float>(c - static_cast<double>(sh.row.c_hi));
-            sh.row.to_bin = static_cast<float>(c) * (kBins / kFarthest);
-        }
+    const bool listed = few && fits;
+    if (listed && rank != 0) return;
+    if (tid == 0) {
+        const double c = 1.4426950408889634 / static_cast<double>(heat);
+        sh.row.top = top;
+        sh.row.c_hi = static_cast<float>(c);
+        sh.row.c_lo = static_cast<float>(c - static_cast<double>(sh.row.c_hi));
+        sh.row.to_bin = static_cast<float>(c) * (kBins / kFarthest);
+    }
+    const float top_p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f;
+    const uint64_t least =
+        min_p >= 1.0f ? uint64_t{1} << kOne : max(fraction_of(min_p, uint64_t{1} << kOne, true), uint64_t{1});
+    auto block_sum = [&](uint64_t x) {
+        x = warp_sum(x);
+        if (lane == 0) sh.part[warp][0] = x;
+        __syncthreads();
+        uint64_t s = 0;
+        for (int w = 0; w < kWarps; w++) s += sh.part[w][0];
+        __syncthreads();
+        return s;
+    };
+    if (listed) {
+        // Of the candidates, those in the bins that hold the first k; then all pairs of these, eight threads each.
+        unsigned long long* names = reinterpret_cast<unsigned long long*>(slice);
+        unsigned long long* weights = names + kList;
+        float lowest = top;
+        for (int e = tid; e < ranks * room; e += kThreads)
+            if (e % room < sh.notes[0][e / room].count)
+                lowest = fminf(lowest, logit_of(static_cast<uint32_t>(sh.list[e] >> 32)));
+        float ignored;
+        block_ends(0.0f, lowest, &ignored, &lowest);  // (and sh.row is there for all)
+        for (int i = tid; i < kBins; i += kThreads) sh.low[i] = 0;
+        if (tid == 0) sh.count = 0;
         __syncthreads();
         const Row row = sh.row;
-        // the distance bin of a logit; logits without weight are past the last
-        auto bin_of = [&](float l) {
-            const float x = (row.top - l) * row.to_bin;
-            return x < static_cast<float>(kBins) ? static_cast<int>(x) : kBins;
+        const float to_bin = (kBins - 0.5f) / fmaxf(top - lowest, 1e-30f);
+        auto bin_of = [&](unsigned long long name) {
+            return min(kBins - 1, static_cast<int>((top - logit_of(static_cast<uint32_t>(name >> 32))) * to_bin));
         };
-        int round = 0;
-        // One round: counts (and weights) of the elements that `in` puts into a bin, then the bin in which the sum
-        // passes `want`, and the sum before it.  Every CTA adds the same numbers.  False: not passed at all.
-        auto histogram = [&](auto in, bool weighted, uint64_t want, int* bin, uint64_t* before) {
-            uint32_t* counts = sh.counts[round];
-            unsigned long long* weights = sh.weights[round];
-            for (int i = tid; i < kBins; i += kThreads) counts[i] = 0, weights[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < places; i += kThreads) {
-                const float l = value_at<BF16>(slice, i);
-                const int at = in(l);
-                if (at < 0 || at >= kBins) continue;
-                if (weighted)
-                    atomicAdd(&weights[at], static_cast<unsigned long long>(weight_of(l, row, sh.table)));
-                else
-                    atomicAdd(&counts[at], 1u);
-            }
-            cluster.sync();
-            // two bins a thread, in order
-            uint64_t v[2] = {0, 0};
-            for (int r = 0; r < ranks; r++)
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-                    v[j] += weighted ? cluster.map_shared_rank(weights, r)[2 * tid + j]
-                                     : cluster.map_shared_rank(counts, r)[2 * tid + j];
-            const uint64_t mine = v[0] + v[1], upto = warp_scan(mine, lane);
-            if (lane == 31) sh.part[warp].a = upto;
-            if (tid == 0) sh.found[0] = kBins;
-            __syncthreads();
-            uint64_t ahead = upto - mine;
-            for (int w = 0; w < warp; w++) ahead += sh.part[w].a;
-            if (ahead < want && ahead + mine >= want) {
-                const int j = ahead + v[0] >= want ? 0 : 1;
-                sh.found[0] = 2 * tid + j;
-                sh.found[1] = ahead + (j ? v[0] : 0);
-            }
-            __syncthreads();
-            *bin = static_cast<int>(sh.found[0]);
-            *before = sh.found[1];
-            __syncthreads();
-            round ^= 1;
-            return *bin < kBins;
-        };
-        // The key at which the sum over the ordered elements with lowest < key passes `want`, and the sum above it.
-        // False: it never does.
-        auto select = [&](bool weighted, uint64_t want, uint32_t lowest, uint32_t* key, uint64_t* before) {
-            int first = 0;
-            uint64_t sum = 0, more = 0;
-            if (!histogram([&](float l) { return key_of(l) > lowest ? bin_of(l) : -1; }, weighted, want, &first, &sum))
-                return false;
-            // the keys of that bin, then ever narrower ranges of keys
-            uint64_t hi = 0, lo = 0;
-            for (int i = tid; i < places; i += kThreads) {
-                const float l = value_at<BF16>(slice, i);
-                if (key_of(l) > lowest && bin_of(l) == first) {
-                    hi = max(hi, static_cast<uint64_t>(key_of(l)));
-                    lo = max(lo, static_cast<uint64_t>(0xFFFFFFFFu - key_of(l)));
-                }
-            }
-            reduce(hi, lo, true, &hi, &lo);
-            uint32_t high = static_cast<uint32_t>(hi), low = 0xFFFFFFFFu - static_cast<uint32_t>(lo);
-            while (low < high) {
-                const int bits = 32 - __clz(high - low), shift = bits > 10 ? bits - 10 : 0;
-                int at = 0;
-                histogram(
-                    [&](float l) {
-                        const uint32_t k = key_of(l);
-                        return k >= low && k <= high ? static_cast<int>((high - k) >> shift) : -1;
-                    },
-                    weighted, want - sum, &at, &more);
-                sum += more;
-                high -= static_cast<uint32_t>(at) << shift;
-                low = shift == 0 ? high : max(low, high - ((1u << shift) - 1));
-            }
-            *key = high;
-            *before = sum;
-            return true;
-        };
-        uint32_t cut = 0;                   // elements with larger keys are kept
-        uint64_t ties = ~uint64_t{0};       // and so many of those with this key
-        auto logit_of = [](uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); };
-        // -inf and NaN have no weight: they are never kept
-        constexpr uint32_t kNothing = 0x007FFFFFu;
-        cut = kNothing, ties = 0;
-        const int k = a.top_k ? a.top_k[b] : 0;
-        if (k > 0 && k < a.V) {
-            uint32_t key;
-            uint64_t before;
-            if (select(false, static_cast<uint64_t>(k), kNothing, &key, &before)) cut = key, ties = k - before;
-        }
-        const float p = a.top_p ? a.top_p[b] : 1.0f;
-        if (p < 1.0f) {
-            uint64_t above = 0, at = 0;
-            for (int i = tid; i < places; i += kThreads) {
-                const float l = value_at<BF16>(slice, i);
-                if (key_of(l) > cut) above += weight_of(l, row, sh.table);
-            }
-            reduce(above, 0, false, &above, &at);
-            const uint64_t of_tie = ties ? weight_of(logit_of(cut), row, sh.table) : 0;
-            const uint64_t all = above + ties * of_tie;
-            const uint64_t want = max(fraction_of(p, all, true), uint64_t{1});
-            if (want > above) {  // of the tied ones, those with less than `want` before them
-                if (of_tie) ties = min(ties, (want - above + of_tie - 1) / of_tie);
-            } else {
-                uint32_t key;
-                uint64_t before;
-                select(true, want, cut, &key, &before);
-                const uint64_t w = weight_of(logit_of(key), row, sh.table);
-                cut = key;
-                ties = w ? (want - before + w - 1) / w : 1;
-            }
-        }
-        const float least_p = a.min_p ? a.min_p[b] : 0.0f;
-        // at least the largest stays
-        const uint64_t least =
-            least_p >= 1.0f ? uint64_t{1} << kOne : max(fraction_of(least_p, uint64_t{1} << kOne, true), uint64_t{1});
-        // Each warp takes a run of the slice; a run's sum is that of what lies above the cut, and of as many tied
-        // elements as the runs before it leave.
-        const int run = ((places + kWarps - 1) / kWarps + 31) / 32 * 32;
-        const int r0 = min(places, warp * run), r1 = min(places, r0 + run);
-        uint64_t sum = 0, tied = 0;
-        const uint64_t of_tie = ties ? weight_of(logit_of(cut), row, sh.table) : 0;
-        const bool tie_counts = of_tie >= least;
-        for (int i = r0 + lane; i < r1; i += 32) {
-            const float l = value_at<BF16>(slice, i);
-            const uint32_t key = key_of(l);
-            if (key > cut) {
-                const uint64_t w = weight_of(l, row, sh.table);
-                sum += w >= least ? w : 0;
-            } else if (key == cut) {
-                tied++;
-            }
-        }
-        sum = warp_sum(sum);
-        tied = warp_sum(tied);
-        if (lane == 0) sh.part[warp] = {sum, tied};
+        for (int e = tid; e < ranks * room; e += kThreads)
+            if (e % room < sh.notes[0][e / room].count) atomicAdd(&sh.low[bin_of(sh.list[e])], 1u);
         __syncthreads();
-        if (tid == 0) {
-            Slot s{0, 0};
-            for (int w = 0; w < kWarps; w++) s.a += sh.part[w].a, s.b += sh.part[w].b;
-            sh.slot[turn] = s;
+        uint64_t unused;
+        const int last = passed(sh.low[2 * tid], sh.low[2 * tid + 1], static_cast<uint64_t>(k), &unused);
+        for (int e = tid; e < ranks * room; e += kThreads) {
+            if (e % room >= sh.notes[0][e / room].count) continue;
+            const unsigned long long name = sh.list[e];
+            if (bin_of(name) > last) continue;
+            const uint32_t at = atomicAdd(&sh.count, 1u);
+            names[at] = name;
+            weights[at] = weight_of(logit_of(static_cast<uint32_t>(name >> 32)), row, kPowers.e);
+        }
+        __syncthreads();
+        const int n = static_cast<int>(sh.count), sub = tid % 8;
+        // the sum of the first k; what stands before each
+        uint64_t of_first = 0;
+        unsigned long long* before = sh.list;  // (the candidates are no longer needed)
+        for (int i = tid / 8; i < (n + 63) / 64 * 64; i += kThreads / 8) {
+            const unsigned long long name = i < n ? names[i] : ~0ull;
+            uint32_t place = 0;
+            uint64_t weight = 0;
+            for (int j = sub; j < n; j += 8)
+                if (names[j] > name) place++, weight += weights[j];
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) {
+                place += __shfl_xor_sync(0xFFFFFFFFu, place, o);
+                weight += __shfl_xor_sync(0xFFFFFFFFu, weight, o);
+            }
+            if (i < n && sub == 0) {
+                const bool in = place < static_cast<uint32_t>(k);
+                of_first += in ? weights[i] : 0;
+                before[i] = place == 0 ? 0 : in ? weight : ~0ull;
+            }
+        }
+        of_first = block_sum(of_first);
+        const uint64_t want = top_p < 1.0f ? max(fraction_of(top_p, of_first, true), uint64_t{1}) : ~uint64_t{0};
+        uint64_t kept = 0;
+        for (int i = tid; i < n; i += kThreads) {
+            if (before[i] >= want || weights[i] < least) weights[i] = 0;
+            kept += weights[i];
+        }
+        kept = block_sum(kept);
+        const uint64_t goal = min(fraction_of(a.random[b], kept, false), kept - 1);
+        for (int i = tid / 8; i < (n + 63) / 64 * 64; i += kThreads / 8) {
+            // (the lower half of a name falls as the index rises)
+            const uint32_t name = i < n ? static_cast<uint32_t>(names[i]) : 0;
+            uint64_t ahead = 0;
+            for (int j = sub; j < n; j += 8)
+                if (static_cast<uint32_t>(names[j]) > name) ahead += weights[j];
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, o);
+            if (i < n && sub == 0 && ahead <= goal && goal < ahead + weights[i])
+                finish(static_cast<int>(0xFFFFFFFFu - name), logit_of(static_cast<uint32_t>(names[i] >> 32)));
+        }
+        return;
+    }
+    // Long way, any size: bins of the distance from the top over the whole row, then what shares the bin in which the
+    // sum passes its goal.
+    for (int i = tid; i < 1024; i += kThreads) sh.table[i] = kPowers.e[i];
+    __syncthreads();
+    const Row row = sh.row;
+    auto bin_of = [&](float l) {  // logits without weight are past the last
+        const float x = (row.top - l) * row.to_bin;
+        return x < static_cast<float>(kBins) ? static_cast<int>(x) : kBins;
+    };
+    // Bins of all CTAs, summed: what `in` puts where, the bin in which the sum passes want(all), the sum before it.
+    auto histogram = [&](auto in, bool weighted, auto want_of, uint64_t* want, uint64_t* before) {
+        for (int i = tid; i < kBins; i += kThreads) sh.low[i] = 0, sh.high[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < places; i += kThreads) {
+            const float l = value_at<BF16>(slice, i);
+            const int at = in(l);
+            if (at < 0 || at >= kBins) continue;
+            if (!weighted) {
+                atomicAdd(&sh.low[at], 1u);
+                continue;
+            }
+            const uint64_t w = weight_of(l, row, sh.table);
+            const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.low[at], lo);
+            const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1 : 0);
+            if (hi) atomicAdd(&sh.high[at], hi);
         }
         cluster.sync();
-        uint64_t ahead = 0, tied_ahead = 0, total = 0;
-        {
-            uint64_t seen = 0;
+        uint64_t v[2] = {0, 0};
+        for (int r = 0; r < ranks; r++) {
+            const uint2 lo = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sh.low, r) + 2 * tid);
+            const uint2 hi = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sh.high, r) + 2 * tid);
+            v[0] += (static_cast<uint64_t>(hi.x) << 32) + lo.x;
+            v[1] += (static_cast<uint64_t>(hi.y) << 32) + lo.y;
+        }
+        *want = want_of(v[0] + v[1]);
+        return passed(v[0], v[1], *want, before);
+    };
+    // The key at which the sum over the elements with keys above `lowest` passes its goal, in falling order, and
+    // the sum above that key.  False: it does not pass.
+    auto select = [&](bool weighted, auto want_of, uint32_t lowest, uint32_t* key, uint64_t* want, uint64_t* before) {
+        const int bin = histogram([&](float l) { return key_of(l) > lowest ? bin_of(l) : -1; }, weighted, want_of, want, before);
+        if (bin == kBins) {
+            cluster.sync();  // all have read the bins
+            return false;
+        }
+        uint32_t high = 0, low = 0;  // the range of keys that the goal is passed in, once it is known
+        for (bool ranged = false;; ranged = true) {
+            // what is there goes to every CTA's list
+            uint32_t* list = reinterpret_cast<uint32_t*>(sh.list);
+            const int places_each = 2 * kList / ranks;
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            float most = minus_inf(), fewest = __uint_as_float(0x7F800000u);
+            for (int i = tid; i < places; i += kThreads) {
+                const float l = value_at<BF16>(slice, i);
+                const uint32_t mine_key = key_of(l);
+                if (ranged ? mine_key > high || mine_key < low : mine_key <= lowest || bin_of(l) != bin) continue;
+                most = fmaxf(most, l), fewest = fminf(fewest, l);
+                const uint32_t at = atomicAdd(&sh.count, 1u);
+                if (at < static_cast<uint32_t>(places_each))
+                    for (int r = 0; r < ranks; r++) cluster.map_shared_rank(list, r)[rank * places_each + at] = mine_key;
+            }
+            block_ends(most, fewest, &most, &fewest);
+            if (tid < ranks)
+                cluster.map_shared_rank(&sh, tid)->notes[1][rank] = {most, fewest, 0, static_cast<int32_t>(sh.count)};
+            cluster.sync();
+            int n = 0;
             for (int r = 0; r < ranks; r++) {
-                const Slot s = *cluster.map_shared_rank(&sh.slot[turn], r);
-                if (r == rank) ahead = total, tied_ahead = seen;
-                const uint64_t kept = tie_counts ? min(static_cast<uint64_t>(s.b), ties - min(ties, seen)) : 0;
-                total += s.a + kept * of_tie;
-                seen += s.b;
+                n += sh.notes[1][r].count;
+                if (sh.notes[1][r].count > places_each) n = 2 * kList + 1;
             }
-            turn ^= 1;
-        }
-        const uint64_t goal = min(fraction_of(a.random[b], total, false), total - 1);
-        for (int w = 0; w < warp; w++) {
-            const Slot s = sh.part[w];
-            const uint64_t kept = tie_counts ? min(static_cast<uint64_t>(s.b), ties - min(ties, tied_ahead)) : 0;
-            ahead += s.a + kept * of_tie;
-            tied_ahead += s.b;
-        }
-        const uint64_t kept = tie_counts ? min(tied, ties - min(ties, tied_ahead)) : 0;
-        if (tid == 0) sh.found[0] = ~0ull;
-        __syncthreads();
-        if (goal >= ahead && goal < ahead + sum + kept * of_tie) {  // this warp's run has the token
-            for (int i0 = r0; i0 < r1; i0 += 32) {
-                const int i = i0 + lane;
-                uint64_t w = 0;
-                const float l = i < r1 ? value_at<BF16>(slice, i) : __uint_as_float(0xFF800000u);
-                const uint32_t key = key_of(l);
-                const uint32_t equal = __ballot_sync(0xFFFFFFFFu, i < r1 && key == cut);
-                if (i < r1 && key > cut) {
-                    w = weight_of(l, row, sh.table);
-                    if (w < least) w = 0;
-                } else if (i < r1 && key == cut && tie_counts &&
-                           tied_ahead + __popc(equal & ((1u << lane) - 1)) < ties) {
-                    w = of_tie;
+            if (n <= kThreads) {
+                // each thread one of them against all
+                uint32_t mine_key = 0;
+                {
+                    int at = tid;
+                    for (int r = 0; r < ranks && at >= 0; r++) {
+                        if (at < sh.notes[1][r].count) {
+                            mine_key = list[r * places_each + at];
+                            at = -1;
+                        } else {
+                            at -= sh.notes[1][r].count;
+                        }
+                    }
                 }
-                const uint64_t upto = ahead + warp_scan(w, lane);
-                const uint32_t passed = __ballot_sync(0xFFFFFFFFu, upto > goal);
-                if (passed) {
-                    if (lane == __ffs(passed) - 1) sh.found[0] = static_cast<unsigned long long>(e0 + i - off);
-                    break;
+                uint64_t above = 0, equal = 0;
+                uint64_t* weights = reinterpret_cast<uint64_t*>(sh.low);  // of keys, kThreads of them
+                uint32_t* keys = sh.high;
+                keys[tid] = mine_key;
+                weights[tid] = !weighted ? 1 : tid < n ? weight_of(logit_of(mine_key), row, sh.table) : 0;
+                __syncthreads();
+                if (tid < n)
+                    for (int j = 0; j < n; j++) {
+                        const uint32_t other = keys[j];
+                        if (other > mine_key)
+                            above += weights[j];
+                        else if (other == mine_key)
+                            equal += weights[j];
+                    }
+                if (tid < n && *before + above < *want && *want <= *before + above + equal) {
+                    sh.found[0] = mine_key;  // the same from every thread that has this key
+                    sh.found[1] = *before + above;
                 }
-                ahead = __shfl_sync(0xFFFFFFFFu, upto, 31);
-                tied_ahead += __popc(equal);
+                __syncthreads();
+                *key = static_cast<uint32_t>(sh.found[0]);
+                *before = sh.found[1];
+                return true;
             }
+            if (!ranged) {
+                for (int r = 0; r < ranks; r++) {
+                    const Note note = sh.notes[1][r];
+                    if (note.count == 0) continue;
+                    most = fmaxf(most, note.top), fewest = fminf(fewest, note.sum);
+                }
+                high = key_of(most), low = key_of(fewest);
+            }
+            if (high == low) {
+                *key = high;
+                return true;
+            }
+            // narrower: bins of keys
+            const int bits = 32 - __clz(high - low), shift = bits > 10 ? bits - 10 : 0;
+            uint64_t more = 0, left = 0;
+            const uint64_t rest = *want - *before;
+            const int at = histogram(
+                [&](float l) {
+                    const uint32_t q = key_of(l);
+                    return q >= low && q <= high ? static_cast<int>((high - q) >> shift) : -1;
+                },
+                weighted, [&](uint64_t) { return rest; }, &left, &more);
+            *before += more;
+            high -= static_cast<uint32_t>(at) << shift;
+            low = shift == 0 ? high : max(low, high - ((1u << shift) - 1));
         }
-        __syncthreads();
-        if (tid == 0 && sh.found[0] != ~0ull) {
-            const int i = static_cast<int>(sh.found[0]);
-            a.tokens[b] = i;
-            if (a.logprobs) a.logprobs[b] = (value_at<BF16>(slice, i - e0 + off) - top_l) - log_sum;
-        }
-    } else if (rank == 0 && tid == 0) {
-        a.tokens[b] = token;
-        if (a.logprobs) a.logprobs[b] = none ? __uint_as_float(0xFF800000u) : 0.0f - log_sum;
+    };
+    uint32_t cut = kNothing;  // elements with larger keys are kept
+    uint64_t ties = 0;        // and so many of those with this key
+    if (k > 0 && k < a.V) {
+        uint32_t key;
+        uint64_t want, before;
+        if (select(false, [&](uint64_t) { return static_cast<uint64_t>(k); }, kNothing, &key, &want, &before))
+            cut = key, ties = k - before;
     }
-    cluster.sync();  // no CTA leaves while another may read from it
+    if (top_p < 1.0f) {
+        const uint64_t of_tie = ties ? weight_of(logit_of(cut), row, sh.table) : 0;
+        uint32_t key;
+        uint64_t want, before, above = 0;
+        const bool inside = select(
+            true,
+            [&](uint64_t x) {
+                above = block_sum(x);
+                return max(fraction_of(top_p, above + ties * of_tie, true), uint64_t{1});
+            },
+            cut, &key, &want, &before);
+        if (inside) {
+            const uint64_t w = weight_of(logit_of(key), row, sh.table);
+            cut = key;
+            ties = (want - before + w - 1) / w;
+        } else if (of_tie) {  // among the tied ones: those with less than `want` before them
+            ties = min(ties, (want - above + of_tie - 1) / of_tie);
+        }
+    }
+    // Every thread takes a run of the slice; a run's sum is that of what lies above the cut, and of as many tied
+    // elements as the runs before it leave.
+    const int run = ((places + kThreads - 1) / kThreads) | 1;  // odd: a warp's reads spread over the banks
+    const int r0 = min(places, tid * run), r1 = min(places, r0 + run);
+    const uint64_t of_tie = ties ? weight_of(logit_of(cut), row, sh.table) : 0;
+    const bool tie_counts = of_tie >= least;
+    uint64_t above = 0, tied = 0;
+    for (int i = r0; i < r1; i++) {
+        const float l = value_at<BF16>(slice, i);
+        const uint32_t key = key_of(l);
+        if (key > cut) {
+            const uint64_t w = weight_of(l, row, sh.table);
+            above += w >= least ? w : 0;
+        } else if (key == cut) {
+            tied++;
+        }
+    }
+    const uint64_t scan_a = warp_scan(above, lane), scan_t = warp_scan(tied, lane);
+    if (lane == 31) sh.part[warp][0] = scan_a, sh.part[warp][1] = scan_t;
+    __syncthreads();
+    uint64_t ahead = scan_a - above, tied_ahead = scan_t - tied, here = 0, tied_here = 0;
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) ahead += sh.part[w][0], tied_ahead += sh.part[w][1];
+        here += sh.part[w][0], tied_here += sh.part[w][1];
+    }
+    if (tid < ranks) {
+        Shared* other = cluster.map_shared_rank(&sh, tid);
+        other->sums[rank][0] = here;
+        other->sums[rank][1] = tied_here;
+    }
+    if (tid == 0) sh.found[0] = kThreads;
+    cluster.sync();
+    // of n tied elements behind `seen` others
+    auto kept_of = [&](uint64_t n, uint64_t seen) { return tie_counts ? min(n, ties - min(ties, seen)) * of_tie : 0; };
+    uint64_t total = 0, seen = 0, before_slice = 0;
+    for (int r = 0; r < ranks; r++) {
+        if (r == rank) before_slice = total - kept_of(seen, 0), tied_ahead += seen;
+        total += sh.sums[r][0] + kept_of(sh.sums[r][1], seen);
+        seen += sh.sums[r][1];
+    }
+    // (all that lies before a run: what is above the cut there, and the first of its tied elements)
+    const uint64_t goal = min(fraction_of(a.random[b], total, false), total - 1);
+    ahead += before_slice + kept_of(tied_ahead, 0);
+    if (goal >= ahead && goal < ahead + above + kept_of(tied, tied_ahead)) {
+        sh.found[0] = tid;
+        sh.part[0][0] = ahead;
+        sh.part[0][1] = tied_ahead;
+    }
+    __syncthreads();
+    const int at = static_cast<int>(sh.found[0]);
+    if (at == kThreads || warp != 0) return;
+    ahead = sh.part[0][0], tied_ahead = sh.part[0][1];
+    const int end = min(places, (at + 1) * run);
+    for (int i0 = at * run; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        const float l = i < end ? value_at<BF16>(slice, i) : minus_inf();
+        const uint32_t key = key_of(l);
+        const uint32_t equal = __ballot_sync(0xFFFFFFFFu, i < end && key == cut);
+        uint64_t w = 0;
+        if (i < end && key > cut) {
+            w = weight_of(l, row, sh.table);
+            if (w < least) w = 0;
+        } else if (i < end && key == cut && tie_counts && tied_ahead + __popc(equal & ((1u << lane) - 1)) < ties) {
+            w = of_tie;
+        }
+        const uint64_t upto = ahead + warp_scan(w, lane);
+        const uint32_t over = __ballot_sync(0xFFFFFFFFu, upto > goal);
+        if (over) {
+            if (lane == __ffs(over) - 1) finish(e0 + i - off, l);
+            break;
+        }
+        ahead = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        tied_ahead += __popc(equal);
+    }
 }
 
 template <bool BF16>
@@ -457,7 +755,10 @@ cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t stream) {
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e != cudaSuccess) return e;
-    constexpr int kMost = static_cast<int>(kSampleMaxVocab / kMaxCluster * E + 32);
+    auto bytes = [](int64_t per) {  // the slice also holds a list's names and weights
+        return static_cast<int>(sizeof(Shared)) + std::max(static_cast<int>(per) * E + 32, 2 * kList * 8);
+    };
+    const int kMost = bytes(kSampleMaxVocab / kMaxCluster);
     std::call_once(once[device & 63], [&] {
         e = cudaFuncSetAttribute(sample_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     });
@@ -470,7 +771,7 @@ cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t stream) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
     cfg.numAttrs = 2;
-    cfg.dynamicSmemBytes = static_cast<size_t>(per) * E + 32;
+    cfg.dynamicSmemBytes = bytes(per);
     (void)num_sms;
     return cudaLaunchKernelEx(&cfg, sample_kernel<BF16>, a, per);
 }
