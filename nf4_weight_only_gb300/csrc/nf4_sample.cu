@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "nf4_kv.cuh"
 
@@ -28,6 +29,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1024;  // two a thread
 constexpr int kMaxCluster = 8;
 constexpr int kList = 2048;            // candidates that a row's cut is found among
+constexpr int kFewBins = 256;          // eight a lane
 constexpr int kFewest = 128;           // top_k up to this may take the short way
 constexpr int kSliceBytes = 80 * 1024; // of a slice, for two CTAs an SM
 constexpr int kOne = 40;               // a weight of 1 is 2^40
@@ -35,7 +37,7 @@ constexpr float kFarthest = 41.0f;     // in powers of 2: what lies further from
 constexpr float kColdest = 0x1p-100f;  // a temperature below counts as 0
 
 // 2^(31 - j / 1024), rounded.  exp by its series, in double precision at compile time.
-struct PowerTable {
+struct alignas(16) PowerTable {
     uint32_t e[1024];
 };
 constexpr PowerTable power_table() {
@@ -145,7 +147,7 @@ __device__ __forceinline__ uint64_t fraction_of(float f, uint64_t s, bool up) {
 }
 
 // What a CTA tells the others: its largest logit, how many have it, the sum of exp(l - that) over the rest, an index or
-// the least candidate, and how many candidates.
+// a line that top_k of its logits reach, and how many reach that.
 struct alignas(16) Note {
     float top, sum;
     int32_t at, count, tops;
@@ -153,15 +155,15 @@ struct alignas(16) Note {
 struct alignas(16) Shared {  // the slice follows, in 16-byte pieces
     uint32_t table[1024];
     uint32_t low[kBins], high[kBins];  // of the bins: counts, or weights in two words
-    unsigned long long list[kList];    // candidates: key and index, or keys
+    unsigned long long list[kList];    // candidates: key and index, or keys; sums before candidates
     Note notes[2][kMaxCluster];
     unsigned long long sums[kMaxCluster][2];
     unsigned long long part[kWarps][2];
     float fpart[kWarps][2];
     int32_t tops[kWarps];
     unsigned long long found[2];
-    uint32_t count;
-    Row row;
+    uint32_t count, line;
+    float log_sum;
 };
 
 static_assert(sizeof(Shared) % 16 == 0, "the slice's pieces are aligned");
@@ -233,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t b = blockIdx.x / ranks;
     for (int i = tid; i < kBins; i += kThreads) sh.low[i] = 0;
+    reinterpret_cast<uint2*>(sh.table)[tid] = reinterpret_cast<const uint2*>(kPowers.e)[tid];
     if (tid == 0) sh.count = 0;
     cluster.barrier_arrive();  // no CTA writes to another before that one has begun
     pdl_launch_dependents();
@@ -244,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const uint8_t* src = static_cast<const uint8_t*>(a.logits) + (b * a.stride + e0) * E;
     const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src) & 15) / E;
     const int places = e1 > e0 ? (off + (e1 - e0) + VEC - 1) / VEC * VEC : 0, pieces = places / VEC;
-    const float heat = a.temperature ? a.temperature[b] : 1.0f;
+    const float heat = a.temperature ? a.temperature[b] : 1.0f, top_p = a.top_p ? a.top_p[b] : 1.0f;
+    const float min_p = a.min_p ? a.min_p[b] : 0.0f, random = a.random[b];
     const int k = a.top_k ? a.top_k[b] : 0;
     float mine;  // the largest of this thread's pieces: tid, tid + kThreads, ...
     {
@@ -302,82 +306,95 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         *out_hi = hi, *out_lo = lo;
         __syncthreads();
     };
-    // Short way, for small top_k: a line that at least k logits of the slice reach, and few more do.  Every warp takes
-    // the m-th of its threads' largest logits, m = k / warps; at least m of them reach that, and the least of the
-    // warps' is the line.  (Bins of all threads' largest logits found a closer one, for more than it saved.)
+    // Short way, for small top_k: a line that at least k logits of the slice reach, and few more do.  It is the k-th of
+    // the largest logits of single threads, as far as the m largest of every warp's tell (m twice the mean number
+    // of the first k that a warp has, or more).
     const bool cold = !(heat >= kColdest);
     const bool few = !cold && k > 0 && k <= kFewest && k < a.V;
-    float line = minus_inf();
+    const int m = k <= 64 ? 8 : 16, known = m * kWarps;
     if (few) {
-        uint32_t key = key_of(mine), largest = 0;
-        for (int i = 0; i < k; i += kWarps) {
-            largest = __reduce_max_sync(0xFFFFFFFFu, key);
+        uint32_t key = key_of(mine);
+        for (int i = 0; i < m; i++) {
+            const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, key);
+            if (lane == 0) sh.high[warp * m + i] = largest;
             if (key == largest) key = 0;  // (equal ones fall together: more reach the line)
         }
-        line = largest <= kNothing ? minus_inf() : logit_of(largest);
+        if (tid == 0) sh.line = 0xFFFFFFFFu;
     }
-    float top_here;  // the slice's largest logit
-    block_ends(mine, line, &top_here, &line);
-    if (!few) line = cold ? top_here : __uint_as_float(0x7F800000u);
+    float top_here, unused_end;  // the slice's largest logit
+    block_ends(mine, 0.0f, &top_here, &unused_end);
+    float line = cold ? top_here : __uint_as_float(0x7F800000u);
+    if (few) {
+        const int parts = kThreads / known, part = tid % parts;
+        const uint32_t own = sh.high[tid / parts];
+        int larger = 0;
+#pragma unroll 8
+        for (int j = part; j < known / 4; j += parts) {
+            const uint4 o = reinterpret_cast<const uint4*>(sh.high)[j];
+            larger += (o.x > own) + (o.y > own) + (o.z > own) + (o.w > own);
+        }
+        for (int o = 1; o < parts; o *= 2) larger += __shfl_xor_sync(0xFFFFFFFFu, larger, o);
+        // the least value with fewer than k larger ones
+        const uint32_t lowest_own = __reduce_min_sync(0xFFFFFFFFu, larger < k ? own : 0xFFFFFFFFu);
+        if (lane == 0 && lowest_own != 0xFFFFFFFFu) atomicMin(&sh.line, lowest_own);
+        __syncthreads();
+        line = sh.line <= kNothing ? minus_inf() : logit_of(sh.line);
+    }
     cluster.barrier_wait();
     const int room_log = 31 - __clz(kList / ranks), room = 1 << room_log;  // of the list, for each CTA
     float sum = 0.0f;
     int first = 0x7FFFFFFF, tops = 0;
-    if (top_here > minus_inf()) {
+    if (top_here > minus_inf() && (a.logprobs || few || cold)) {
         unsigned long long* list = cluster.map_shared_rank(sh.list, 0) + rank * room;
-        auto look = [&](const P& p, int v) {
-            if (!(P::single(p.top()) >= line)) return;
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                if (!(p[j] >= line) || p[j] == minus_inf()) continue;
-                const int i = e0 + v * VEC + j - off;
-                if (cold) {
-                    first = min(first, i);
-                } else {
-                    const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < static_cast<uint32_t>(room))
-                        list[at] = (static_cast<unsigned long long>(key_of(p[j])) << 32) | (0xFFFFFFFFu - i);
-                }
-            }
+        const Pair minus_top(-top_here), log2e(1.4426950408889634f);
+        Pair sums(0.0f);
+        auto power = [&](const P& p, int j) {
+            float2 e = ((Pair(p[j], p[j + 1]) + minus_top) * log2e).get();
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+            asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+            return e;
         };
-        if (a.logprobs) {
-            const Pair minus_top(-top_here), log2e(1.4426950408889634f);
-            auto power = [&](const P& p, int j) {
-                float2 e = ((Pair(p[j], p[j + 1]) + minus_top) * log2e).get();
-                asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-                asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-                return e;
-            };
-            // The largest logits are counted, not added: next to their 1 a small rest would lose its last bits, and
-            // with them the logarithm of a probability near 1.
-            if (mine == top_here) {
-                for (int v = tid; v < pieces; v += kThreads) {
-                    const P p(reinterpret_cast<const uint4*>(slice)[v]);
-#pragma unroll 2
-                    for (int j = 0; j < VEC; j += 2) {
-                        const float2 e = power(p, j);
-                        sum += p[j] == top_here ? 0.0f : e.x;
-                        sum += p[j + 1] == top_here ? 0.0f : e.y;
-                        tops += (p[j] == top_here) + (p[j + 1] == top_here);
-                    }
-                    look(p, v);
-                }
-            } else {
-                Pair sums(0.0f);
-                for (int v = tid; v < pieces; v += kThreads) {
-                    const P p(reinterpret_cast<const uint4*>(slice)[v]);
+        for (int v = tid; v < pieces; v += kThreads) {
+            const P p(reinterpret_cast<const uint4*>(slice)[v]);
+            const float most = P::single(p.top());
+            if (a.logprobs) {
+                if (most < top_here) {
 #pragma unroll
                     for (int j = 0; j < VEC; j += 2) {
                         const float2 e = power(p, j);
                         sums = sums + Pair(e.x, e.y);
                     }
-                    look(p, v);
+                } else {
+                    // The largest logits are counted, not added: next to their 1 a small rest would lose its last
+                    // bits, and with them the logarithm of a probability near 1.
+#pragma unroll
+                    for (int j = 0; j < VEC; j += 2) {
+                        const float2 e = power(p, j);
+                        tops += (p[j] == top_here) + (p[j + 1] == top_here);
+                        sum += (p[j] == top_here ? 0.0f : e.x) + (p[j + 1] == top_here ? 0.0f : e.y);
+                    }
                 }
-                sum = sums.get().x + sums.get().y;
             }
-        } else if (few || cold) {
-            for (int v = tid; v < pieces; v += kThreads) look(P(reinterpret_cast<const uint4*>(slice)[v]), v);
+            if (!(most >= line)) continue;
+            const int i0 = e0 + v * VEC - off;
+            uint32_t reach = 0;
+#pragma unroll
+            for (int j = 0; j < VEC; j++) reach |= (p[j] >= line ? 1u : 0u) << j;
+            if (cold) {
+                first = min(first, i0 + __ffs(reach) - 1);
+                continue;
+            }
+            uint32_t at = atomicAdd(&sh.count, __popc(reach));
+            for (; reach; reach &= reach - 1, at++) {
+                const int j = __ffs(reach) - 1;
+                const uint32_t low_word = j & (VEC / 4) ? p.w[1] : p.w[0], high_word = j & (VEC / 4) ? p.w[3] : p.w[2];
+                const uint32_t word = j & (VEC / 2) ? high_word : low_word;
+                const float l = __uint_as_float(!BF16 ? word : j & 1 ? word & 0xFFFF0000u : word << 16);
+                if (at < static_cast<uint32_t>(room))
+                    list[at] = (static_cast<unsigned long long>(key_of(l)) << 32) | (0xFFFFFFFFu - (i0 + j));
+            }
         }
+        sum += sums.get().x + sums.get().y;
     }
     {
 #pragma unroll
@@ -386,30 +403,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         tops = __reduce_add_sync(0xFFFFFFFFu, tops);
         if (lane == 0) sh.fpart[warp][0] = sum, sh.fpart[warp][1] = __int_as_float(first), sh.tops[warp] = tops;
         __syncthreads();
-        if (tid < ranks) {
-            sum = 0.0f, tops = 0;
-            for (int w = 0; w < kWarps; w++) {
-                sum += sh.fpart[w][0];
-                first = min(first, __float_as_int(sh.fpart[w][1]));
-                tops += sh.tops[w];
-            }
-            cluster.map_shared_rank(&sh, tid)->notes[0][rank] = {top_here, sum, few ? __float_as_int(line) : first,
-                                                                 static_cast<int32_t>(sh.count), tops};
+        if (warp == 0) {
+            sum = lane < kWarps ? sh.fpart[lane][0] : 0.0f;
+            first = __reduce_min_sync(0xFFFFFFFFu, __float_as_int(sh.fpart[lane % kWarps][1]));
+            tops = __reduce_add_sync(0xFFFFFFFFu, lane < kWarps ? sh.tops[lane] : 0);
+#pragma unroll
+            for (int o = kWarps / 2; o > 0; o >>= 1) sum += __shfl_down_sync(0xFFFFFFFFu, sum, o);
+            sum = __shfl_sync(0xFFFFFFFFu, sum, 0);
+            if (lane < ranks)
+                cluster.map_shared_rank(&sh, lane)->notes[0][rank] = {top_here, sum, few ? __float_as_int(line) : first,
+                                                                      static_cast<int32_t>(sh.count), tops};
         }
     }
     cluster.sync();
-    float top = minus_inf(), lowest = __uint_as_float(0x7F800000u);  // of the row; below its candidates
+    float top = minus_inf(), lowest = minus_inf();  // of the row; at least k of its logits reach `lowest`
     bool fits = true;
     int arg = 0x7FFFFFFF;
     for (int r = 0; r < ranks; r++) {
         const Note n = sh.notes[0][r];
         if (n.top > top) top = n.top, arg = n.at;
         fits &= n.count <= room;
-        if (n.count > 0) lowest = fminf(lowest, __int_as_float(n.at));
+        lowest = fmaxf(lowest, __int_as_float(n.at));  // (of use where they are lines)
     }
-    auto finish = [&](int token, float logit) {  // one thread
-        a.tokens[b] = token;
-        if (!a.logprobs) return;
+    auto log_of_sum = [&] {
         float rest = 0.0f, ones = 0.0f;
         for (int r = 0; r < ranks; r++) {
             const Note n = sh.notes[0][r];
@@ -419,10 +435,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             else if (n.top > minus_inf())
                 rest += (tops + n.sum) * exp2f((n.top - top) * 1.4426950408889634f);
         }
-        a.logprobs[b] = token < 0 ? minus_inf() : (logit - top) - (log1pf(rest / ones) + logf(ones));
+        return log1pf(rest / ones) + logf(ones);
+    };
+    // one thread; the others have seen sh.log_sum written
+    auto finish = [&](int token, float logit) {
+        a.tokens[b] = token;
+        if (a.logprobs) a.logprobs[b] = token < 0 ? minus_inf() : (logit - top) - sh.log_sum;
     };
     if (top == minus_inf() || cold) {  // no token, or the first of the largest
-        if (rank == 0 && tid == 0) finish(top == minus_inf() ? -1 : arg, top);
+        if (rank == 0 && tid == 0) {
+            if (a.logprobs) sh.log_sum = log_of_sum();
+            finish(top == minus_inf() ? -1 : arg, top);
+        }
         return;
     }
     if (top == __uint_as_float(0x7F800000u)) {  // the first of the infinite ones
@@ -440,12 +464,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         cluster.sync();
         if (rank == 0 && tid == 0) {
             for (int r = 0; r < ranks; r++) at = min(at, sh.notes[1][r].at);
+            sh.log_sum = 0.0f;
             finish(at, top);
         }
         return;
     }
     const bool listed = few && fits;
     if (listed && rank != 0) return;
+    if (a.logprobs && tid == kThreads - 1) sh.log_sum = log_of_sum();  // barriers follow before it is used
     // The bin in which the counts (or weights) of the bins, two a thread, pass `want`, and their sum before it; kBins if
     // they do not.
     auto passed = [&](uint64_t v0, uint64_t v1, uint64_t want, uint64_t* before) {
@@ -466,14 +492,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         __syncthreads();
         return bin;
     };
-    if (tid == 0) {
-        const double c = 1.4426950408889634 / static_cast<double>(heat);
-        sh.row.top = top;
-        sh.row.c_hi = static_cast<float>(c);
-        sh.row.c_lo = static_cast<float>(c - static_cast<double>(sh.row.c_hi));
-        sh.row.to_bin = static_cast<float>(c) * (kBins / kFarthest);
-    }
-    const float top_p = a.top_p ? a.top_p[b] : 1.0f, min_p = a.min_p ? a.min_p[b] : 0.0f;
+    // log2(e) / T in two floats: the quotient, and what its remainder gives
+    Row row;
+    row.top = top;
+    row.c_hi = __fdiv_rn(1.4426950216293335f, heat);
+    const float rest = fmaf(-row.c_hi, heat, 1.4426950216293335f) + 1.9259629911266175e-8f;
+    row.c_lo = row.c_hi > 0.0f ? __fdividef(rest, heat) : 0.0f;
+    row.to_bin = row.c_hi * (kBins / kFarthest);
     const uint64_t least =
         min_p >= 1.0f ? uint64_t{1} << kOne : max(fraction_of(min_p, uint64_t{1} << kOne, true), uint64_t{1});
     auto block_sum = [&](uint64_t x) {
@@ -489,42 +514,68 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         // Of the candidates, those in the bins that hold the first k; then all pairs of these, eight threads each.
         unsigned long long* names = reinterpret_cast<unsigned long long*>(slice);
         unsigned long long* weights = names + kList;
-        if (tid == 0) sh.count = 0;
-        if (lowest == minus_inf()) {  // a CTA had fewer logits than lines ask for
-            lowest = top;
-            for (int e = tid; e < kList; e += kThreads)
-                if ((e & (room - 1)) < sh.notes[0][e >> room_log].count)
-                    lowest = fminf(lowest, logit_of(static_cast<uint32_t>(sh.list[e] >> 32)));
-            float ignored;
-            block_ends(0.0f, lowest, &ignored, &lowest);
-        }
-        __syncthreads();  // sh.row, too (and sh.low is still zero)
-        const Row row = sh.row;
-        const float to_bin = (kBins - 0.5f) / fmaxf(top - lowest, 1e-30f);
-        auto bin_of = [&](unsigned long long name) {
-            return min(kBins - 1, static_cast<int>((top - logit_of(static_cast<uint32_t>(name >> 32))) * to_bin));
+        // (a name: key and index, so that larger names stand first)
+        auto listed_at = [&](int e) {
+            const bool in = (e & (room - 1)) < sh.notes[0][e >> room_log].count;
+            const unsigned long long name = in ? sh.list[e] : 0;
+            return static_cast<uint32_t>(name >> 32) >= max(key_of(lowest), kNothing + 1) ? name : 0ull;
         };
-        for (int e = tid; e < kList; e += kThreads)
-            if ((e & (room - 1)) < sh.notes[0][e >> room_log].count) atomicAdd(&sh.low[bin_of(sh.list[e])], 1u);
+        if (lowest == minus_inf()) {  // all the CTAs have fewer logits than lines ask for
+            float least_one = top, ignored;
+            for (int e = tid; e < kList; e += kThreads) {
+                const unsigned long long name = listed_at(e);
+                if (name) least_one = fminf(least_one, logit_of(static_cast<uint32_t>(name >> 32)));
+            }
+            block_ends(0.0f, least_one, &ignored, &lowest);
+        }
+        if (tid == 0) sh.count = 0;
+        const float to_bin = (kFewBins - 0.5f) / fmaxf(top - lowest, 1e-30f);
+        auto bin_of = [&](unsigned long long name) {
+            return min(kFewBins - 1, static_cast<int>((top - logit_of(static_cast<uint32_t>(name >> 32))) * to_bin));
+        };
+#pragma unroll
+        for (int e = 0; e < kList; e += kThreads) {
+            const unsigned long long name = listed_at(e + tid);
+            if (name) atomicAdd(&sh.low[bin_of(name)], 1u);
+        }
         __syncthreads();
-        uint64_t unused;
-        const int last = passed(sh.low[2 * tid], sh.low[2 * tid + 1], static_cast<uint64_t>(k), &unused);
+        // every warp for itself: the bin that the first k reach
+        int last;
+        {
+            uint32_t in_bins[8], all = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j++) all += in_bins[j] = sh.low[8 * lane + j];
+            uint32_t upto = all;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += u;
+            }
+            upto -= all;
+            int bin = kFewBins - 1;
+#pragma unroll
+            for (int j = 7; j >= 0; j--) {
+                all -= in_bins[j];
+                if (upto + all < static_cast<uint32_t>(k) && upto + all + in_bins[j] >= static_cast<uint32_t>(k))
+                    bin = 8 * lane + j;
+            }
+            last = __reduce_min_sync(0xFFFFFFFFu, bin);
+        }
+#pragma unroll 1
         for (int e = tid; e < kList; e += kThreads) {
-            if ((e & (room - 1)) >= sh.notes[0][e >> room_log].count) continue;
-            const unsigned long long name = sh.list[e];
-            if (bin_of(name) > last) continue;
+            const unsigned long long name = listed_at(e);
+            if (!name || bin_of(name) > last) continue;
             const uint32_t at = atomicAdd(&sh.count, 1u);
             names[at] = name;
-            weights[at] = weight_of(logit_of(static_cast<uint32_t>(name >> 32)), row, kPowers.e);
+            weights[at] = weight_of(logit_of(static_cast<uint32_t>(name >> 32)), row, sh.table);
         }
         __syncthreads();
         const int n = static_cast<int>(sh.count), sub = tid % 8;
-        // the sum of the first k; what stands before each
-        uint64_t of_first = 0;
-        unsigned long long* before = sh.list;  // (the candidates are no longer needed)
+        // what stands before each; the sum of the first k
+        unsigned long long* before = sh.list;  // (no longer needed)
         for (int i = tid / 8; i < (n + 63) / 64 * 64; i += kThreads / 8) {
             const unsigned long long name = i < n ? names[i] : ~0ull;
-            uint32_t place = 0;
+            int place = 0;
             uint64_t weight = 0;
             for (int j = sub; j < n; j += 8)
                 if (names[j] > name) place++, weight += weights[j];
@@ -534,20 +585,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 weight += __shfl_xor_sync(0xFFFFFFFFu, weight, o);
             }
             if (i < n && sub == 0) {
-                const bool in = place < static_cast<uint32_t>(k);
-                of_first += in ? weights[i] : 0;
-                before[i] = place == 0 ? 0 : in ? weight : ~0ull;
+                before[i] = place < k ? weight : ~0ull;
+                if (place == min(k, n) - 1) sh.found[0] = weight + weights[i];
             }
         }
-        of_first = block_sum(of_first);
-        const uint64_t want = top_p < 1.0f ? max(fraction_of(top_p, of_first, true), uint64_t{1}) : ~uint64_t{0};
+        __syncthreads();
+        const uint64_t want =
+            top_p < 1.0f ? max(fraction_of(top_p, sh.found[0], true), uint64_t{1}) : ~uint64_t{0};
         uint64_t kept = 0;
-        for (int i = tid; i < n; i += kThreads) {
-            if (before[i] >= want || weights[i] < least) weights[i] = 0;
-            kept += weights[i];
+        for (int i = sub == 0 ? tid / 8 : n; i < n; i += kThreads / 8) {
+            const uint64_t w = before[i] >= want || weights[i] < least ? 0 : weights[i];
+            weights[i] = w;
+            kept += w;
         }
-        kept = block_sum(kept);
-        const uint64_t goal = min(fraction_of(a.random[b], kept, false), kept - 1);
+        kept += __shfl_xor_sync(0xFFFFFFFFu, kept, 8);
+        kept += __shfl_xor_sync(0xFFFFFFFFu, kept, 16);
+        if (lane == 0) sh.part[warp][0] = kept;
+        __syncthreads();
+        kept = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) kept += sh.part[w][0];
+        const uint64_t goal = min(fraction_of(random, kept, false), kept - 1);
         for (int i = tid / 8; i < (n + 63) / 64 * 64; i += kThreads / 8) {
             // (the lower half of a name falls as the index rises)
             const uint32_t name = i < n ? static_cast<uint32_t>(names[i]) : 0;
@@ -563,174 +621,143 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     // Long way, any size: bins of the distance from the top over the whole row, then what shares the bin in which the
     // sum passes its goal.
-    for (int i = tid; i < 1024; i += kThreads) sh.table[i] = kPowers.e[i];
-    __syncthreads();
-    const Row row = sh.row;
     auto bin_of = [&](float l) {  // logits without weight are past the last
         const float x = (row.top - l) * row.to_bin;
         return x < static_cast<float>(kBins) ? static_cast<int>(x) : kBins;
     };
-    // Bins of all CTAs, summed: what `in` puts where, the bin in which the sum passes want(all), the sum before it.
-    auto histogram = [&](auto in, bool weighted, auto want_of, uint64_t* want, uint64_t* before) {
-        for (int i = tid; i < kBins; i += kThreads) sh.low[i] = 0, sh.high[i] = 0;
-        __syncthreads();
-        for (int v = tid; v < pieces; v += kThreads) {
-            const P p(reinterpret_cast<const uint4*>(slice)[v]);
-#pragma unroll
-            for (int j = 0; j < VEC; j += 2) {
-                const int at[2] = {in(p[j]), in(p[j + 1])};
-                uint64_t w[2] = {1, 1};
-                if (weighted && (static_cast<uint32_t>(at[0]) < kBins || static_cast<uint32_t>(at[1]) < kBins))
-                    weights_of(p[j], p[j + 1], row, sh.table, w);
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    if (static_cast<uint32_t>(at[i]) >= kBins) continue;
-                    const uint32_t lo = static_cast<uint32_t>(w[i]), old = atomicAdd(&sh.low[at[i]], lo);
-                    if (!weighted) continue;
-                    const uint32_t hi = static_cast<uint32_t>(w[i] >> 32) + (old + lo < old ? 1 : 0);
-                    if (hi) atomicAdd(&sh.high[at[i]], hi);
-                }
-            }
-        }
-        cluster.sync();
-        uint64_t v[2] = {0, 0};
-        for (int r = 0; r < ranks; r++) {
-            const uint2 lo = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sh.low, r) + 2 * tid);
-            const uint2 hi = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sh.high, r) + 2 * tid);
-            v[0] += (static_cast<uint64_t>(hi.x) << 32) + lo.x;
-            v[1] += (static_cast<uint64_t>(hi.y) << 32) + lo.y;
-        }
-        *want = want_of(v[0] + v[1]);
-        return passed(v[0], v[1], *want, before);
-    };
-    // The key at which the sum over the elements with keys above `lowest_key` passes its goal, in falling order, and
-    // the sum above that key.  False: it does not pass.
-    auto select = [&](bool weighted, auto want_of, uint32_t lowest_key, uint32_t* key, uint64_t* want, uint64_t* before) {
-        const int bin = histogram([&](float l) { return key_of(l) > lowest_key ? bin_of(l) : -1; }, weighted, want_of, want, before);
-        if (bin == kBins) {
-            cluster.sync();  // all have read the bins
-            return false;
-        }
-        uint32_t high = 0, low = 0;  // the range of keys that the goal is passed in, once it is known
+    uint32_t cut = kNothing;  // elements with larger keys are kept
+    uint64_t ties = 0;        // and so many of those with this key
+    // First by number (top_k), then, of these, by weight (top_p): the key at which the sum over the elements above
+    // the cut, in falling order, reaches `want`, and the sum before it.
+#pragma unroll 1
+    for (int weighted = 0; weighted < 2; weighted++) {
+        if (weighted ? !(top_p < 1.0f) : !(k > 0 && k < a.V)) continue;
+        const uint64_t of_tie = ties ? weight_of(logit_of(cut), row, sh.table) : 0;
+        uint64_t want = static_cast<uint64_t>(k), before = 0, above = 0;
+        uint32_t high = 0, low = 0;  // the range of keys that it is reached in, once that is known
+        int bin = 0;
+        bool reached = true;
+#pragma unroll 1
         for (bool ranged = false;; ranged = true) {
-            // what is there goes to every CTA's list
-            uint32_t* list = reinterpret_cast<uint32_t*>(sh.list);
-            const int places_each = 2 * kList / ranks;
+            // bins, of the distance from the top, then of keys
+            const int bits = 32 - __clz(high - low), shift = bits > 10 ? bits - 10 : 0;
+            for (int i = tid; i < kBins; i += kThreads) sh.low[i] = 0, sh.high[i] = 0;
             if (tid == 0) sh.count = 0;
             __syncthreads();
+            for (int v = tid; v < pieces; v += kThreads) {
+                const P p(reinterpret_cast<const uint4*>(slice)[v]);
+#pragma unroll
+                for (int j = 0; j < VEC; j += 2) {
+                    int at[2];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t key = key_of(p[j + i]);
+                        at[i] = ranged ? (key >= low && key <= high ? static_cast<int>((high - key) >> shift) : kBins)
+                                       : (key > cut ? bin_of(p[j + i]) : kBins);
+                    }
+                    if (at[0] >= kBins && at[1] >= kBins) continue;
+                    uint64_t w[2] = {1, 1};
+                    if (weighted) weights_of(p[j], p[j + 1], row, sh.table, w);
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        if (at[i] >= kBins) continue;
+                        const uint32_t lo = static_cast<uint32_t>(w[i]), old = atomicAdd(&sh.low[at[i]], lo);
+                        const uint32_t hi = static_cast<uint32_t>(w[i] >> 32) + (old + lo < old ? 1 : 0);
+                        if (hi) atomicAdd(&sh.high[at[i]], hi);
+                    }
+                }
+            }
+            cluster.sync();
+            uint64_t in_bin[2] = {0, 0};
+            for (int r = 0; r < ranks; r++) {
+                const uint2 lo = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sh.low, r) + 2 * tid);
+                const uint2 hi = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(sh.high, r) + 2 * tid);
+                in_bin[0] += (static_cast<uint64_t>(hi.x) << 32) + lo.x;
+                in_bin[1] += (static_cast<uint64_t>(hi.y) << 32) + lo.y;
+            }
+            if (weighted && !ranged) {
+                above = block_sum(in_bin[0] + in_bin[1]);
+                want = max(fraction_of(top_p, above + ties * of_tie, true), uint64_t{1});
+            }
+            uint64_t more = 0;
+            const int found = passed(in_bin[0], in_bin[1], want - before, &more);
+            if (found == kBins) {  // only in the first round: the elements above the cut do not reach it
+                reached = false;
+                break;
+            }
+            before += more;
+            if (ranged) {
+                high -= static_cast<uint32_t>(found) << shift;
+                low = shift == 0 ? high : max(low, high - ((1u << shift) - 1));
+            } else {
+                bin = found;
+            }
+            if (ranged && low == high) break;
+            // what is in that bin goes to every CTA's list
+            uint32_t* list = reinterpret_cast<uint32_t*>(sh.list);
+            const int room_each = 2 * kList / ranks;
             float most = minus_inf(), fewest = __uint_as_float(0x7F800000u);
             for (int v = tid; v < pieces; v += kThreads) {
                 const P p(reinterpret_cast<const uint4*>(slice)[v]);
 #pragma unroll
                 for (int j = 0; j < VEC; j++) {
-                    const uint32_t key_here = key_of(p[j]);
-                    if (ranged ? key_here > high || key_here < low : key_here <= lowest_key || bin_of(p[j]) != bin) continue;
+                    const uint32_t key = key_of(p[j]);
+                    if (ranged ? key > high || key < low : key <= cut || bin_of(p[j]) != bin) continue;
                     most = fmaxf(most, p[j]), fewest = fminf(fewest, p[j]);
                     const uint32_t at = atomicAdd(&sh.count, 1u);
-                    if (at < static_cast<uint32_t>(places_each))
-                        for (int r = 0; r < ranks; r++)
-                            cluster.map_shared_rank(list, r)[rank * places_each + at] = key_here;
+                    if (at < static_cast<uint32_t>(room_each))
+                        for (int r = 0; r < ranks; r++) cluster.map_shared_rank(list, r)[rank * room_each + at] = key;
                 }
             }
             block_ends(most, fewest, &most, &fewest);
             if (tid < ranks)
                 cluster.map_shared_rank(&sh, tid)->notes[1][rank] = {most, fewest, 0, static_cast<int32_t>(sh.count), 0};
             cluster.sync();
-            int n = 0;
+            int n = 0, mine_at = tid;
+            uint32_t own = 0;
+            bool whole = true;
             for (int r = 0; r < ranks; r++) {
-                n += sh.notes[1][r].count;
-                if (sh.notes[1][r].count > places_each) n = 2 * kList + 1;
+                const Note note = sh.notes[1][r];
+                if (mine_at >= 0 && mine_at < note.count && note.count <= room_each) own = list[r * room_each + mine_at];
+                mine_at -= note.count;
+                n += note.count;
+                whole &= note.count <= room_each;
+                if (note.count > 0) most = fmaxf(most, note.top), fewest = fminf(fewest, note.sum);
             }
-            if (n <= kThreads) {
-                // each thread one of them against all
-                uint32_t mine_key = 0;
-                {
-                    int at = tid;
-                    for (int r = 0; r < ranks && at >= 0; r++) {
-                        if (at < sh.notes[1][r].count) {
-                            mine_key = list[r * places_each + at];
-                            at = -1;
-                        } else {
-                            at -= sh.notes[1][r].count;
-                        }
-                    }
-                }
-                uint64_t above = 0, equal = 0;
-                uint64_t* weights = reinterpret_cast<uint64_t*>(sh.low);  // of keys, kThreads of them
+            if (whole && n <= kThreads) {
+                // each thread has one of them, and compares it with all
+                uint64_t* weights = reinterpret_cast<uint64_t*>(sh.low);
                 uint32_t* keys = sh.high;
-                keys[tid] = mine_key;
-                weights[tid] = !weighted ? 1 : tid < n ? weight_of(logit_of(mine_key), row, sh.table) : 0;
+                keys[tid] = own;
+                weights[tid] = !weighted ? 1 : weight_of(logit_of(own), row, sh.table);
                 __syncthreads();
+                uint64_t larger = 0, equal = 0;
                 if (tid < n)
                     for (int j = 0; j < n; j++) {
-                        const uint32_t other = keys[j];
-                        if (other > mine_key)
-                            above += weights[j];
-                        else if (other == mine_key)
-                            equal += weights[j];
+                        larger += keys[j] > own ? weights[j] : 0;
+                        equal += keys[j] == own ? weights[j] : 0;
                     }
-                if (tid < n && *before + above < *want && *want <= *before + above + equal) {
-                    sh.found[0] = mine_key;  // the same from every thread that has this key
-                    sh.found[1] = *before + above;
+                if (tid < n && before + larger < want && want <= before + larger + equal) {
+                    sh.found[0] = own;  // the same from every thread that has this key
+                    sh.found[1] = before + larger;
                 }
                 __syncthreads();
-                *key = static_cast<uint32_t>(sh.found[0]);
-                *before = sh.found[1];
-                return true;
+                high = low = static_cast<uint32_t>(sh.found[0]);
+                before = sh.found[1];
+                break;
             }
-            if (!ranged) {
-                for (int r = 0; r < ranks; r++) {
-                    const Note note = sh.notes[1][r];
-                    if (note.count == 0) continue;
-                    most = fmaxf(most, note.top), fewest = fminf(fewest, note.sum);
-                }
-                high = key_of(most), low = key_of(fewest);
-            }
-            if (high == low) {
-                *key = high;
-                return true;
-            }
-            // narrower: bins of keys
-            const int bits = 32 - __clz(high - low), shift = bits > 10 ? bits - 10 : 0;
-            uint64_t more = 0, left = 0;
-            const uint64_t rest = *want - *before;
-            const int at = histogram(
-                [&](float l) {
-                    const uint32_t q = key_of(l);
-                    return q >= low && q <= high ? static_cast<int>((high - q) >> shift) : -1;
-                },
-                weighted, [&](uint64_t) { return rest; }, &left, &more);
-            *before += more;
-            high -= static_cast<uint32_t>(at) << shift;
-            low = shift == 0 ? high : max(low, high - ((1u << shift) - 1));
+            if (!ranged) high = key_of(most), low = key_of(fewest);
+            if (low == high) break;
         }
-    };
-    uint32_t cut = kNothing;  // elements with larger keys are kept
-    uint64_t ties = 0;        // and so many of those with this key
-    if (k > 0 && k < a.V) {
-        uint32_t key;
-        uint64_t want, before;
-        if (select(false, [&](uint64_t) { return static_cast<uint64_t>(k); }, kNothing, &key, &want, &before))
-            cut = key, ties = k - before;
-    }
-    if (top_p < 1.0f) {
-        const uint64_t of_tie = ties ? weight_of(logit_of(cut), row, sh.table) : 0;
-        uint32_t key;
-        uint64_t want, before, above = 0;
-        const bool inside = select(
-            true,
-            [&](uint64_t x) {
-                above = block_sum(x);
-                return max(fraction_of(top_p, above + ties * of_tie, true), uint64_t{1});
-            },
-            cut, &key, &want, &before);
-        if (inside) {
-            const uint64_t w = weight_of(logit_of(key), row, sh.table);
-            cut = key;
+        if (reached) {
+            const uint64_t w = weighted ? weight_of(logit_of(high), row, sh.table) : 1;
+            cut = high;
             ties = (want - before + w - 1) / w;
-        } else if (of_tie) {  // among the tied ones: those with less than `want` before them
+        } else if (weighted && of_tie) {  // among the tied ones: those with less than `want` before them
             ties = min(ties, (want - above + of_tie - 1) / of_tie);
         }
+        __syncthreads();
+        cluster.sync();  // all have read the bins, the lists and the notes
     }
     // Every thread takes a run of the slice's pieces; a run's sum is that of what lies above the cut, and of as many
     // tied elements as the runs before it leave.
@@ -780,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         seen += sh.sums[r][1];
     }
     // (all that lies before a run: what is above the cut there, and the first of its tied elements)
-    const uint64_t goal = min(fraction_of(a.random[b], total, false), total - 1);
+    const uint64_t goal = min(fraction_of(random, total, false), total - 1);
     ahead += before_slice + kept_of(tied_ahead, 0);
     if (goal >= ahead && goal < ahead + above + kept_of(tied, tied_ahead)) {
         sh.found[0] = tid;
