@@ -500,11 +500,12 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
     // rows without an adapter are copied where the output is not the base itself
     const int idle = copy ? static_cast<int>((a.T - p.n_tokens + kChunk - 1) / kChunk) : 0;
     const int64_t units = static_cast<int64_t>(p.n_chunks + idle) * blocks;
-    const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
-    int held = -1, batch = 1;  // the chunk and projection in shared memory
-    for (int64_t u = units * blockIdx.x / gridDim.x; u < u1; u += batch) {
-        const int c = static_cast<int>(u / blocks);
-        int block = static_cast<int>(u % blocks), i = 0, last = 0;
+    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    int held = -1, batch = 0;  // the chunk and projection in shared memory
+    int c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+    for (int64_t u = u0; u < u1; u += batch, at_block += batch) {
+        if (at_block >= blocks) at_block -= blocks, c++;  // (a batch ends with its projection)
+        int block = at_block, i = 0, last = 0;
         for (; i < a.count; i++) {
             last = static_cast<int>((a.N[i] + 255) / 256);
             if (block < last) break;
@@ -518,15 +519,30 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
         if (c >= p.n_chunks) {
             if (base == y) continue;
             const int first = p.n_tokens + (c - p.n_chunks) * kChunk, n = min(kChunk, static_cast<int>(a.T) - first);
-            for (int r = g; r < n; r += 8) {
-                const int64_t at = token_at(a, p, first + r) * N + n0 + 8 * t;
-                if (vec) {
-                    if (n0 + 8 * t < N)
-                        *reinterpret_cast<uint4*>(y + at) = *reinterpret_cast<const uint4*>(base + at);
-                } else {
-                    for (int j = 0; j < 8; j++)
-                        if (n0 + 8 * t + j < N) y[at + j] = base[at + j];
+            const int rounds = (n + 7) / 8;  // of eight rows a warp
+            batch = static_cast<int>(min(static_cast<int64_t>(min(8 / rounds, last - block)), u1 - u));
+            uint4 v[8];
+            if (vec) {
+#pragma unroll
+                for (int q = 0; q < 8; q++) {
+                    const int r = q % rounds * 8 + g;
+                    const int64_t col = n0 + q / rounds * 256 + 8 * t;
+                    if (q < batch * rounds && r < n && col < N)
+                        v[q] = *reinterpret_cast<const uint4*>(base + token_at(a, p, first + r) * N + col);
                 }
+#pragma unroll
+                for (int q = 0; q < 8; q++) {
+                    const int r = q % rounds * 8 + g;
+                    const int64_t col = n0 + q / rounds * 256 + 8 * t;
+                    if (q < batch * rounds && r < n && col < N)
+                        *reinterpret_cast<uint4*>(y + token_at(a, p, first + r) * N + col) = v[q];
+                }
+            } else {
+                for (int q = 0; q < batch; q++)
+                    for (int r = 0; r < n; r++) {
+                        const int64_t col = n0 + q * 256 + lane, at = token_at(a, p, first + r) * N + col;
+                        if (col < N) y[at] = base[at];
+                    }
             }
             continue;
         }
@@ -536,19 +552,38 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
             held = c * a.count + i;
             __syncthreads();
             const float s = a.scales[chunk.x];
-            for (int e = threadIdx.x; e < (chunk.z + 15) / 16 * 16 * kCols; e += kThreads) {
-                const int row = e / kCols, col = e % kCols;
-                float v = 0.0f;
-                if (row < chunk.z && col < a.rank) {
-                    const float* h = a.h + (static_cast<int64_t>(chunk.y) + row) * R + i * a.rank + col;
-#pragma unroll 4
-                    for (int q = 0; q < n_slices; q++) v += h[static_cast<int64_t>(q) * p.n_tokens * R];
-                    v *= s;
+            // four columns of a row each, up to 4 at a time; the slices in order
+            const int items = (chunk.z + 15) / 16 * 16 * (kCols / 4);
+            for (int e0 = threadIdx.x; e0 < items; e0 += 4 * kThreads) {
+                float4 v[4];
+                int at[4];  // in the chunk's part of a slice
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
+                    v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    at[j] = row < chunk.z && col < a.rank ? row * R + i * a.rank + col : -1;
                 }
-                // to the sum of two bf16 numbers (2^-16 of it)
-                const uint16_t h16 = bf16_bits(v);
-                hi[row * kStride + col] = h16;
-                lo[row * kStride + col] = bf16_bits(v - __uint_as_float(static_cast<uint32_t>(h16) << 16));
+                const float* h = a.h + static_cast<int64_t>(chunk.y) * R;
+#pragma unroll 2
+                for (int q = 0; q < n_slices; q++, h += static_cast<int64_t>(p.n_tokens) * R)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (at[j] >= 0) {
+                            const float4 o = *reinterpret_cast<const float4*>(h + at[j]);
+                            v[j].x += o.x, v[j].y += o.y, v[j].z += o.z, v[j].w += o.w;
+                        }
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
+                    if (e >= items) continue;
+                    // to the sum of two bf16 numbers (2^-16 of it)
+                    const float f[4] = {v[j].x * s, v[j].y * s, v[j].z * s, v[j].w * s};
+                    const uint32_t h01 = f32x2_to_bf16x2(f[0], f[1]), h23 = f32x2_to_bf16x2(f[2], f[3]);
+                    const float2 r01 = bf16x2_to_f32x2(h01), r23 = bf16x2_to_f32x2(h23);
+                    *reinterpret_cast<uint2*>(hi + row * kStride + col) = make_uint2(h01, h23);
+                    *reinterpret_cast<uint2*>(lo + row * kStride + col) = make_uint2(
+                        f32x2_to_bf16x2(f[0] - r01.x, f[1] - r01.y), f32x2_to_bf16x2(f[2] - r23.x, f[3] - r23.y));
+                }
             }
             if (threadIdx.x < kChunk)
                 rows[threadIdx.x] =
