@@ -515,9 +515,9 @@ nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, i
     }
     if (rows > kMaxDim) return NF4_ERR_SHAPE;
     if (T == 0 || rows == 0) return NF4_OK;
-    if (!x || !plan || !workspace || (adapters > 0 && !scales)) return NF4_ERR_NULL;
-    if (!aligned16(x) || !aligned16(plan) || !aligned16(workspace) || !aligned4(scales)) return NF4_ERR_ALIGN;
     const int64_t need = nf4::lora_workspace_bytes(T, adapters, rank, count), pb = nf4::lora_plan_bytes(T, adapters);
+    if (!x || !plan || (need > 0 && !workspace) || (adapters > 0 && !scales)) return NF4_ERR_NULL;
+    if (!aligned16(x) || !aligned16(plan) || !aligned16(workspace) || !aligned4(scales)) return NF4_ERR_ALIGN;
     if (workspace_bytes < need || plan_bytes < pb) return NF4_ERR_SHAPE;
     nf4::LoraArgs args{};
     for (int i = 0; i < count; i++) {  // empty projections are dropped, the order stays

@@ -2,7 +2,8 @@
 //   y[t] = base[t] + s[a] * B[a] (A[a] x[t]),  a the adapter of token t.
 //
 // Tokens are first listed adapter by adapter (lora_plan_kernel, once for all calls of a step), in chunks of up to
-// 64 tokens of one adapter, so that an adapter's matrices are read once a chunk.  Two kernels follow:
+// 64 tokens of one adapter, so that an adapter's matrices are read once a chunk.  Chunks of few tokens, up to 16, stand
+// behind the others: their products are bound by reading A and B, the others' by x and y.  Two kernels follow:
 //   shrink  h = A x for a chunk, the rank columns of all projections side by side; the long axis K is split over
 //           warps and CTAs, and a slice's sums go to the workspace in fp32
 //   expand  adds the slices in order, scales, and adds B h to the base
@@ -17,15 +18,18 @@ namespace nf4 {
 namespace {
 
 constexpr int kChunk = 64;      // tokens of a chunk at most
-constexpr int kHeader = 8;      // int32 before the chunks: T, adapters, chunks, tokens with an adapter
+constexpr int kFew = 16;        // of a chunk of few
+constexpr int kHeader = 8;      // int32 before the chunks: T, adapters, chunks of many, of few, tokens with an adapter
 constexpr int kThreads = 256;
-constexpr int kSliceUnits = 304;  // chunks * slices of K, two CTAs for each of 152 SMs
+constexpr int kUnits = 608;     // of the first product at most, in two rounds of two CTAs for each of 152 SMs
 constexpr int kMaxSlices = 32;
 
 __device__ int g_lora_error;  // 46: an adapter or a row outside its list; 47: a plan of other sizes
 
+__host__ __device__ inline int64_t max_many(int64_t T) { return T / (kFew + 1); }
+__host__ __device__ inline int64_t max_few(int64_t T, int64_t adapters) { return adapters < T ? adapters : T; }
 __host__ __device__ inline int64_t max_chunks(int64_t T, int64_t adapters) {
-    const int64_t n = T / kChunk + (adapters < T ? adapters : T);
+    const int64_t n = max_many(T) + max_few(T, adapters);
     return n < T ? n : T;
 }
 
@@ -37,7 +41,7 @@ __host__ __device__ inline int64_t max_chunks(int64_t T, int64_t adapters) {
 // each warp the places of its tokens, and it walks its run again.  With many lists fewer warps share the work, as
 // their counts have to fit in shared memory.
 constexpr int kPlanWarps = 32;
-constexpr int kPlanCounts = 200 * 1024 / 4 - 2 * (static_cast<int>(kLoraMaxAdapters) + 1);
+constexpr int kPlanCounts = 200 * 1024 / 4 - 3 * (static_cast<int>(kLoraMaxAdapters) + 1);
 
 __host__ __device__ inline int plan_warps(int64_t T, int64_t adapters) {
     const int64_t room = kPlanCounts / (adapters + 1), need = (T + 31) / 32;
@@ -48,11 +52,11 @@ __host__ __device__ inline int plan_warps(int64_t T, int64_t adapters) {
 __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restrict__ ids,
                                                          const int32_t* __restrict__ sequences, int64_t S, int64_t T,
                                                          int adapters, int32_t* __restrict__ plan, int warps) {
-    extern __shared__ int32_t first_of[];  // [adapters + 1] tokens before a list; the same of chunks; counts
+    extern __shared__ int32_t first_of[];  // [adapters + 1] tokens before a list; chunks of many, of few; counts
     const int lists = adapters + 1;
-    int32_t* chunk_at = first_of + lists;
-    int32_t* counts = chunk_at + lists;  // [warps][lists]
-    __shared__ int32_t part[2][32];
+    int32_t *many_at = first_of + lists, *few_at = many_at + lists;
+    int32_t* counts = few_at + lists;  // [warps][lists]
+    __shared__ int32_t part[3][32];
     pdl_launch_dependents();
     for (int i = threadIdx.x; i < warps * lists; i += blockDim.x) counts[i] = 0;
     __syncthreads();
@@ -100,7 +104,13 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     // each thread a run of lists: what the warps before a warp have, the list's tokens; sums over the lists
     const int per = (lists + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
     const int a0 = min(lists, static_cast<int>(threadIdx.x) * per), a1 = min(lists, a0 + per);
-    int32_t n = 0, c = 0;
+    auto many_of = [&](int a, int32_t tokens) {
+        return a < adapters ? tokens / kChunk + (tokens % kChunk > kFew ? 1 : 0) : 0;
+    };
+    auto few_of = [&](int a, int32_t tokens) {
+        return a < adapters && tokens % kChunk != 0 && tokens % kChunk <= kFew ? 1 : 0;
+    };
+    int32_t n[3] = {0, 0, 0}, upto[3];  // tokens, chunks of many, chunks of few
     for (int a = a0; a < a1; a++) {
         int32_t all = 0;
         for (int w = 0; w < warps; w++) {
@@ -109,48 +119,52 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
             all += of_warp;
         }
         first_of[a] = all;
-        n += all;
-        c += a < adapters ? (all + kChunk - 1) / kChunk : 0;
+        n[0] += all, n[1] += many_of(a, all), n[2] += few_of(a, all);
     }
-    int32_t sn = n, sc = c;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int32_t un = __shfl_up_sync(0xFFFFFFFFu, sn, o), uc = __shfl_up_sync(0xFFFFFFFFu, sc, o);
-        if (lane >= o) sn += un, sc += uc;
+    for (int i = 0; i < 3; i++) {
+        upto[i] = n[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t v = __shfl_up_sync(0xFFFFFFFFu, upto[i], o);
+            if (lane >= o) upto[i] += v;
+        }
+        if (lane == 31) part[i][warp] = upto[i];
+        upto[i] -= n[i];
     }
-    if (lane == 31) part[0][warp] = sn, part[1][warp] = sc;
     __syncthreads();
-    int32_t bn = sn - n, bc = sc - c, chunks = 0;
+    int32_t many = 0, few = 0;
     for (int w = 0; w < static_cast<int>(blockDim.x) / 32; w++) {
-        if (w < warp) bn += part[0][w], bc += part[1][w];
-        chunks += part[1][w];
+        if (w < warp) upto[0] += part[0][w], upto[1] += part[1][w], upto[2] += part[2][w];
+        many += part[1][w], few += part[2][w];
     }
-    for (int a = a0; a < a1; a++) {
-        const int32_t tokens = first_of[a];
-        first_of[a] = bn;
-        chunk_at[a] = bc;
-        for (int w = 0; w < warps; w++) counts[w * lists + a] += bn;
-        bn += tokens;
-        bc += a < adapters ? (tokens + kChunk - 1) / kChunk : 0;
-    }
-    __syncthreads();
     int4* out = reinterpret_cast<int4*>(plan + kHeader);
     int32_t* order = plan + kHeader + 4 * max_chunks(T, adapters);
-    for (int i = threadIdx.x; i < chunks; i += blockDim.x) {
+    for (int a = a0; a < a1; a++) {
+        const int32_t tokens = first_of[a];
+        first_of[a] = upto[0];
+        many_at[a] = upto[1];
+        if (few_of(a, tokens))
+            out[many + upto[2]] = make_int4(a, upto[0] + tokens / kChunk * kChunk, tokens % kChunk, 0);
+        for (int w = 0; w < warps; w++) counts[w * lists + a] += upto[0];
+        upto[0] += tokens, upto[1] += many_of(a, tokens), upto[2] += few_of(a, tokens);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < many; i += blockDim.x) {
         int lo = 0, hi = adapters;  // the last list whose first chunk is at most i (lists without chunks come before)
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (chunk_at[mid] <= i)
+            if (many_at[mid] <= i)
                 lo = mid;
             else
                 hi = mid;
         }
-        const int32_t first = first_of[lo] + (i - chunk_at[lo]) * kChunk;
+        const int32_t first = first_of[lo] + (i - many_at[lo]) * kChunk;
         out[i] = make_int4(lo, first, min(kChunk, first_of[lo + 1] - first), 0);
     }
     if (threadIdx.x == 0) {
-        reinterpret_cast<int4*>(plan)[0] = make_int4(static_cast<int32_t>(T), adapters, chunks, first_of[adapters]);
-        reinterpret_cast<int4*>(plan)[1] = make_int4(0, 0, 0, 0);
+        reinterpret_cast<int4*>(plan)[0] = make_int4(static_cast<int32_t>(T), adapters, many, few);
+        reinterpret_cast<int4*>(plan)[1] = make_int4(first_of[adapters], 0, 0, 0);
     }
     walk([&](int64_t t, int list, uint32_t same) {
         const int leader = __ffs(same) - 1;
@@ -175,6 +189,13 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 // Two k steps: rows g and g + 8 of 16 tokens against column g of 8 weights, eight k a lane.
 __device__ __forceinline__ void mma_k32(float (&d)[4], const uint4& x0, const uint4& x1, const uint4& w) {
     mma_bf16(d, x0.x, x1.x, x0.y, x1.y, w.x, w.y);
@@ -183,43 +204,62 @@ __device__ __forceinline__ void mma_k32(float (&d)[4], const uint4& x0, const ui
 
 // The plan as both kernels read it.
 struct Plan {
-    const int4* chunks;
+    const int4* chunks;  // adapter, first place in `order`, tokens
     const int32_t* order;
-    int n_chunks, n_tokens;
+    int n_many, n_few, n_tokens;
 };
 // False (and 47 recorded) if the plan was made for other sizes.
 __device__ __forceinline__ bool read_plan(const LoraArgs& a, Plan* p) {
-    const int4 h = *reinterpret_cast<const int4*>(a.plan);
-    const int64_t most = max_chunks(a.T, a.adapters);
+    const int4 h = reinterpret_cast<const int4*>(a.plan)[0];
     p->chunks = reinterpret_cast<const int4*>(a.plan + kHeader);
-    p->order = a.plan + kHeader + 4 * most;
-    p->n_chunks = h.z, p->n_tokens = h.w;
-    if (h.x != a.T || h.y != a.adapters || h.z < 0 || h.z > most || h.w < 0 || h.w > a.T ||
-        h.w > static_cast<int64_t>(h.z) * kChunk) {
+    p->order = a.plan + kHeader + 4 * max_chunks(a.T, a.adapters);
+    p->n_many = h.z, p->n_few = h.w, p->n_tokens = a.plan[4];
+    if (h.x != a.T || h.y != a.adapters || h.z < 0 || h.z > max_many(a.T) || h.w < 0 || h.w > max_few(a.T, a.adapters) ||
+        h.z + h.w > max_chunks(a.T, a.adapters) || p->n_tokens < 0 || p->n_tokens > a.T) {
         if (threadIdx.x == 0) atomicCAS(&g_lora_error, 0, 47);
         return false;
     }
     return true;
 }
-__device__ __forceinline__ bool chunk_ok(const LoraArgs& a, const Plan& p, const int4& c) {
-    return c.x >= 0 && c.x < a.adapters && c.y >= 0 && c.z > 0 && c.z <= kChunk && c.y + c.z <= p.n_tokens;
+__device__ __forceinline__ bool chunk_ok(const LoraArgs& a, const Plan& p, const int4& c, int most) {
+    return c.x >= 0 && c.x < a.adapters && c.y >= 0 && c.z > 0 && c.z <= most && c.y + c.z <= p.n_tokens;
 }
 __device__ __forceinline__ int64_t token_at(const LoraArgs& a, const Plan& p, int at) {
     return min(static_cast<uint32_t>(p.order[at]), static_cast<uint32_t>(a.T - 1));
 }
-// Slices of K (in units of 64): as many as fill the GPU, each with at least one step of 32 for every warp.
-__device__ __forceinline__ int slices(const LoraArgs& a, const Plan& p) {
-    const int steps = static_cast<int>(a.K / 32 / (kThreads / 32));
-    return max(1, min(min(kMaxSlices, steps), kSliceUnits / max(1, p.n_chunks)));
+constexpr int kFewTiles = 4;    // rank columns of a unit with few tokens, in eights
+constexpr int kManyTiles = 16;  // and with many
+
+// How the first product is cut: rank-column groups, slices of K (in units of 64), and the rows of the workspace that a
+// chunk's slice takes (64 or 16, the chunks of many first).  Slices fill the GPU: with many tokens in one round; with
+// few in two if a warp still has three steps of 32 in each slice, or, if that leaves SMs empty, one step.
+struct Cut {
+    int many_groups, few_groups, many_slices, few_slices;
+    __device__ __forceinline__ int64_t many_row(int chunk, int slice) const {
+        return (static_cast<int64_t>(chunk) * many_slices + slice) * kChunk;
+    }
+    __device__ __forceinline__ int64_t few_row(int many, int chunk, int slice) const {
+        return many_row(many, 0) + (static_cast<int64_t>(chunk) * few_slices + slice) * kFew;
+    }
+};
+__device__ __forceinline__ Cut cut_of(const LoraArgs& a, const Plan& p) {
+    const int tiles = a.count * a.rank / 8, K = static_cast<int>(a.K), most = max(1, min(kMaxSlices, K / 256));
+    Cut c;
+    c.many_groups = (tiles + kManyTiles - 1) / kManyTiles;
+    c.few_groups = (tiles + kFewTiles - 1) / kFewTiles;
+    const int many = max(1, p.n_many * c.many_groups), few = max(1, p.n_few * c.few_groups);
+    c.many_slices = max(1, min(most, kUnits / 2 / many));
+    c.few_slices = max(1, min(most, max(min(kUnits / few, K / 768), kUnits / 4 / few)));
+    return c;
 }
 
 // The sums of a unit (a chunk, a slice of K, some rank columns): parts [part][64][cols] in shared memory, added in
 // order, go to the workspace.  All threads have written theirs.
-__device__ __forceinline__ void write_sums(const LoraArgs& a, const Plan& p, const int4& chunk, int slice, int tile0,
-                                           int tiles, const float* sums, int parts, int stride, int part_stride) {
+__device__ __forceinline__ void write_sums(const LoraArgs& a, int64_t row0, int rows, int tile0, int tiles,
+                                           const float* sums, int parts, int stride, int part_stride) {
     const int R = a.count * a.rank, cols = tiles * 8;
-    float* out = a.h + (static_cast<int64_t>(slice) * p.n_tokens + chunk.y) * R + tile0 * 8;
-    for (int e = threadIdx.x; e < chunk.z * cols / 4; e += kThreads) {
+    float* out = a.h + row0 * R + tile0 * 8;
+    for (int e = threadIdx.x; e < rows * cols / 4; e += kThreads) {
         const int row = e / (cols / 4), col = e % (cols / 4) * 4;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int q = 0; q < parts; q++) {
@@ -240,7 +280,7 @@ __device__ __forceinline__ const uint16_t* column_of(const LoraArgs& a, int adap
 // operands go straight to registers.  MT tiles of 16 tokens, up to NT * 8 columns.
 template <int MT, int NT, int U>
 __device__ __forceinline__ void shrink_few(const LoraArgs& a, const Plan& p, const int4& chunk, int slice, int n_slices,
-                                           int tile0, float* sums) {
+                                           int tile0, int64_t row0, float* sums) {
     constexpr int kStride = NT * 8 + 4;  // (a warp's 64-bit stores: 8 rows, 4 columns apart)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int tiles = min(NT, a.count * a.rank / 8 - tile0);
@@ -305,7 +345,7 @@ __device__ __forceinline__ void shrink_few(const LoraArgs& a, const Plan& p, con
                     }
         __syncthreads();
     }
-    write_sums(a, p, chunk, slice, tile0, tiles, sums, 4, kStride, MT * 16 * kStride);
+    write_sums(a, row0, chunk.z, tile0, tiles, sums, 4, kStride, MT * 16 * kStride);
 }
 
 // A unit with many tokens, up to 64 by 128 columns: bound by the bytes of x, so x is read once for all columns.  Stages
@@ -320,23 +360,23 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
 }
 
 __device__ __forceinline__ void shrink_many(const LoraArgs& a, const Plan& p, const int4& chunk, int slice, int n_slices,
-                                            int tile0, uint8_t* ring) {
+                                            int tile0, int64_t row0, uint8_t* ring) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int tiles = min(16, a.count * a.rank / 8 - tile0);
+    const int tiles = min(kManyTiles, a.count * a.rank / 8 - tile0);
     const int col_groups = tiles > 8 ? 4 : tiles > 4 ? 2 : 1, k_groups = 4 / col_groups;
     const int half = warp % 2, col_group = warp / 2 % col_groups, k_group = warp / 2 / col_groups;
     const int each = (tiles + col_groups - 1) / col_groups, first_tile = col_group * each;
     const int own_tiles = max(0, min(each, tiles - first_tile));
     const int64_t steps = a.K / 64, k0 = 64 * (steps * slice / n_slices), k1 = 64 * (steps * (slice + 1) / n_slices);
-    // what this thread copies: piece `piece` of rows row0, row0 + 16, ...
-    const int piece = threadIdx.x % 16, row0 = threadIdx.x / 16;
+    // what this thread copies: piece `piece` of rows first, first + 16, ...
+    const int piece = threadIdx.x % 16, first = threadIdx.x / 16;
     const uint16_t* src[12];
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        src[i] = a.x + token_at(a, p, chunk.y + min(row0 + 16 * i, chunk.z - 1)) * a.K + piece * 8;
+        src[i] = a.x + token_at(a, p, chunk.y + min(first + 16 * i, chunk.z - 1)) * a.K + piece * 8;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const int col = min(row0 + 16 * i, tiles * 8 - 1);
+        const int col = min(first + 16 * i, tiles * 8 - 1);
         src[4 + i] = column_of(a, chunk.x, tile0 + col / 8, col % 8) + piece * 8;
     }
     auto copy = [&](int64_t k, uint8_t* stage) {
@@ -344,7 +384,7 @@ __device__ __forceinline__ void shrink_many(const LoraArgs& a, const Plan& p, co
         const int64_t at = bytes ? k : 0;
 #pragma unroll
         for (int i = 0; i < 12; i++) {
-            const int row = row0 + 16 * i;  // rows of x, then of A
+            const int row = first + 16 * i;  // rows of x, then of A
             if (i >= 4 && row - kChunk >= tiles * 8) continue;
             cp_async16(stage + piece_at(row, piece), src[i] + at, bytes);
         }
@@ -395,11 +435,8 @@ __device__ __forceinline__ void shrink_many(const LoraArgs& a, const Plan& p, co
                     make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
         }
     __syncthreads();
-    write_sums(a, p, chunk, slice, tile0, tiles, sums, k_groups, stride, part);
+    write_sums(a, row0, chunk.z, tile0, tiles, sums, k_groups, stride, part);
 }
-
-constexpr int kFewTiles = 4;     // rank columns of a unit with few tokens, in eights
-constexpr int kFewTokens = 32;
 
 __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const LoraArgs a) {
     extern __shared__ __align__(16) uint8_t ring[];
@@ -407,21 +444,24 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const LoraArgs a) {
     pdl_wait();
     Plan p;
     if (!read_plan(a, &p)) return;
-    const int n_slices = slices(a, p), tiles = a.count * a.rank / 8;
-    const int64_t pairs = static_cast<int64_t>(p.n_chunks) * n_slices;
-    const int64_t units = pairs * ((tiles + kFewTiles - 1) / kFewTiles);
+    const Cut cut = cut_of(a, p);
+    const int64_t many = static_cast<int64_t>(p.n_many) * cut.many_slices * cut.many_groups;
+    const int64_t units = many + static_cast<int64_t>(p.n_few) * cut.few_slices * cut.few_groups;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t cs = u % pairs;
-        const int group = static_cast<int>(u / pairs);
-        const int4 chunk = p.chunks[cs / n_slices];
-        if (!chunk_ok(a, p, chunk)) continue;
-        const int slice = static_cast<int>(cs % n_slices);
-        if (chunk.z > kFewTokens) {
-            if (group * 16 < tiles) shrink_many(a, p, chunk, slice, n_slices, group * 16, ring);
-        } else if (chunk.z > 16) {
-            shrink_few<2, kFewTiles, 2>(a, p, chunk, slice, n_slices, group * kFewTiles, reinterpret_cast<float*>(ring));
+        // (a chunk's units are neighbours: they read the same x or the same A)
+        if (u < many) {
+            const int group = static_cast<int>(u) % cut.many_groups, rest = static_cast<int>(u) / cut.many_groups;
+            const int slice = rest % cut.many_slices, c = rest / cut.many_slices;
+            const int4 chunk = p.chunks[c];
+            if (chunk_ok(a, p, chunk, kChunk))
+                shrink_many(a, p, chunk, slice, cut.many_slices, group * kManyTiles, cut.many_row(c, slice), ring);
         } else {
-            shrink_few<1, kFewTiles, 3>(a, p, chunk, slice, n_slices, group * kFewTiles, reinterpret_cast<float*>(ring));
+            const int v = static_cast<int>(u - many), group = v % cut.few_groups, rest = v / cut.few_groups;
+            const int slice = rest % cut.few_slices, c = rest / cut.few_slices;
+            const int4 chunk = p.chunks[p.n_many + c];
+            if (chunk_ok(a, p, chunk, kFew))
+                shrink_few<1, kFewTiles, 3>(a, p, chunk, slice, cut.few_slices, group * kFewTiles,
+                                            cut.few_row(p.n_many, c, slice), reinterpret_cast<float*>(ring));
         }
     }
 }
@@ -432,18 +472,20 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const LoraArgs a) {
 template <int W>
 struct Weights {
     uint4 w[4][W];
-    __device__ __forceinline__ void load(const uint16_t* b, int64_t n0, int64_t N, int rank, int g, int t) {
+    static constexpr int kLane = 8;  // values of a row that a lane takes
+    // rows `from`, from + 2, ... behind p; one past `last` reads that instead (its results are not stored)
+    __device__ __forceinline__ void load(const uint16_t* p, int from, int last, int rank, int t) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const int64_t n = n0 + 8 * (g / 2) + 2 * j + g % 2;
+            const uint16_t* row = p + static_cast<int64_t>(min(from + 2 * j, last)) * rank;
 #pragma unroll
             for (int k = 0; k < W; k++) {
                 w[j][k] = make_uint4(0, 0, 0, 0);
-                if (n < N && k * 32 + 8 * t < rank)
-                    w[j][k] = __ldg(reinterpret_cast<const uint4*>(b + n * rank + k * 32 + 8 * t));
+                if (k * 32 + 8 * t < rank) w[j][k] = __ldg(reinterpret_cast<const uint4*>(row + k * 32));
             }
         }
     }
+    // acc: the product of 16 tokens, rows row .. of hi + lo, and these 32 rows of B
     __device__ __forceinline__ void multiply(float (&acc)[4][4], const uint16_t* hi, const uint16_t* lo, int row, int stride,
                                              int t) const {
 #pragma unroll
@@ -453,7 +495,11 @@ struct Weights {
             const uint4 h0 = lds128(hi + at), h1 = lds128(hi + at + 8 * stride);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                mma_k32(acc[j], l0, l1, w[j][k]);
+                if (k == 0)
+                    mma_bf16_first(acc[j], l0.x, l1.x, l0.y, l1.y, w[j][k].x, w[j][k].y);
+                else
+                    mma_bf16(acc[j], l0.x, l1.x, l0.y, l1.y, w[j][k].x, w[j][k].y);
+                mma_bf16(acc[j], l0.z, l1.z, l0.w, l1.w, w[j][k].z, w[j][k].w);
                 mma_k32(acc[j], h0, h1, w[j][k]);
             }
         }
@@ -462,12 +508,13 @@ struct Weights {
 template <>
 struct Weights<0> {
     uint2 w[4];
-    __device__ __forceinline__ void load(const uint16_t* b, int64_t n0, int64_t N, int rank, int g, int t) {
+    static constexpr int kLane = 4;
+    __device__ __forceinline__ void load(const uint16_t* p, int from, int last, int rank, int t) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const int64_t n = n0 + 8 * (g / 2) + 2 * j + g % 2;
             w[j] = make_uint2(0, 0);
-            if (n < N && 4 * t < rank) w[j] = __ldg(reinterpret_cast<const uint2*>(b + n * rank + 4 * t));
+            if (4 * t < rank)
+                w[j] = __ldg(reinterpret_cast<const uint2*>(p + static_cast<int64_t>(min(from + 2 * j, last)) * rank));
         }
     }
     __device__ __forceinline__ void multiply(float (&acc)[4][4], const uint16_t* hi, const uint16_t* lo, int row, int stride,
@@ -477,185 +524,231 @@ struct Weights<0> {
         const uint2 h0 = *reinterpret_cast<const uint2*>(hi + at), h1 = *reinterpret_cast<const uint2*>(hi + at + 8 * stride);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            mma_bf16(acc[j], l0.x, l1.x, l0.y, l1.y, w[j].x, w[j].y);
+            mma_bf16_first(acc[j], l0.x, l1.x, l0.y, l1.y, w[j].x, w[j].y);
             mma_bf16(acc[j], h0.x, h1.x, h0.y, h1.y, w[j].x, w[j].y);
         }
     }
 };
 
+// Which 256 rows of which projection a unit has.
+struct Block {
+    int i, first, left;  // the projection, its first row, and how many blocks from here on it has
+};
+__device__ __forceinline__ Block block_of(const LoraArgs& a, int block) {
+    Block r{0, 0, 0};
+    for (;; r.i++) {
+        r.left = static_cast<int>((a.N[r.i] + 255) / 256) - block;
+        if (r.left > 0 || r.i + 1 == a.count) break;
+        block -= static_cast<int>((a.N[r.i] + 255) / 256);
+    }
+    r.first = block * 256;
+    return r;
+}
+
+// h of a chunk for one projection: its slices from `h` on, `step` floats apart, summed in order, times s, as the sum of
+// two bf16 numbers (2^-16 of it), rows of kStride; zeros up to whole tiles.
+template <int kCols, int kStride>
+__device__ __forceinline__ void stage_h(const float* h, int R, int rank, int tokens, int n_slices, int step, float s,
+                                        uint16_t* hi, uint16_t* lo) {
+    // four columns of a row each, up to four such at a time
+    const int items = (tokens + 15) / 16 * 16 * (kCols / 4);
+    for (int e0 = threadIdx.x; e0 < items; e0 += 4 * kThreads) {
+        float4 v[4];
+        int at[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
+            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            at[j] = row < tokens && col < rank ? row * R + col : -1;
+        }
+#pragma unroll 2
+        for (int q = 0; q < n_slices; q++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (at[j] >= 0) {
+                    const float4 o = *reinterpret_cast<const float4*>(h + q * step + at[j]);
+                    v[j].x += o.x, v[j].y += o.y, v[j].z += o.z, v[j].w += o.w;
+                }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
+            if (e >= items) continue;
+            const float f[4] = {v[j].x * s, v[j].y * s, v[j].z * s, v[j].w * s};
+            const uint32_t h01 = f32x2_to_bf16x2(f[0], f[1]), h23 = f32x2_to_bf16x2(f[2], f[3]);
+            const float2 r01 = bf16x2_to_f32x2(h01), r23 = bf16x2_to_f32x2(h23);
+            *reinterpret_cast<uint2*>(hi + row * kStride + col) = make_uint2(h01, h23);
+            *reinterpret_cast<uint2*>(lo + row * kStride + col) =
+                make_uint2(f32x2_to_bf16x2(f[0] - r01.x, f[1] - r01.y), f32x2_to_bf16x2(f[2] - r23.x, f[3] - r23.y));
+        }
+    }
+}
+
+// Adds a lane's eight results (row h * 8 + g of a tile) to the base, at `base` and `y`: columns col .. col + 7 of N.
+__device__ __forceinline__ void add_row(const uint16_t* base, uint16_t* y, const uint4& v, const float (&acc)[4][4], int h,
+                                        bool vec, int col, int N) {
+    if (vec) {
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t out[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 f = bf16x2_to_f32x2(in[j]);
+            out[j] = f32x2_to_bf16x2(f.x + acc[j][2 * h], f.y + acc[j][2 * h + 1]);
+        }
+        *reinterpret_cast<uint4*>(y) = make_uint4(out[0], out[1], out[2], out[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (col + j < N)
+                y[j] = bf16_bits(__uint_as_float(static_cast<uint32_t>(base[j]) << 16) + acc[j / 2][2 * h + j % 2]);
+    }
+}
+
 // A unit is a chunk and 256 rows of one projection, 32 a warp.  Bound by the bytes of y (many tokens) or of B (few), so
-// all that a warp needs is on its way before anything is multiplied: B's rows and the base of D units with few
-// tokens, or those of one unit and up to 64 tokens.
+// what a warp needs is on its way before anything is multiplied: B's rows and the base of up to 64 tokens, or those of
+// D units with few tokens.
 template <int W, int D>
 __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, int blocks, bool copy) {
     constexpr int kCols = W ? W * 32 : 16, kStride = kCols + 8;
     __shared__ __align__(16) uint16_t hi[kChunk * kStride], lo[kChunk * kStride];
     __shared__ int32_t rows[kChunk];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4, warp_row = threadIdx.x / 32 * 32;
     pdl_launch_dependents();
     pdl_wait();
     Plan p;
     if (!read_plan(a, &p)) return;
-    const int n_slices = slices(a, p), R = a.count * a.rank;
+    const Cut cut = cut_of(a, p);
+    const int R = a.count * a.rank;
+    auto stage = [&](const int4& chunk, int i, int64_t row0, int n_slices, int rows_each) {
+        __syncthreads();
+        stage_h<kCols, kStride>(a.h + row0 * R + i * a.rank, R, a.rank, chunk.z, n_slices, rows_each * R, a.scales[chunk.x],
+                                hi, lo);
+        if (threadIdx.x < kChunk)
+            rows[threadIdx.x] =
+                static_cast<int32_t>(token_at(a, p, chunk.y + min(static_cast<int>(threadIdx.x), chunk.z - 1)));
+        __syncthreads();
+    };
+    // this lane's first row of B in a block, behind `first`
+    auto rows_of_b = [&](int i, int adapter, int first_row) {
+        return a.b[i] + (static_cast<int64_t>(adapter) * a.N[i] + first_row) * a.rank + Weights<W>::kLane * t;
+    };
+    {
+        const int64_t units = static_cast<int64_t>(p.n_many) * blocks;
+        const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+        int held = -1, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+#pragma unroll 1
+        for (int64_t u = u0; u < u1; u++, at_block++) {
+            if (at_block == blocks) at_block = 0, c++;
+            const Block block = block_of(a, at_block);
+            const int i = block.i, N = static_cast<int>(a.N[i]), n0 = block.first + warp_row, n = n0 + 8 * t;
+            const int4 chunk = p.chunks[c];
+            if (!chunk_ok(a, p, chunk, kChunk)) continue;
+            if (held != c * a.count + i) {
+                held = c * a.count + i;
+                stage(chunk, i, cut.many_row(c, 0), cut.many_slices, kChunk);
+            }
+            if (n0 >= N) continue;
+            const bool vec = N % 8 == 0, in_row = n < N;
+            const int first_row = n0 + 8 * (g / 2) + g % 2;
+            const uint16_t* base = a.base[i] + n;
+            uint16_t* y = a.y[i] + n;
+            Weights<W> w;
+            w.load(rows_of_b(i, chunk.x, first_row), 0, N - 1 - first_row, a.rank, t);
+            constexpr int kTiles = W >= 2 ? 2 : 4;  // tiles of 16 tokens whose base is on its way
+#pragma unroll 1
+            for (int r0 = g; r0 - g < chunk.z; r0 += 16 * kTiles) {
+                uint4 in[2 * kTiles];
+#pragma unroll
+                for (int m = 0; m < 2 * kTiles; m++)
+                    if (vec && in_row && r0 + 8 * m < chunk.z)
+                        in[m] = *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(rows[r0 + 8 * m]) * N);
+#pragma unroll
+                for (int m = 0; m < 2 * kTiles; m += 2) {
+                    if (r0 - g + 8 * m >= chunk.z) continue;
+                    float acc[4][4];
+                    w.multiply(acc, hi, lo, r0 + 8 * m, kStride, t);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int r = r0 + 8 * (m + h);
+                        if (r >= chunk.z || !in_row) continue;
+                        const int64_t at = static_cast<int64_t>(rows[r]) * N;
+                        add_row(base + at, y + at, in[m + h], acc, h, vec, n, N);
+                    }
+                }
+            }
+        }
+    }
     // rows without an adapter are copied where the output is not the base itself
     const int idle = copy ? static_cast<int>((a.T - p.n_tokens + kChunk - 1) / kChunk) : 0;
-    const int64_t units = static_cast<int64_t>(p.n_chunks + idle) * blocks;
+    const int64_t units = static_cast<int64_t>(p.n_few + idle) * blocks;
     const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    int held = -1, batch = 0;  // the chunk and projection in shared memory
-    int c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+    int held = -1, batch = 0, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+#pragma unroll 1
     for (int64_t u = u0; u < u1; u += batch, at_block += batch) {
         if (at_block >= blocks) at_block -= blocks, c++;  // (a batch ends with its projection)
-        int block = at_block, i = 0, last = 0;
-        for (; i < a.count; i++) {
-            last = static_cast<int>((a.N[i] + 255) / 256);
-            if (block < last) break;
-            block -= last;
-        }
-        const int64_t N = a.N[i], n0 = static_cast<int64_t>(block) * 256 + warp * 32;
-        const uint16_t* base = a.base[i];
-        uint16_t* y = a.y[i];
+        const Block block = block_of(a, at_block);
+        const int i = block.i, N = static_cast<int>(a.N[i]), n0 = block.first + warp_row, n = n0 + 8 * t;
+        const int left = static_cast<int>(min(static_cast<int64_t>(block.left), u1 - u));
         const bool vec = N % 8 == 0;
+        const uint16_t* base = a.base[i] + n;
+        uint16_t* y = a.y[i] + n;
         batch = 1;
-        if (c >= p.n_chunks) {
+        if (c >= p.n_few) {
             if (base == y) continue;
-            const int first = p.n_tokens + (c - p.n_chunks) * kChunk, n = min(kChunk, static_cast<int>(a.T) - first);
-            const int rounds = (n + 7) / 8;  // of eight rows a warp
-            batch = static_cast<int>(min(static_cast<int64_t>(min(8 / rounds, last - block)), u1 - u));
-            uint4 v[8];
+            const int first = p.n_tokens + (c - p.n_few) * kChunk, tokens = min(kChunk, static_cast<int>(a.T) - first);
+            const int rounds = (tokens + 7) / 8;  // of eight rows a warp
+            batch = min(8 / rounds, left);
             if (vec) {
+                uint4 v[8];
+                int64_t at[8];
 #pragma unroll
                 for (int q = 0; q < 8; q++) {
-                    const int r = q % rounds * 8 + g;
-                    const int64_t col = n0 + q / rounds * 256 + 8 * t;
-                    if (q < batch * rounds && r < n && col < N)
-                        v[q] = *reinterpret_cast<const uint4*>(base + token_at(a, p, first + r) * N + col);
+                    const int r = q % rounds * 8 + g, more = q / rounds * 256;
+                    at[q] = q < batch * rounds && r < tokens && n + more < N ? token_at(a, p, first + r) * N + more : -1;
+                    if (at[q] >= 0) v[q] = *reinterpret_cast<const uint4*>(base + at[q]);
                 }
 #pragma unroll
-                for (int q = 0; q < 8; q++) {
-                    const int r = q % rounds * 8 + g;
-                    const int64_t col = n0 + q / rounds * 256 + 8 * t;
-                    if (q < batch * rounds && r < n && col < N)
-                        *reinterpret_cast<uint4*>(y + token_at(a, p, first + r) * N + col) = v[q];
-                }
+                for (int q = 0; q < 8; q++)
+                    if (at[q] >= 0) *reinterpret_cast<uint4*>(y + at[q]) = v[q];
             } else {
                 for (int q = 0; q < batch; q++)
-                    for (int r = 0; r < n; r++) {
-                        const int64_t col = n0 + q * 256 + lane, at = token_at(a, p, first + r) * N + col;
-                        if (col < N) y[at] = base[at];
+                    for (int r = 0; r < tokens; r++) {
+                        const int col = n0 + q * 256 + lane;
+                        const int64_t at = token_at(a, p, first + r) * N + col;
+                        if (col < N) a.y[i][at] = a.base[i][at];
                     }
             }
             continue;
         }
-        const int4 chunk = p.chunks[c];
-        if (!chunk_ok(a, p, chunk)) continue;
+        const int4 chunk = p.chunks[p.n_many + c];
+        if (!chunk_ok(a, p, chunk, kFew)) continue;
         if (held != c * a.count + i) {
             held = c * a.count + i;
-            __syncthreads();
-            const float s = a.scales[chunk.x];
-            // four columns of a row each, up to 4 at a time; the slices in order
-            const int items = (chunk.z + 15) / 16 * 16 * (kCols / 4);
-            for (int e0 = threadIdx.x; e0 < items; e0 += 4 * kThreads) {
-                float4 v[4];
-                int at[4];  // in the chunk's part of a slice
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
-                    v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    at[j] = row < chunk.z && col < a.rank ? row * R + i * a.rank + col : -1;
-                }
-                const float* h = a.h + static_cast<int64_t>(chunk.y) * R;
-#pragma unroll 2
-                for (int q = 0; q < n_slices; q++, h += static_cast<int64_t>(p.n_tokens) * R)
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        if (at[j] >= 0) {
-                            const float4 o = *reinterpret_cast<const float4*>(h + at[j]);
-                            v[j].x += o.x, v[j].y += o.y, v[j].z += o.z, v[j].w += o.w;
-                        }
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
-                    if (e >= items) continue;
-                    // to the sum of two bf16 numbers (2^-16 of it)
-                    const float f[4] = {v[j].x * s, v[j].y * s, v[j].z * s, v[j].w * s};
-                    const uint32_t h01 = f32x2_to_bf16x2(f[0], f[1]), h23 = f32x2_to_bf16x2(f[2], f[3]);
-                    const float2 r01 = bf16x2_to_f32x2(h01), r23 = bf16x2_to_f32x2(h23);
-                    *reinterpret_cast<uint2*>(hi + row * kStride + col) = make_uint2(h01, h23);
-                    *reinterpret_cast<uint2*>(lo + row * kStride + col) = make_uint2(
-                        f32x2_to_bf16x2(f[0] - r01.x, f[1] - r01.y), f32x2_to_bf16x2(f[2] - r23.x, f[3] - r23.y));
-                }
-            }
-            if (threadIdx.x < kChunk)
-                rows[threadIdx.x] =
-                    static_cast<int32_t>(token_at(a, p, chunk.y + min(static_cast<int>(threadIdx.x), chunk.z - 1)));
-            __syncthreads();
+            stage(chunk, i, cut.few_row(p.n_many, c, 0), cut.few_slices, kFew);
         }
-        const uint16_t* b = a.b[i] + static_cast<int64_t>(chunk.x) * N * a.rank;
-        // token r's eight values from column n on: base in, y out
-        auto fetch = [&](int r, int64_t n) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (vec && r < chunk.z && n < N) v = *reinterpret_cast<const uint4*>(base + rows[r] * N + n);
-            return v;
-        };
-        auto store = [&](int r, int64_t n, const uint4& v, const float (&acc)[4][4], int h) {
-            if (r >= chunk.z) return;
-            const int64_t at = rows[r] * N + n;
-            if (vec) {
-                if (n >= N) return;
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t out[4];
+        batch = min(D, left);
+        const int first_row = n0 + 8 * (g / 2) + g % 2;
+        const uint16_t* b = rows_of_b(i, chunk.x, first_row);
+        const int64_t at[2] = {static_cast<int64_t>(rows[g]) * N, static_cast<int64_t>(rows[g + 8]) * N};
+        const bool real[2] = {g < chunk.z, g + 8 < chunk.z}, both = chunk.z > 8;
+        Weights<W> w[D];
+        uint4 in[D][2];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float2 f = bf16x2_to_f32x2(in[j]);
-                    out[j] = f32x2_to_bf16x2(f.x + acc[j][2 * h], f.y + acc[j][2 * h + 1]);
-                }
-                *reinterpret_cast<uint4*>(y + at) = make_uint4(out[0], out[1], out[2], out[3]);
-            } else {
+        for (int d = 0; d < D; d++) {
+            if (d >= batch) continue;
+            w[d].load(b, 256 * d, N - 1 - first_row, a.rank, t);
 #pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (n + j < N)
-                        y[at + j] = bf16_bits(__uint_as_float(static_cast<uint32_t>(base[at + j]) << 16) +
-                                              acc[j / 2][2 * h + j % 2]);
-            }
-        };
-        if (chunk.z <= 16) {
-            batch = static_cast<int>(min(static_cast<int64_t>(min(D, last - block)), u1 - u));
-            Weights<W> w[D];
-            uint4 in[D][2];
+            for (int h = 0; h < 2; h++)
+                if (vec && real[h] && n + 256 * d < N) in[d][h] = *reinterpret_cast<const uint4*>(base + at[h] + 256 * d);
+        }
 #pragma unroll
-            for (int d = 0; d < D; d++) {
-                const int64_t n = n0 + 256 * d, edge = d < batch ? N : 0;
-                w[d].load(b, n, edge, a.rank, g, t);
-                in[d][0] = in[d][1] = make_uint4(0, 0, 0, 0);
-                if (d < batch) in[d][0] = fetch(g, n + 8 * t), in[d][1] = fetch(g + 8, n + 8 * t);
-            }
-#pragma unroll
-            for (int d = 0; d < D; d++) {
-                if (d >= batch) continue;
-                float acc[4][4] = {};
-                w[d].multiply(acc, hi, lo, g, kStride, t);
-                store(g, n0 + 256 * d + 8 * t, in[d][0], acc, 0);
-                store(g + 8, n0 + 256 * d + 8 * t, in[d][1], acc, 1);
-            }
-        } else if (n0 < N) {
-            constexpr int kTiles = W >= 4 ? 2 : 4;  // tiles of 16 tokens whose base is on its way
-            Weights<W> w;
-            w.load(b, n0, N, a.rank, g, t);
-            for (int m0 = 0; m0 * 16 < chunk.z; m0 += kTiles) {
-                uint4 in[kTiles][2];
-#pragma unroll
-                for (int m = 0; m < kTiles; m++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) in[m][h] = fetch((m0 + m) * 16 + h * 8 + g, n0 + 8 * t);
-#pragma unroll
-                for (int m = 0; m < kTiles; m++) {
-                    if ((m0 + m) * 16 >= chunk.z) continue;
-                    float acc[4][4] = {};
-                    w.multiply(acc, hi, lo, (m0 + m) * 16 + g, kStride, t);
-#pragma unroll
-                    for (int h = 0; h < 2; h++) store((m0 + m) * 16 + h * 8 + g, n0 + 8 * t, in[m][h], acc, h);
-                }
-            }
+        for (int d = 0; d < D; d++) {
+            if (d >= batch) continue;
+            float acc[4][4];
+            w[d].multiply(acc, hi, lo, g, kStride, t);
+            const int64_t more = 256 * d;
+            if (n + 256 * d >= N) continue;
+            if (real[0]) add_row(base + at[0] + more, y + at[0] + more, in[d][0], acc, 0, vec, n + 256 * d, N);
+            if (both && real[1]) add_row(base + at[1] + more, y + at[1] + more, in[d][1], acc, 1, vec, n + 256 * d, N);
         }
     }
 }
@@ -676,10 +769,12 @@ int64_t lora_plan_bytes(int64_t T, int64_t adapters) {
 }
 
 int64_t lora_workspace_bytes(int64_t T, int64_t adapters, int64_t rank, int64_t count) {
-    (void)adapters;
-    // tokens * slices: at most kMaxSlices each, and a chunk's 64 tokens kSliceUnits times in all
-    int64_t rows = T > kChunk * kSliceUnits ? T : int64_t{kChunk} * kSliceUnits;
-    if (rows > T * kMaxSlices) rows = T * kMaxSlices;
+    // chunks * slices: kMaxSlices each at most, and so many in all as the slices' rule allows
+    auto rows_of = [](int64_t chunks, int64_t units, int64_t each) {
+        const int64_t most = chunks > units ? chunks : units;
+        return each * (chunks * kMaxSlices < most ? chunks * kMaxSlices : most);
+    };
+    const int64_t rows = rows_of(max_many(T), kUnits / 2, kChunk) + rows_of(max_few(T, adapters), kUnits, kFew);
     return rows * rank * count * static_cast<int64_t>(sizeof(float));
 }
 
@@ -697,7 +792,7 @@ cudaError_t launch_lora_plan(const int32_t* ids, const int32_t* sequences, int64
     const int warps = plan_warps(T, adapters);
     const int threads = warps <= 8 && adapters < 256 ? 256 : 1024;
     cudaLaunchConfig_t cfg = pdl_config(dim3(1), threads, stream, &attr);
-    cfg.dynamicSmemBytes = (2 + warps) * (adapters + 1) * sizeof(int32_t);
+    cfg.dynamicSmemBytes = (3 + warps) * (adapters + 1) * sizeof(int32_t);
     return cudaLaunchKernelEx(&cfg, lora_plan_kernel, ids, sequences, S, T, static_cast<int>(adapters),
                               static_cast<int32_t*>(plan), warps);
 }
@@ -730,9 +825,9 @@ cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
     }
     const int64_t most = (chunks + (copy ? (a.T + kChunk - 1) / kChunk : 0)) * blocks;
     if (most == 0) return cudaSuccess;  // no adapters, and in place
-    if (a.rank <= 16) return expand<0, 4>(a, blocks, copy, most, num_sms, stream);
-    if (a.rank <= 32) return expand<1, 3>(a, blocks, copy, most, num_sms, stream);
-    if (a.rank <= 64) return expand<2, 2>(a, blocks, copy, most, num_sms, stream);
+    if (a.rank <= 16) return expand<0, 3>(a, blocks, copy, most, num_sms, stream);
+    if (a.rank <= 32) return expand<1, 2>(a, blocks, copy, most, num_sms, stream);
+    if (a.rank <= 64) return expand<2, 1>(a, blocks, copy, most, num_sms, stream);
     return expand<4, 1>(a, blocks, copy, most, num_sms, stream);
 }
 

@@ -160,8 +160,9 @@ def test_many_adapters_and_tokens():
 def plan_lists(plan, t, adapters):
     words = plan.view(torch.int32).tolist()
     assert words[:2] == [t, adapters]
-    n_chunks, n_tokens = words[2:4]
-    chunks = [words[8 + 4 * i:11 + 4 * i] for i in range(n_chunks)]
+    many, few, n_tokens = words[2:5]
+    chunks = [words[8 + 4 * i:11 + 4 * i] for i in range(many + few)]
+    assert all(n > 16 for _, _, n in chunks[:many]) and all(n <= 16 for _, _, n in chunks[many:])
     order = words[len(words) - t:]
     return chunks, order, n_tokens
 
@@ -177,7 +178,7 @@ def test_plan(t, adapters, layout):
     want = sorted(range(t), key=lambda i: (ids[i] < 0, ids[i]))  # stable
     assert order == want and n_tokens == sum(i >= 0 for i in ids)
     at = 0
-    for adapter, first, n in chunks:
+    for adapter, first, n in sorted(chunks, key=lambda c: c[1]):
         assert first == at and 1 <= n <= 64
         assert all(ids[i] == adapter for i in order[first:first + n])
         at += n
