@@ -438,7 +438,7 @@ __device__ __forceinline__ void shrink_many(const LoraArgs& a, const Plan& p, co
     write_sums(a, row0, chunk.z, tile0, tiles, sums, k_groups, stride, part);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const LoraArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_constant__ LoraArgs a) {
     extern __shared__ __align__(16) uint8_t ring[];
     pdl_launch_dependents();
     pdl_wait();
@@ -472,8 +472,16 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const LoraArgs a) {
 template <int W>
 struct Weights {
     uint4 w[4][W];
-    static constexpr int kLane = 8;  // values of a row that a lane takes
-    // rows `from`, from + 2, ... behind p; one past `last` reads that instead (its results are not stored)
+    static constexpr int kLane = 8, kCols = W * 32;  // values of a row that a lane takes at a time, that fit
+    // Rows `from`, from + 2, ... behind p, all there and of kCols values: every address is a constant away.
+    __device__ __forceinline__ void load_whole(const uint16_t* p, int from) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int k = 0; k < W; k++)
+                w[j][k] = __ldg(reinterpret_cast<const uint4*>(p + (from + 2 * j) * kCols + k * 32));
+    }
+    // Any: a row past `last` reads that instead (its results are not stored), columns from the rank on are zeros.
     __device__ __forceinline__ void load(const uint16_t* p, int from, int last, int rank, int t) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -508,7 +516,11 @@ struct Weights {
 template <>
 struct Weights<0> {
     uint2 w[4];
-    static constexpr int kLane = 4;
+    static constexpr int kLane = 4, kCols = 16;
+    __device__ __forceinline__ void load_whole(const uint16_t* p, int from) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) w[j] = __ldg(reinterpret_cast<const uint2*>(p + (from + 2 * j) * kCols));
+    }
     __device__ __forceinline__ void load(const uint16_t* p, int from, int last, int rank, int t) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -545,16 +557,48 @@ __device__ __forceinline__ Block block_of(const LoraArgs& a, int block) {
     return r;
 }
 
+// v * s as the sum of two bf16 numbers each.
+__device__ __forceinline__ void split_h(const float4& v, float s, uint16_t* hi, uint16_t* lo) {
+    const float f[4] = {v.x * s, v.y * s, v.z * s, v.w * s};
+    const uint32_t h01 = f32x2_to_bf16x2(f[0], f[1]), h23 = f32x2_to_bf16x2(f[2], f[3]);
+    const float2 r01 = bf16x2_to_f32x2(h01), r23 = bf16x2_to_f32x2(h23);
+    *reinterpret_cast<uint2*>(hi) = make_uint2(h01, h23);
+    *reinterpret_cast<uint2*>(lo) =
+        make_uint2(f32x2_to_bf16x2(f[0] - r01.x, f[1] - r01.y), f32x2_to_bf16x2(f[2] - r23.x, f[3] - r23.y));
+}
+
 // h of a chunk for one projection: its slices from `h` on, `step` floats apart, summed in order, times s, as the sum of
 // two bf16 numbers (2^-16 of it), rows of kStride; zeros up to whole tiles.
+// (The thread's number is hidden from the compiler: it would work the places out ahead of the loop that stages now and
+// then, and keep them in registers that the loop needs.)
 template <int kCols, int kStride>
 __device__ __forceinline__ void stage_h(const float* h, int R, int rank, int tokens, int n_slices, int step, float s,
                                         uint16_t* hi, uint16_t* lo) {
     // four columns of a row each, up to four such at a time
     const int items = (tokens + 15) / 16 * 16 * (kCols / 4);
-    for (int e0 = threadIdx.x; e0 < items; e0 += 4 * kThreads) {
+    int thread = threadIdx.x;
+    asm volatile("" : "+r"(thread));
+    for (int e0 = thread; e0 < items; e0 += 4 * kThreads) {
         float4 v[4];
         int at[4];
+        if (items <= kThreads) {  // one item a thread: four slices at a time
+            const int row = e0 / (kCols / 4), col = e0 % (kCols / 4) * 4;
+            const float* from = h + row * R + col;
+            v[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (row < tokens && col < rank)
+                for (int q0 = 0; q0 < n_slices; q0 += 4) {
+                    float4 o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if (q0 + q < n_slices) o[q] = *reinterpret_cast<const float4*>(from + (q0 + q) * step);
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        if (q0 + q < n_slices)
+                            v[0].x += o[q].x, v[0].y += o[q].y, v[0].z += o[q].z, v[0].w += o[q].w;
+                }
+            split_h(v[0], s, hi + row * kStride + col, lo + row * kStride + col);
+            break;
+        }
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
@@ -572,13 +616,7 @@ __device__ __forceinline__ void stage_h(const float* h, int R, int rank, int tok
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
-            if (e >= items) continue;
-            const float f[4] = {v[j].x * s, v[j].y * s, v[j].z * s, v[j].w * s};
-            const uint32_t h01 = f32x2_to_bf16x2(f[0], f[1]), h23 = f32x2_to_bf16x2(f[2], f[3]);
-            const float2 r01 = bf16x2_to_f32x2(h01), r23 = bf16x2_to_f32x2(h23);
-            *reinterpret_cast<uint2*>(hi + row * kStride + col) = make_uint2(h01, h23);
-            *reinterpret_cast<uint2*>(lo + row * kStride + col) =
-                make_uint2(f32x2_to_bf16x2(f[0] - r01.x, f[1] - r01.y), f32x2_to_bf16x2(f[2] - r23.x, f[3] - r23.y));
+            if (e < items) split_h(v[j], s, hi + row * kStride + col, lo + row * kStride + col);
         }
     }
 }
@@ -606,9 +644,9 @@ __device__ __forceinline__ void add_row(const uint16_t* base, uint16_t* y, const
 // A unit is a chunk and 256 rows of one projection, 32 a warp.  Bound by the bytes of y (many tokens) or of B (few), so
 // what a warp needs is on its way before anything is multiplied: B's rows and the base of up to 64 tokens, or those of
 // D units with few tokens.
-template <int W, int D>
-__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, int blocks, bool copy) {
-    constexpr int kCols = W ? W * 32 : 16, kStride = kCols + 8;
+template <int W, int D, bool EXACT>
+__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_constant__ LoraArgs a, int blocks, bool copy) {
+    constexpr int kCols = Weights<W>::kCols, kStride = kCols + 8;
     __shared__ __align__(16) uint16_t hi[kChunk * kStride], lo[kChunk * kStride];
     __shared__ int32_t rows[kChunk];
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4, warp_row = threadIdx.x / 32 * 32;
@@ -617,10 +655,10 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
     Plan p;
     if (!read_plan(a, &p)) return;
     const Cut cut = cut_of(a, p);
-    const int R = a.count * a.rank;
+    const int rank = EXACT ? kCols : a.rank, R = a.count * rank;
     auto stage = [&](const int4& chunk, int i, int64_t row0, int n_slices, int rows_each) {
         __syncthreads();
-        stage_h<kCols, kStride>(a.h + row0 * R + i * a.rank, R, a.rank, chunk.z, n_slices, rows_each * R, a.scales[chunk.x],
+        stage_h<kCols, kStride>(a.h + row0 * R + i * rank, R, rank, chunk.z, n_slices, rows_each * R, a.scales[chunk.x],
                                 hi, lo);
         if (threadIdx.x < kChunk)
             rows[threadIdx.x] =
@@ -629,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
     };
     // this lane's first row of B in a block, behind `first`
     auto rows_of_b = [&](int i, int adapter, int first_row) {
-        return a.b[i] + (static_cast<int64_t>(adapter) * a.N[i] + first_row) * a.rank + Weights<W>::kLane * t;
+        return a.b[i] + (static_cast<int64_t>(adapter) * a.N[i] + first_row) * rank + Weights<W>::kLane * t;
     };
     {
         const int64_t units = static_cast<int64_t>(p.n_many) * blocks;
@@ -652,7 +690,11 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
             const uint16_t* base = a.base[i] + n;
             uint16_t* y = a.y[i] + n;
             Weights<W> w;
-            w.load(rows_of_b(i, chunk.x, first_row), 0, N - 1 - first_row, a.rank, t);
+            const uint16_t* b = rows_of_b(i, chunk.x, first_row);
+            if (EXACT && block.first + 256 <= N)
+                w.load_whole(b, 0);
+            else
+                w.load(b, 0, N - 1 - first_row, rank, t);
             constexpr int kTiles = W >= 2 ? 2 : 4;  // tiles of 16 tokens whose base is on its way
 #pragma unroll 1
             for (int r0 = g; r0 - g < chunk.z; r0 += 16 * kTiles) {
@@ -721,45 +763,60 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
         }
         const int4 chunk = p.chunks[p.n_many + c];
         if (!chunk_ok(a, p, chunk, kFew)) continue;
-        if (held != c * a.count + i) {
-            held = c * a.count + i;
-            stage(chunk, i, cut.few_row(p.n_many, c, 0), cut.few_slices, kFew);
-        }
         batch = min(D, left);
         const int first_row = n0 + 8 * (g / 2) + g % 2;
         const uint16_t* b = rows_of_b(i, chunk.x, first_row);
-        const int64_t at[2] = {static_cast<int64_t>(rows[g]) * N, static_cast<int64_t>(rows[g + 8]) * N};
         const bool real[2] = {g < chunk.z, g + 8 < chunk.z}, both = chunk.z > 8;
+        const bool whole = EXACT && vec && block.first + 256 * D <= N && left >= D;
+        int64_t at[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+            if (real[h]) at[h] = token_at(a, p, chunk.y + 8 * h + g) * N;
         Weights<W> w[D];
         uint4 in[D][2];
+        if (whole) {
 #pragma unroll
-        for (int d = 0; d < D; d++) {
-            if (d >= batch) continue;
-            w[d].load(b, 256 * d, N - 1 - first_row, a.rank, t);
+            for (int d = 0; d < D; d++) w[d].load_whole(b, 256 * d);
 #pragma unroll
             for (int h = 0; h < 2; h++)
-                if (vec && real[h] && n + 256 * d < N) in[d][h] = *reinterpret_cast<const uint4*>(base + at[h] + 256 * d);
+                if (real[h])
+#pragma unroll
+                    for (int d = 0; d < D; d++) in[d][h] = *reinterpret_cast<const uint4*>(base + at[h] + 256 * d);
+        } else {
+#pragma unroll
+            for (int d = 0; d < D; d++) {
+                if (d >= batch) continue;
+                w[d].load(b, 256 * d, N - 1 - first_row, rank, t);
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    if (vec && real[h] && n + 256 * d < N)
+                        in[d][h] = *reinterpret_cast<const uint4*>(base + at[h] + 256 * d);
+            }
+        }
+        if (held != c * a.count + i) {
+            held = c * a.count + i;
+            stage(chunk, i, cut.few_row(p.n_many, c, 0), cut.few_slices, kFew);
         }
 #pragma unroll
         for (int d = 0; d < D; d++) {
             if (d >= batch) continue;
             float acc[4][4];
             w[d].multiply(acc, hi, lo, g, kStride, t);
-            const int64_t more = 256 * d;
             if (n + 256 * d >= N) continue;
+            const int64_t more = 256 * d;
             if (real[0]) add_row(base + at[0] + more, y + at[0] + more, in[d][0], acc, 0, vec, n + 256 * d, N);
             if (both && real[1]) add_row(base + at[1] + more, y + at[1] + more, in[d][1], acc, 1, vec, n + 256 * d, N);
         }
     }
 }
 
-template <int W, int D>
+template <int W, int D, bool EXACT>
 cudaError_t expand(const LoraArgs& a, int blocks, bool copy, int64_t most, int num_sms, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     const int64_t cap = static_cast<int64_t>(num_sms) * 2;
     const cudaLaunchConfig_t cfg =
         pdl_config(dim3(static_cast<unsigned>(most < cap ? most : cap)), kThreads, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, expand_kernel<W, D>, a, blocks, copy);
+    return cudaLaunchKernelEx(&cfg, expand_kernel<W, D, EXACT>, a, blocks, copy);
 }
 
 }  // namespace
@@ -825,10 +882,15 @@ cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
     }
     const int64_t most = (chunks + (copy ? (a.T + kChunk - 1) / kChunk : 0)) * blocks;
     if (most == 0) return cudaSuccess;  // no adapters, and in place
-    if (a.rank <= 16) return expand<0, 3>(a, blocks, copy, most, num_sms, stream);
-    if (a.rank <= 32) return expand<1, 2>(a, blocks, copy, most, num_sms, stream);
-    if (a.rank <= 64) return expand<2, 1>(a, blocks, copy, most, num_sms, stream);
-    return expand<4, 1>(a, blocks, copy, most, num_sms, stream);
+    // (ranks of exactly 16, 32, 64 and 128 have constants for addresses)
+#define NF4_EXPAND(W, D)                                                                                       \
+    return a.rank == Weights<W>::kCols ? expand<W, D, true>(a, blocks, copy, most, num_sms, stream)            \
+                                       : expand<W, D, false>(a, blocks, copy, most, num_sms, stream)
+    if (a.rank <= 16) NF4_EXPAND(0, 3);
+    if (a.rank <= 32) NF4_EXPAND(1, 2);
+    if (a.rank <= 64) NF4_EXPAND(2, 1);
+    NF4_EXPAND(4, 1);
+#undef NF4_EXPAND
 }
 
 cudaError_t read_and_clear_lora_error(int* code) {
