@@ -21,7 +21,7 @@ constexpr int kChunk = 64;      // tokens of a chunk at most
 constexpr int kFew = 16;        // of a chunk of few
 constexpr int kHeader = 8;      // int32 before the chunks: T, adapters, chunks of many, of few, tokens with an adapter
 constexpr int kThreads = 256;
-constexpr int kUnits = 608;     // of the first product at most, in two rounds of two CTAs for each of 152 SMs
+constexpr int kUnits = 304;     // of the first product: two CTAs for each of 152 SMs
 constexpr int kMaxSlices = 32;
 
 __device__ int g_lora_error;  // 46: an adapter or a row outside its list; 47: a plan of other sizes
@@ -231,8 +231,8 @@ constexpr int kFewTiles = 4;    // rank columns of a unit with few tokens, in ei
 constexpr int kManyTiles = 16;  // and with many
 
 // How the first product is cut: rank-column groups, slices of K (in units of 64), and the rows of the workspace that a
-// chunk's slice takes (64 or 16, the chunks of many first).  Slices fill the GPU: with many tokens in one round; with
-// few in two if a warp still has three steps of 32 in each slice, or, if that leaves SMs empty, one step.
+// chunk's slice takes (64 or 16, the chunks of many first).  As many slices as fill the GPU in one round, each with at
+// least one step of 32 for every warp; but eight at most with many tokens, whose sums the second product waits for.
 struct Cut {
     int many_groups, few_groups, many_slices, few_slices;
     __device__ __forceinline__ int64_t many_row(int chunk, int slice) const {
@@ -248,8 +248,8 @@ __device__ __forceinline__ Cut cut_of(const LoraArgs& a, const Plan& p) {
     c.many_groups = (tiles + kManyTiles - 1) / kManyTiles;
     c.few_groups = (tiles + kFewTiles - 1) / kFewTiles;
     const int many = max(1, p.n_many * c.many_groups), few = max(1, p.n_few * c.few_groups);
-    c.many_slices = max(1, min(most, kUnits / 2 / many));
-    c.few_slices = max(1, min(most, max(min(kUnits / few, K / 768), kUnits / 4 / few)));
+    c.many_slices = max(1, min(min(most, 8), kUnits / many));
+    c.few_slices = max(1, min(most, kUnits / few));
     return c;
 }
 
@@ -276,28 +276,27 @@ __device__ __forceinline__ const uint16_t* column_of(const LoraArgs& a, int adap
     return a.a[i] + (static_cast<int64_t>(adapter) * a.rank + (tile - i * per) * 8 + row) * a.K;
 }
 
-// A unit with few tokens: bound by the latency of reading A, so U steps of a warp are on their way at once, and the
-// operands go straight to registers.  MT tiles of 16 tokens, up to NT * 8 columns.
-template <int MT, int NT, int U>
+// A unit with few tokens, up to ROWS (8 or 16), and up to NT * 8 columns: bound by the latency of reading A, so U steps of
+// a warp are on their way at once, and the operands go straight to registers.
+template <int ROWS, int NT, int U>
 __device__ __forceinline__ void shrink_few(const LoraArgs& a, const Plan& p, const int4& chunk, int slice, int n_slices,
                                            int tile0, int64_t row0, float* sums) {
     constexpr int kStride = NT * 8 + 4;  // (a warp's 64-bit stores: 8 rows, 4 columns apart)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int tiles = min(NT, a.count * a.rank / 8 - tile0);
-    const uint16_t* xp[MT][2];
+    constexpr int H = ROWS / 8;
+    const uint16_t* xp[H];
 #pragma unroll
-    for (int m = 0; m < MT; m++)
-#pragma unroll
-        for (int h = 0; h < 2; h++)  // a row past the chunk's end repeats the last
-            xp[m][h] = a.x + token_at(a, p, chunk.y + min(m * 16 + h * 8 + g, chunk.z - 1)) * a.K + 8 * t;
+    for (int h = 0; h < H; h++)  // a row past the chunk's end repeats the last
+        xp[h] = a.x + token_at(a, p, chunk.y + min(h * 8 + g, chunk.z - 1)) * a.K + 8 * t;
     const uint16_t* wp[NT];
 #pragma unroll
     for (int j = 0; j < NT; j++) wp[j] = column_of(a, chunk.x, tile0 + min(j, tiles - 1), g) + 8 * t;
-    float acc[MT][NT][4] = {};
+    float acc[NT][4] = {};
     const int64_t steps = a.K / 64, k0 = 2 * (steps * slice / n_slices), k1 = 2 * (steps * (slice + 1) / n_slices);
     constexpr int kWarps = kThreads / 32;
     for (int64_t k = k0 + warp; k < k1; k += kWarps * U) {
-        uint4 x[U][MT][2], w[U][NT];
+        uint4 x[U][2], w[U][NT];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const bool in = k + u * kWarps < k1;
@@ -308,44 +307,38 @@ __device__ __forceinline__ void shrink_few(const LoraArgs& a, const Plan& p, con
                 if (in && j < tiles) w[u][j] = __ldg(reinterpret_cast<const uint4*>(wp[j] + at));
             }
 #pragma unroll
-            for (int m = 0; m < MT; m++)
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    x[u][m][h] = make_uint4(0, 0, 0, 0);
-                    if (in) x[u][m][h] = *reinterpret_cast<const uint4*>(xp[m][h] + at);
-                }
+            for (int h = 0; h < 2; h++) {
+                x[u][h] = make_uint4(0, 0, 0, 0);
+                if (in && h < H) x[u][h] = *reinterpret_cast<const uint4*>(xp[h % H] + at);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
             for (int j = 0; j < NT; j++)
-                if (j < tiles)
-#pragma unroll
-                    for (int m = 0; m < MT; m++) mma_k32(acc[m][j], x[u][m][0], x[u][m][1], w[u][j]);
+                if (j < tiles) mma_k32(acc[j], x[u][0], x[u][1], w[u][j]);
     }
     // four of the warps write, the others add, then all add the four
-    float* own = sums + (warp % 4) * (MT * 16 * kStride);
+    float* own = sums + (warp % 4) * (ROWS * kStride);
     __syncthreads();  // the last unit's sums are read
 #pragma unroll
     for (int round = 0; round < 2; round++) {
         if (warp / 4 == round)
 #pragma unroll
-            for (int m = 0; m < MT; m++)
+            for (int j = 0; j < NT; j++)
 #pragma unroll
-                for (int j = 0; j < NT; j++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        float2* at = reinterpret_cast<float2*>(own + (m * 16 + h * 8 + g) * kStride + j * 8 + 2 * t);
-                        float2 v = make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
-                        if (round) {
-                            const float2 o = *at;
-                            v.x += o.x, v.y += o.y;
-                        }
-                        *at = v;
+                for (int h = 0; h < H; h++) {
+                    float2* at = reinterpret_cast<float2*>(own + (h * 8 + g) * kStride + j * 8 + 2 * t);
+                    float2 v = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+                    if (round) {
+                        const float2 o = *at;
+                        v.x += o.x, v.y += o.y;
                     }
+                    *at = v;
+                }
         __syncthreads();
     }
-    write_sums(a, row0, chunk.z, tile0, tiles, sums, 4, kStride, MT * 16 * kStride);
+    write_sums(a, row0, chunk.z, tile0, tiles, sums, 4, kStride, ROWS * kStride);
 }
 
 // A unit with many tokens, up to 64 by 128 columns: bound by the bytes of x, so x is read once for all columns.  Stages
@@ -459,9 +452,13 @@ __global__ void __launch_bounds__(kThreads, 2) shrink_kernel(const __grid_consta
             const int v = static_cast<int>(u - many), group = v % cut.few_groups, rest = v / cut.few_groups;
             const int slice = rest % cut.few_slices, c = rest / cut.few_slices;
             const int4 chunk = p.chunks[p.n_many + c];
-            if (chunk_ok(a, p, chunk, kFew))
-                shrink_few<1, kFewTiles, 3>(a, p, chunk, slice, cut.few_slices, group * kFewTiles,
-                                            cut.few_row(p.n_many, c, slice), reinterpret_cast<float*>(ring));
+            if (!chunk_ok(a, p, chunk, kFew)) continue;
+            float* sums = reinterpret_cast<float*>(ring);
+            const int64_t row0 = cut.few_row(p.n_many, c, slice);
+            if (chunk.z <= 8)
+                shrink_few<8, kFewTiles, 4>(a, p, chunk, slice, cut.few_slices, group * kFewTiles, row0, sums);
+            else
+                shrink_few<16, kFewTiles, 3>(a, p, chunk, slice, cut.few_slices, group * kFewTiles, row0, sums);
         }
     }
 }
@@ -568,53 +565,43 @@ __device__ __forceinline__ void split_h(const float4& v, float s, uint16_t* hi, 
 }
 
 // h of a chunk for one projection: its slices from `h` on, `step` floats apart, summed in order, times s, as the sum of
-// two bf16 numbers (2^-16 of it), rows of kStride; zeros up to whole tiles.
+// two bf16 numbers (2^-16 of it), rows of kStride; zeros up to whole tiles.  A thread takes four columns of a row, ITEMS
+// such and AHEAD slices at a time.
 // (The thread's number is hidden from the compiler: it would work the places out ahead of the loop that stages now and
 // then, and keep them in registers that the loop needs.)
-template <int kCols, int kStride>
+template <int kCols, int kStride, int ITEMS, int AHEAD>
 __device__ __forceinline__ void stage_h(const float* h, int R, int rank, int tokens, int n_slices, int step, float s,
                                         uint16_t* hi, uint16_t* lo) {
-    // four columns of a row each, up to four such at a time
     const int items = (tokens + 15) / 16 * 16 * (kCols / 4);
     int thread = threadIdx.x;
     asm volatile("" : "+r"(thread));
-    for (int e0 = thread; e0 < items; e0 += 4 * kThreads) {
-        float4 v[4];
-        int at[4];
-        if (items <= kThreads) {  // one item a thread: four slices at a time
-            const int row = e0 / (kCols / 4), col = e0 % (kCols / 4) * 4;
-            const float* from = h + row * R + col;
-            v[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (row < tokens && col < rank)
-                for (int q0 = 0; q0 < n_slices; q0 += 4) {
-                    float4 o[4];
+    for (int e0 = thread; e0 < items; e0 += ITEMS * kThreads) {
+        float4 v[ITEMS];
+        int at[ITEMS];
 #pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        if (q0 + q < n_slices) o[q] = *reinterpret_cast<const float4*>(from + (q0 + q) * step);
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        if (q0 + q < n_slices)
-                            v[0].x += o[q].x, v[0].y += o[q].y, v[0].z += o[q].z, v[0].w += o[q].w;
-                }
-            split_h(v[0], s, hi + row * kStride + col, lo + row * kStride + col);
-            break;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < ITEMS; j++) {
             const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
             v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             at[j] = row < tokens && col < rank ? row * R + col : -1;
         }
-#pragma unroll 2
-        for (int q = 0; q < n_slices; q++)
+#pragma unroll 1
+        for (int q0 = 0; q0 < n_slices; q0 += AHEAD) {
+            float4 o[ITEMS][AHEAD];
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (at[j] >= 0) {
-                    const float4 o = *reinterpret_cast<const float4*>(h + q * step + at[j]);
-                    v[j].x += o.x, v[j].y += o.y, v[j].z += o.z, v[j].w += o.w;
-                }
+            for (int q = 0; q < AHEAD; q++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+                for (int j = 0; j < ITEMS; j++)
+                    if (at[j] >= 0 && q0 + q < n_slices)
+                        o[j][q] = *reinterpret_cast<const float4*>(h + (q0 + q) * step + at[j]);
+#pragma unroll
+            for (int q = 0; q < AHEAD; q++)
+#pragma unroll
+                for (int j = 0; j < ITEMS; j++)
+                    if (at[j] >= 0 && q0 + q < n_slices)
+                        v[j].x += o[j][q].x, v[j].y += o[j][q].y, v[j].z += o[j][q].z, v[j].w += o[j][q].w;
+        }
+#pragma unroll
+        for (int j = 0; j < ITEMS; j++) {
             const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
             if (e < items) split_h(v[j], s, hi + row * kStride + col, lo + row * kStride + col);
         }
@@ -641,89 +628,116 @@ __device__ __forceinline__ void add_row(const uint16_t* base, uint16_t* y, const
     }
 }
 
-// A unit is a chunk and 256 rows of one projection, 32 a warp.  Bound by the bytes of y (many tokens) or of B (few), so
-// what a warp needs is on its way before anything is multiplied: B's rows and the base of up to 64 tokens, or those of
-// D units with few tokens.
-template <int W, int D, bool EXACT>
-__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_constant__ LoraArgs a, int blocks, bool copy) {
+// A unit is a chunk and 256 rows of one projection, 32 a warp.  Units u0 .. u1 of the chunks of many: bound by the bytes
+// of y, so the base of 32 or 64 tokens is on its way before anything is multiplied.
+template <int W, bool EXACT>
+__device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, const Cut& cut, int blocks, int64_t u0,
+                                            int64_t u1, uint16_t* hi, uint16_t* lo, int32_t* rows) {
     constexpr int kCols = Weights<W>::kCols, kStride = kCols + 8;
-    __shared__ __align__(16) uint16_t hi[kChunk * kStride], lo[kChunk * kStride];
-    __shared__ int32_t rows[kChunk];
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4, warp_row = threadIdx.x / 32 * 32;
-    pdl_launch_dependents();
-    pdl_wait();
-    Plan p;
-    if (!read_plan(a, &p)) return;
-    const Cut cut = cut_of(a, p);
     const int rank = EXACT ? kCols : a.rank, R = a.count * rank;
-    auto stage = [&](const int4& chunk, int i, int64_t row0, int n_slices, int rows_each) {
-        __syncthreads();
-        stage_h<kCols, kStride>(a.h + row0 * R + i * rank, R, rank, chunk.z, n_slices, rows_each * R, a.scales[chunk.x],
-                                hi, lo);
-        if (threadIdx.x < kChunk)
-            rows[threadIdx.x] =
-                static_cast<int32_t>(token_at(a, p, chunk.y + min(static_cast<int>(threadIdx.x), chunk.z - 1)));
-        __syncthreads();
-    };
-    // this lane's first row of B in a block, behind `first`
-    auto rows_of_b = [&](int i, int adapter, int first_row) {
-        return a.b[i] + (static_cast<int64_t>(adapter) * a.N[i] + first_row) * rank + Weights<W>::kLane * t;
-    };
-    {
-        const int64_t units = static_cast<int64_t>(p.n_many) * blocks;
-        const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-        int held = -1, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+    int held = -1, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
 #pragma unroll 1
-        for (int64_t u = u0; u < u1; u++, at_block++) {
-            if (at_block == blocks) at_block = 0, c++;
-            const Block block = block_of(a, at_block);
-            const int i = block.i, N = static_cast<int>(a.N[i]), n0 = block.first + warp_row, n = n0 + 8 * t;
-            const int4 chunk = p.chunks[c];
-            if (!chunk_ok(a, p, chunk, kChunk)) continue;
-            if (held != c * a.count + i) {
-                held = c * a.count + i;
-                stage(chunk, i, cut.many_row(c, 0), cut.many_slices, kChunk);
-            }
-            if (n0 >= N) continue;
-            const bool vec = N % 8 == 0, in_row = n < N;
-            const int first_row = n0 + 8 * (g / 2) + g % 2;
-            const uint16_t* base = a.base[i] + n;
-            uint16_t* y = a.y[i] + n;
-            Weights<W> w;
-            const uint16_t* b = rows_of_b(i, chunk.x, first_row);
-            if (EXACT && block.first + 256 <= N)
-                w.load_whole(b, 0);
-            else
-                w.load(b, 0, N - 1 - first_row, rank, t);
-            constexpr int kTiles = W >= 2 ? 2 : 4;  // tiles of 16 tokens whose base is on its way
+    for (int64_t u = u0; u < u1; u++, at_block++) {
+        if (at_block == blocks) at_block = 0, c++;
+        const Block block = block_of(a, at_block);
+        const int i = block.i, N = static_cast<int>(a.N[i]), n0 = block.first + warp_row, n = n0 + 8 * t;
+        const int4 chunk = p.chunks[c];
+        if (!chunk_ok(a, p, chunk, kChunk)) continue;
+        if (held != c * a.count + i) {
+            held = c * a.count + i;
+            __syncthreads();
+            stage_h<kCols, kStride, 2, 2>(a.h + cut.many_row(c, 0) * R + i * rank, R, rank, chunk.z, cut.many_slices, kChunk * R,
+                                    a.scales[chunk.x], hi, lo);
+            if (threadIdx.x < kChunk)
+                rows[threadIdx.x] =
+                    static_cast<int32_t>(token_at(a, p, chunk.y + min(static_cast<int>(threadIdx.x), chunk.z - 1)));
+            __syncthreads();
+        }
+        if (n0 >= N) continue;
+        const bool vec = N % 8 == 0, in_row = n < N;
+        const int first_row = n0 + 8 * (g / 2) + g % 2;
+        const uint16_t* base = a.base[i] + n;
+        uint16_t* y = a.y[i] + n;
+        const uint16_t* b = a.b[i] + (static_cast<int64_t>(chunk.x) * N + first_row) * rank + Weights<W>::kLane * t;
+        Weights<W> w;
+        if (EXACT && block.first + 256 <= N)
+            w.load_whole(b, 0);
+        else
+            w.load(b, 0, N - 1 - first_row, rank, t);
+        constexpr int kTiles = W >= 2 ? 2 : 4;  // tiles of 16 tokens whose base is on its way
 #pragma unroll 1
-            for (int r0 = g; r0 - g < chunk.z; r0 += 16 * kTiles) {
-                uint4 in[2 * kTiles];
+        for (int r0 = g; r0 - g < chunk.z; r0 += 16 * kTiles) {
+            uint4 in[2 * kTiles];
 #pragma unroll
-                for (int m = 0; m < 2 * kTiles; m++)
-                    if (vec && in_row && r0 + 8 * m < chunk.z)
-                        in[m] = *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(rows[r0 + 8 * m]) * N);
+            for (int m = 0; m < 2 * kTiles; m++)
+                if (vec && in_row && r0 + 8 * m < chunk.z)
+                    in[m] = *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(rows[r0 + 8 * m]) * N);
 #pragma unroll
-                for (int m = 0; m < 2 * kTiles; m += 2) {
-                    if (r0 - g + 8 * m >= chunk.z) continue;
-                    float acc[4][4];
-                    w.multiply(acc, hi, lo, r0 + 8 * m, kStride, t);
+            for (int m = 0; m < 2 * kTiles; m += 2) {
+                if (r0 - g + 8 * m >= chunk.z) continue;
+                float acc[4][4];
+                w.multiply(acc, hi, lo, r0 + 8 * m, kStride, t);
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const int r = r0 + 8 * (m + h);
-                        if (r >= chunk.z || !in_row) continue;
-                        const int64_t at = static_cast<int64_t>(rows[r]) * N;
-                        add_row(base + at, y + at, in[m + h], acc, h, vec, n, N);
-                    }
+                for (int h = 0; h < 2; h++) {
+                    const int r = r0 + 8 * (m + h);
+                    if (r >= chunk.z || !in_row) continue;
+                    const int64_t at = static_cast<int64_t>(rows[r]) * N;
+                    add_row(base + at, y + at, in[m + h], acc, h, vec, n, N);
                 }
             }
         }
     }
-    // rows without an adapter are copied where the output is not the base itself
-    const int idle = copy ? static_cast<int>((a.T - p.n_tokens + kChunk - 1) / kChunk) : 0;
-    const int64_t units = static_cast<int64_t>(p.n_few + idle) * blocks;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    int held = -1, batch = 0, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+}
+
+// Rows without an adapter, where the output is not the base itself: copied, 64 tokens and 256 columns a unit.
+// A warp's eight loads, of eight rows each, may be of several units.
+__device__ __forceinline__ void copy_idle(const LoraArgs& a, const Plan& p, int blocks, int64_t u0, int64_t u1) {
+    const int lane = threadIdx.x % 32, g = lane / 4, warp_row = threadIdx.x / 32 * 32;
+    int batch = 0;
+#pragma unroll 1
+    for (int64_t u = u0; u < u1; u += batch) {
+        const Block block = block_of(a, static_cast<int>(u % blocks));
+        const int first = p.n_tokens + static_cast<int>(u / blocks) * kChunk;
+        const int tokens = min(kChunk, static_cast<int>(a.T) - first), rounds = (tokens + 7) / 8;
+        const int N = static_cast<int>(a.N[block.i]), n0 = block.first + warp_row, n = n0 + 8 * (lane % 4);
+        batch = min(8 / rounds, static_cast<int>(min(static_cast<int64_t>(block.left), u1 - u)));
+        const uint16_t* base = a.base[block.i];
+        uint16_t* y = a.y[block.i];
+        if (base == y) continue;
+        if (N % 8 == 0) {
+            uint4 v[8];
+            int64_t at[8];
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+                const int r = q % rounds * 8 + g, col = n + q / rounds * 256;
+                at[q] = q < batch * rounds && r < tokens && col < N ? token_at(a, p, first + r) * N + col : -1;
+                if (at[q] >= 0) v[q] = *reinterpret_cast<const uint4*>(base + at[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 8; q++)
+                if (at[q] >= 0) *reinterpret_cast<uint4*>(y + at[q]) = v[q];
+        } else {
+            for (int r = 0; r < tokens; r++)
+                for (int col = n0 + lane; col < N && col < n0 + batch * 256; col += 256) {
+                    const int64_t at = token_at(a, p, first + r) * N + col;
+                    y[at] = base[at];
+                }
+        }
+    }
+}
+
+// Units u0 .. u1 of the chunks of few: bound by the bytes of B, so the rows and the base of D units are on their way at
+// once.
+template <int W, int D, bool EXACT>
+__device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, const Cut& cut, int blocks, int64_t u0,
+                                           int64_t u1, uint16_t* hi, uint16_t* lo) {
+    constexpr int kCols = Weights<W>::kCols, kStride = kCols + 8;
+    const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4, warp_row = threadIdx.x / 32 * 32;
+    const int rank = EXACT ? kCols : a.rank, R = a.count * rank;
+    int held = -1, held_chunk = -1, batch = 0, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
+    int4 chunk = make_int4(0, 0, 0, 0);
+    int32_t token[2] = {0, 0};  // of rows g and g + 8
 #pragma unroll 1
     for (int64_t u = u0; u < u1; u += batch, at_block += batch) {
         if (at_block >= blocks) at_block -= blocks, c++;  // (a batch ends with its projection)
@@ -733,48 +747,36 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
         const bool vec = N % 8 == 0;
         const uint16_t* base = a.base[i] + n;
         uint16_t* y = a.y[i] + n;
-        batch = 1;
-        if (c >= p.n_few) {
-            if (base == y) continue;
-            const int first = p.n_tokens + (c - p.n_few) * kChunk, tokens = min(kChunk, static_cast<int>(a.T) - first);
-            const int rounds = (tokens + 7) / 8;  // of eight rows a warp
-            batch = min(8 / rounds, left);
-            if (vec) {
-                uint4 v[8];
-                int64_t at[8];
+        if (held_chunk != c) {
+            held_chunk = c;
+            chunk = p.chunks[p.n_many + c];
+            if (!chunk_ok(a, p, chunk, kFew)) chunk.z = 0;
 #pragma unroll
-                for (int q = 0; q < 8; q++) {
-                    const int r = q % rounds * 8 + g, more = q / rounds * 256;
-                    at[q] = q < batch * rounds && r < tokens && n + more < N ? token_at(a, p, first + r) * N + more : -1;
-                    if (at[q] >= 0) v[q] = *reinterpret_cast<const uint4*>(base + at[q]);
-                }
-#pragma unroll
-                for (int q = 0; q < 8; q++)
-                    if (at[q] >= 0) *reinterpret_cast<uint4*>(y + at[q]) = v[q];
-            } else {
-                for (int q = 0; q < batch; q++)
-                    for (int r = 0; r < tokens; r++) {
-                        const int col = n0 + q * 256 + lane;
-                        const int64_t at = token_at(a, p, first + r) * N + col;
-                        if (col < N) a.y[i][at] = a.base[i][at];
-                    }
-            }
-            continue;
+            for (int h = 0; h < 2; h++)
+                if (8 * h + g < chunk.z) token[h] = static_cast<int32_t>(token_at(a, p, chunk.y + 8 * h + g));
         }
-        const int4 chunk = p.chunks[p.n_many + c];
-        if (!chunk_ok(a, p, chunk, kFew)) continue;
         batch = min(D, left);
-        const int first_row = n0 + 8 * (g / 2) + g % 2;
-        const uint16_t* b = rows_of_b(i, chunk.x, first_row);
-        const bool real[2] = {g < chunk.z, g + 8 < chunk.z}, both = chunk.z > 8;
-        const bool whole = EXACT && vec && block.first + 256 * D <= N && left >= D;
-        int64_t at[2] = {0, 0};
+        if (chunk.z == 0) continue;
+        const int first_row = n0 + 8 * (g / 2) + g % 2, last_row = N - 1 - first_row;
+        const uint16_t* b = a.b[i] + (static_cast<int64_t>(chunk.x) * N + first_row) * rank + Weights<W>::kLane * t;
+        if (held != c * a.count + i) {
+            held = c * a.count + i;
+            // B starts on its way to L2 meanwhile
 #pragma unroll
-        for (int h = 0; h < 2; h++)
-            if (real[h]) at[h] = token_at(a, p, chunk.y + 8 * h + g) * N;
+            for (int j = 0; j < 4 * D; j++) {
+                const int row = min(j / 4 * 256 + j % 4 * 2, last_row);
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(b + static_cast<int64_t>(row) * rank));
+            }
+            __syncthreads();
+            stage_h<kCols, kStride, 1, 4>(a.h + cut.few_row(p.n_many, c, 0) * R + i * rank, R, rank, chunk.z, cut.few_slices,
+                                    kFew * R, a.scales[chunk.x], hi, lo);
+            __syncthreads();
+        }
+        const bool real[2] = {g < chunk.z, g + 8 < chunk.z}, both = chunk.z > 8;
+        const int64_t at[2] = {static_cast<int64_t>(token[0]) * N, static_cast<int64_t>(token[1]) * N};
         Weights<W> w[D];
         uint4 in[D][2];
-        if (whole) {
+        if (EXACT && vec && block.first + 256 * D <= N && left >= D) {
 #pragma unroll
             for (int d = 0; d < D; d++) w[d].load_whole(b, 256 * d);
 #pragma unroll
@@ -786,16 +788,12 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
 #pragma unroll
             for (int d = 0; d < D; d++) {
                 if (d >= batch) continue;
-                w[d].load(b, 256 * d, N - 1 - first_row, rank, t);
+                w[d].load(b, 256 * d, last_row, rank, t);
 #pragma unroll
                 for (int h = 0; h < 2; h++)
                     if (vec && real[h] && n + 256 * d < N)
                         in[d][h] = *reinterpret_cast<const uint4*>(base + at[h] + 256 * d);
             }
-        }
-        if (held != c * a.count + i) {
-            held = c * a.count + i;
-            stage(chunk, i, cut.few_row(p.n_many, c, 0), cut.few_slices, kFew);
         }
 #pragma unroll
         for (int d = 0; d < D; d++) {
@@ -810,12 +808,51 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const __grid_consta
     }
 }
 
+// The units of all kinds on one line, each as long as it weighs (what it moves, roughly), cut into equal parts for the
+// CTAs: a unit belongs to the one in whose part it begins.
 template <int W, int D, bool EXACT>
-cudaError_t expand(const LoraArgs& a, int blocks, bool copy, int64_t most, int num_sms, cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, int blocks, bool copy) {
+    constexpr int kStride = Weights<W>::kCols + 8;
+    __shared__ __align__(16) uint16_t hi[kChunk * kStride], lo[kChunk * kStride];
+    __shared__ int32_t rows[kChunk];
+    pdl_launch_dependents();
+    pdl_wait();
+    Plan p;
+    if (!read_plan(a, &p)) return;
+    const Cut cut = cut_of(a, p);
+    constexpr int kMany = 4, kFewWeight = W >= 2 ? 2 : 1;
+    const int64_t idle = copy ? (a.T - p.n_tokens + kChunk - 1) / kChunk * blocks : 0;
+    const int idle_weight = a.T - p.n_tokens >= kChunk ? kMany : 1;
+    const int64_t to_few = static_cast<int64_t>(p.n_many) * blocks * kMany;
+    const int64_t to_idle = to_few + static_cast<int64_t>(p.n_few) * blocks * kFewWeight;
+    const int64_t end = to_idle + idle * idle_weight;
+    const int64_t from = end * blockIdx.x / gridDim.x, to = end * (blockIdx.x + 1) / gridDim.x;
+    // the first unit, of those of `weight` from `first` up to `last`, that begins at `at` or later
+    auto unit = [](int64_t at, int64_t first, int64_t last, int weight) {
+        return (max(min(at, last), first) - first + weight - 1) / weight;
+    };
+    if (from < to_few)
+        expand_many<W, EXACT>(a, p, cut, blocks, unit(from, 0, to_few, kMany), unit(to, 0, to_few, kMany), hi, lo, rows);
+    if (from < to_idle && to > to_few)
+        expand_few<W, D, EXACT>(a, p, cut, blocks, unit(from, to_few, to_idle, kFewWeight),
+                                unit(to, to_few, to_idle, kFewWeight), hi, lo);
+    if (to > to_idle) copy_idle(a, p, blocks, unit(from, to_idle, end, idle_weight), unit(to, to_idle, end, idle_weight));
+}
+
+template <int W, int D, bool EXACT>
+cudaError_t expand(const LoraArgs& a, int num_sms, cudaStream_t stream) {
+    int blocks = 0;
+    bool copy = false;
+    for (int i = 0; i < a.count; i++) {
+        blocks += static_cast<int>((a.N[i] + 255) / 256);
+        copy |= a.base[i] != a.y[i];
+    }
     cudaLaunchAttribute attr;
     const int64_t cap = static_cast<int64_t>(num_sms) * 2;
+    const int64_t units = (max_chunks(a.T, a.adapters) + (copy ? (a.T + kChunk - 1) / kChunk : 0)) * blocks;
+    if (units == 0) return cudaSuccess;  // no adapters, and in place
     const cudaLaunchConfig_t cfg =
-        pdl_config(dim3(static_cast<unsigned>(most < cap ? most : cap)), kThreads, stream, &attr);
+        pdl_config(dim3(static_cast<unsigned>(units < cap ? units : cap)), kThreads, stream, &attr);
     return cudaLaunchKernelEx(&cfg, expand_kernel<W, D, EXACT>, a, blocks, copy);
 }
 
@@ -831,7 +868,7 @@ int64_t lora_workspace_bytes(int64_t T, int64_t adapters, int64_t rank, int64_t 
         const int64_t most = chunks > units ? chunks : units;
         return each * (chunks * kMaxSlices < most ? chunks * kMaxSlices : most);
     };
-    const int64_t rows = rows_of(max_many(T), kUnits / 2, kChunk) + rows_of(max_few(T, adapters), kUnits, kFew);
+    const int64_t rows = rows_of(max_many(T), kUnits, kChunk) + rows_of(max_few(T, adapters), kUnits, kFew);
     return rows * rank * count * static_cast<int64_t>(sizeof(float));
 }
 
@@ -857,12 +894,6 @@ cudaError_t launch_lora_plan(const int32_t* ids, const int32_t* sequences, int64
 cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     const int64_t chunks = max_chunks(a.T, a.adapters), cap = static_cast<int64_t>(num_sms) * 2;
-    int blocks = 0;
-    bool copy = false;
-    for (int i = 0; i < a.count; i++) {
-        blocks += static_cast<int>((a.N[i] + 255) / 256);
-        copy |= a.base[i] != a.y[i];
-    }
     const int64_t groups = (a.count * a.rank / 8 + kFewTiles - 1) / kFewTiles;
     const int64_t units = chunks * groups * kMaxSlices;
     if (units > 0) {
@@ -880,13 +911,10 @@ cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
         e = cudaLaunchKernelEx(&cfg, shrink_kernel, a);
         if (e != cudaSuccess) return e;
     }
-    const int64_t most = (chunks + (copy ? (a.T + kChunk - 1) / kChunk : 0)) * blocks;
-    if (most == 0) return cudaSuccess;  // no adapters, and in place
     // (ranks of exactly 16, 32, 64 and 128 have constants for addresses)
-#define NF4_EXPAND(W, D)                                                                                       \
-    return a.rank == Weights<W>::kCols ? expand<W, D, true>(a, blocks, copy, most, num_sms, stream)            \
-                                       : expand<W, D, false>(a, blocks, copy, most, num_sms, stream)
-    if (a.rank <= 16) NF4_EXPAND(0, 3);
+#define NF4_EXPAND(W, D) \
+    return a.rank == Weights<W>::kCols ? expand<W, D, true>(a, num_sms, stream) : expand<W, D, false>(a, num_sms, stream)
+    if (a.rank <= 16) NF4_EXPAND(0, 4);
     if (a.rank <= 32) NF4_EXPAND(1, 2);
     if (a.rank <= 64) NF4_EXPAND(2, 1);
     NF4_EXPAND(4, 1);
