@@ -767,45 +767,60 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const bool tie_counts = of_tie >= least;
     uint64_t above = 0, tied = 0;
     const float cut_at = logit_of(cut);
-    for (int v = r0; v < r1; v++) {
-        const P p(reinterpret_cast<const uint4*>(slice)[v]);
-        const float most = P::single(p.top());
-        if (most < cut_at) continue;
+    if (cut == kNothing && least == 1) {  // nothing is cut off
+        for (int v = r0; v < r1; v++) {
+            const P p(reinterpret_cast<const uint4*>(slice)[v]);
 #pragma unroll
-        for (int j = 0; j < VEC; j += 2) {
-            if (!(fmaxf(p[j], p[j + 1]) > cut_at)) continue;
-            uint64_t w[2];
-            weights_of(p[j], p[j + 1], row, sh.table, w);
-#pragma unroll
-            for (int i = 0; i < 2; i++) above += p[j + i] > cut_at && w[i] >= least ? w[i] : 0;
+            for (int j = 0; j < VEC; j += 2) {
+                uint64_t w[2];
+                weights_of(p[j], p[j + 1], row, sh.table, w);
+                above += w[0] + w[1];
+            }
         }
-        if (ties)
+    } else {
+        for (int v = r0; v < r1; v++) {
+            const P p(reinterpret_cast<const uint4*>(slice)[v]);
+            if (P::single(p.top()) < cut_at) continue;
 #pragma unroll
-            for (int j = 0; j < VEC; j++) tied += p[j] == cut_at;
+            for (int j = 0; j < VEC; j += 2) {
+                if (!(fmaxf(p[j], p[j + 1]) > cut_at)) continue;
+                uint64_t w[2];
+                weights_of(p[j], p[j + 1], row, sh.table, w);
+#pragma unroll
+                for (int i = 0; i < 2; i++) above += p[j + i] > cut_at && w[i] >= least ? w[i] : 0;
+            }
+            if (ties)
+#pragma unroll
+                for (int j = 0; j < VEC; j++) tied += p[j] == cut_at;
+        }
     }
-    const uint64_t scan_a = warp_scan(above, lane), scan_t = warp_scan(tied, lane);
+    const uint64_t scan_a = warp_scan(above, lane), scan_t = ties ? warp_scan(tied, lane) : 0;
     if (lane == 31) sh.part[warp][0] = scan_a, sh.part[warp][1] = scan_t;
+    if (tid == 0) sh.found[0] = kThreads;
     __syncthreads();
     uint64_t ahead = scan_a - above, tied_ahead = scan_t - tied, here = 0, tied_here = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; w++) {
-        if (w < warp) ahead += sh.part[w][0], tied_ahead += sh.part[w][1];
-        here += sh.part[w][0], tied_here += sh.part[w][1];
+        const uint64_t x = sh.part[w][0], y = sh.part[w][1];
+        if (w < warp) ahead += x, tied_ahead += y;
+        here += x, tied_here += y;
     }
     if (tid < ranks) {
         Shared* other = cluster.map_shared_rank(&sh, tid);
         other->sums[rank][0] = here;
         other->sums[rank][1] = tied_here;
     }
-    if (tid == 0) sh.found[0] = kThreads;
     cluster.sync();
     // of n tied elements behind `seen` others
     auto kept_of = [&](uint64_t n, uint64_t seen) { return tie_counts ? min(n, ties - min(ties, seen)) * of_tie : 0; };
-    uint64_t total = 0, seen = 0, before_slice = 0;
+    uint64_t total = 0, seen = 0, before_slice = 0, seen_before = 0;
     for (int r = 0; r < ranks; r++) {
-        if (r == rank) before_slice = total - kept_of(seen, 0), tied_ahead += seen;
-        total += sh.sums[r][0] + kept_of(sh.sums[r][1], seen);
+        if (r == rank) before_slice = total, seen_before = seen;
+        total += sh.sums[r][0];
         seen += sh.sums[r][1];
     }
+    total += kept_of(seen, 0);
+    tied_ahead += seen_before;
     // (all that lies before a run: what is above the cut there, and the first of its tied elements)
     const uint64_t goal = min(fraction_of(random, total, false), total - 1);
     ahead += before_slice + kept_of(tied_ahead, 0);
