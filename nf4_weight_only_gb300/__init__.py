@@ -148,7 +148,7 @@ def _load_calls(lib: ctypes.CDLL) -> None:
     functions = (lib.nf4_kv_append, lib.nf4_kv_read, lib.nf4_attention_decode, lib.nf4_rope, lib.nf4_rmsnorm,
                  lib.nf4_plan_step, lib.nf4_lora_plan, lib.nf4_lora, lib.nf4_sample)
     module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in functions), torch.bfloat16, torch.float8_e4m3fn,
-                torch.float32, torch.int32, torch.int64, torch.uint8, _raw_stream, _current_device)
+                torch.float32, torch.int32, torch.int64, torch.uint8, _raw_stream, _current_device, torch.Tensor)
     _calls = module
 
 

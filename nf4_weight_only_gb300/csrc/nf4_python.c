@@ -36,6 +36,25 @@ static PyObject* g_types[TYPES];
 static PyObject *g_raw_stream, *g_current_device;
 static PyObject *s_dtype, *s_shape, *s_is_contiguous, *s_is_cuda, *s_data_ptr, *s_cuda_stream;
 
+/* What a plain torch.Tensor's attributes and methods are made of, found once (of subclasses, or if torch makes them of
+ * something else, they are looked up every time: 0.35 us a tensor then, and 0.24 so). */
+static PyTypeObject* g_tensor;
+static PyGetSetDescrObject *g_dtype, *g_shape, *g_is_cuda;
+static PyMethodDescrObject *g_is_contiguous, *g_data_ptr;
+static PyObject* g_no_args;
+
+static PyObject* get_(PyObject* t, PyGetSetDescrObject* of, PyObject* name) {
+    if (of && Py_TYPE(t) == g_tensor) return of->d_getset->get(t, of->d_getset->closure);
+    return PyObject_GetAttr(t, name);
+}
+static PyObject* call_(PyObject* t, PyMethodDescrObject* of, PyObject* name) {
+    if (of && Py_TYPE(t) == g_tensor) {
+        if (of->d_method->ml_flags == METH_NOARGS) return of->d_method->ml_meth(t, NULL);
+        return ((PyCFunctionWithKeywords)(void (*)(void))of->d_method->ml_meth)(t, g_no_args, NULL);
+    }
+    return PyObject_CallMethodNoArgs(t, name);
+}
+
 static int is_true(PyObject* v) { /* steals v */
     const int yes = v == Py_True;
     if (!v) PyErr_Clear();
@@ -45,12 +64,12 @@ static int is_true(PyObject* v) { /* steals v */
 
 /* Whether t is a contiguous CUDA tensor of that type and shape; a negative dim takes the tensor's.  *at: its address. */
 static int tensor(PyObject* t, int type, int nd, int64_t* dims, void** at) {
-    PyObject* v = PyObject_GetAttr(t, s_dtype);
+    PyObject* v = get_(t, g_dtype, s_dtype);
     int ok = v == g_types[type];
     if (!v) PyErr_Clear();
     Py_XDECREF(v);
     if (!ok) return 0;
-    v = PyObject_GetAttr(t, s_shape);
+    v = get_(t, g_shape, s_shape);
     ok = v && PyTuple_Check(v) && PyTuple_GET_SIZE(v) == nd;
     for (int i = 0; ok && i < nd; i++) {
         const int64_t d = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i));
@@ -59,9 +78,8 @@ static int tensor(PyObject* t, int type, int nd, int64_t* dims, void** at) {
     }
     if (PyErr_Occurred()) PyErr_Clear();
     Py_XDECREF(v);
-    if (!ok || !is_true(PyObject_CallMethodNoArgs(t, s_is_contiguous)) || !is_true(PyObject_GetAttr(t, s_is_cuda)))
-        return 0;
-    v = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (!ok || !is_true(call_(t, g_is_contiguous, s_is_contiguous)) || !is_true(get_(t, g_is_cuda, s_is_cuda))) return 0;
+    v = call_(t, g_data_ptr, s_data_ptr);
     if (!v) {
         PyErr_Clear();
         return 0;
@@ -312,11 +330,30 @@ static PyObject* sample(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
                   stream));
 }
 
-/* init(addresses of the nine functions, the six types, raw-stream and current-device functions) */
+/* An attribute of the tensor type, if it is made of C as expected; a new reference that is kept. */
+static PyGetSetDescrObject* getter_of(PyObject* type, PyObject* name) {
+    PyObject* v = PyObject_GetAttr(type, name);
+    if (v && Py_TYPE(v) == &PyGetSetDescr_Type && ((PyGetSetDescrObject*)v)->d_getset->get) return (PyGetSetDescrObject*)v;
+    if (!v) PyErr_Clear();
+    Py_XDECREF(v);
+    return NULL;
+}
+static PyMethodDescrObject* method_of(PyObject* type, PyObject* name) {
+    PyObject* v = PyObject_GetAttr(type, name);
+    if (v && Py_TYPE(v) == &PyMethodDescr_Type) {
+        const int flags = ((PyMethodDescrObject*)v)->d_method->ml_flags;
+        if (flags == METH_NOARGS || flags == (METH_VARARGS | METH_KEYWORDS)) return (PyMethodDescrObject*)v;
+    }
+    if (!v) PyErr_Clear();
+    Py_XDECREF(v);
+    return NULL;
+}
+
+/* init(addresses of the nine functions, the six types, raw-stream and current-device functions, the tensor type) */
 static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
     (void)self;
     enum { CALLS = 9 };
-    ARGS(CALLS + TYPES + 2)
+    ARGS(CALLS + TYPES + 3)
     void* f[CALLS];
     for (int i = 0; i < CALLS; i++) f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return NULL;
@@ -325,6 +362,14 @@ static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t nargs) {
     for (int i = 0; i < TYPES; i++) Py_XSETREF(g_types[i], Py_NewRef(a[CALLS + i]));
     Py_XSETREF(g_raw_stream, Py_NewRef(a[CALLS + TYPES]));
     Py_XSETREF(g_current_device, Py_NewRef(a[CALLS + TYPES + 1]));
+    PyObject* type = a[CALLS + TYPES + 2];
+    if (!g_tensor && PyType_Check(type)) {
+        g_tensor = (PyTypeObject*)Py_NewRef(type);
+        g_no_args = PyTuple_New(0);
+        if (!g_no_args) return NULL;
+        g_dtype = getter_of(type, s_dtype), g_shape = getter_of(type, s_shape), g_is_cuda = getter_of(type, s_is_cuda);
+        g_is_contiguous = method_of(type, s_is_contiguous), g_data_ptr = method_of(type, s_data_ptr);
+    }
     Py_RETURN_NONE;
 }
 
