@@ -395,14 +395,14 @@ nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
  *   lengths      in   int32 [B]; a negative one counts as 0
  *   new_tokens   in   int32 [B]
  *   page_size    16 .. 65536, a multiple of 16 (nf4_kv_cache)
- *   pages        entries of the ring and pages of the cache, 0 .. 2^31-1
+ *   pages        entries of the ring and pages of the cache, 0 .. 2^31-2
  *   page_table   in/out int32 [B][max_pages]: entries of new pages are written, no others; those of a
  *                finished sequence stay as they are
  *   free_pages   in/out int32 [pages]: entries behind the ring's end are written
  *   free_in      in   int64 [2]
  *   free_out     out  int64 [2]; may be free_in
  *   lengths_out  out  int32 [B]; may be lengths
- *   starts       out  int32 [B + 1]; starts[B] is the number of new tokens (which must be below 2^31)
+ *   starts       out  int32 [B + 1]; starts[B] is the number of new tokens (sums stop at 2^31-1)
  *   slots        out  int64 [T], what nf4_kv_append takes: page * page_size + offset; -1 for the tokens of a
  *                     refused sequence and for rows from starts[B] on
  *   positions    out  int32 [T], lengths[b] + i for token i of sequence b; 0 from row starts[B] on

@@ -444,7 +444,7 @@ nf4_status nf4_plan_step(const int32_t* lengths, const int32_t* new_tokens, int6
                          int32_t* page_table, int64_t max_pages, int32_t* free_pages, const int64_t* free_in,
                          int64_t* free_out, int32_t* lengths_out, int32_t* starts, int64_t T, int64_t* slots,
                          int32_t* positions, int32_t* sequences, cudaStream_t stream) {
-    if (B < 0 || B > nf4::kPlanMaxBatch || T < 0 || T > kMaxDim || pages < 0 || pages > kMaxDim) return NF4_ERR_SHAPE;
+    if (B < 0 || B > nf4::kPlanMaxBatch || T < 0 || T > kMaxDim || pages < 0 || pages >= kMaxDim) return NF4_ERR_SHAPE;
     if (page_size < 16 || page_size > 65536 || page_size % 16 != 0) return NF4_ERR_SHAPE;
     if (max_pages < 0 || max_pages > kMaxDim || B * max_pages > (int64_t{1} << 40)) return NF4_ERR_SHAPE;
     if (!free_in || !free_out || !starts || (B > 0 && (!lengths || !new_tokens || !lengths_out))) return NF4_ERR_NULL;
@@ -472,7 +472,8 @@ nf4_status nf4_plan_step(const int32_t* lengths, const int32_t* new_tokens, int6
     a.slots = slots, a.positions = positions, a.sequences = sequences;
     a.T = T, a.max_pages = max_pages, a.pages = pages, a.B = static_cast<int>(B);
     a.page_size = static_cast<uint32_t>(page_size);
-    return from_cuda(nf4::launch_plan(a, stream));
+    a.in_place = lengths_out == lengths || free_out == free_in;
+    return from_cuda(nf4::launch_plan(a, sms, stream));
 }
 
 int64_t nf4_lora_plan_bytes(int64_t T, int64_t adapters) {

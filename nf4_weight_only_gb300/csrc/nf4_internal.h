@@ -78,7 +78,7 @@ cudaError_t launch_rmsnorm(const uint16_t* x, const uint16_t* residual, const ui
                            float eps, uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y8_scales, int num_sms,
                            cudaStream_t stream);
 
-// A step's indices (nf4_plan_step); every CTA keeps four int32 a sequence in shared memory.
+// A step's indices (nf4_plan_step); every CTA keeps five words a sequence in shared memory.
 constexpr int kPlanMaxBatch = 8192, kPlanThreads = 1024;
 struct PlanArgs {
     const int32_t *lengths, *new_tokens;
@@ -92,8 +92,9 @@ struct PlanArgs {
     int64_t T, max_pages, pages;
     int B;
     uint32_t page_size;
+    bool in_place;  // an output is its own input
 };
-cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
+cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 // Error words: 45, a page or a ring's state outside the pool; 46, an adapter or a row outside its list; 47, a plan
 // of other sizes.
 cudaError_t read_and_clear_plan_error(int* code);

@@ -81,27 +81,56 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     // a run of whole warps' widths each
     const int64_t steps = (T + 31) / 32, run0 = warp < warps ? steps * warp / warps : 0;
     const int64_t run1 = warp < warps ? steps * (warp + 1) / warps : 0;
-    constexpr int kAhead = 8;  // loads in flight
+    constexpr int kAhead = 8;  // steps whose loads are in flight; a run of no more keeps what it found
     int32_t* own = counts + warp * lists;
-    auto walk = [&](auto what) {
+    int list[kAhead];
+    uint32_t same[kAhead];  // the lanes with the same list
+    auto walk = [&](bool again, auto what) {
+#pragma unroll 1
         for (int64_t i = run0; i < run1; i += kAhead) {
-            int list[kAhead];
+            if (!again || run1 - run0 > kAhead) {
 #pragma unroll
-            for (int j = 0; j < kAhead; j++) list[j] = i + j < run1 ? list_of((i + j) * 32 + lane) : -1;
+                for (int j = 0; j < kAhead; j++) list[j] = i + j < run1 ? list_of((i + j) * 32 + lane) : -1;
+#pragma unroll
+                for (int j = 0; j < kAhead; j++) same[j] = __match_any_sync(0xFFFFFFFFu, list[j]);
+            }
 #pragma unroll
             for (int j = 0; j < kAhead; j++) {
-                if (i + j >= run1) break;
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, list[j]);
-                what((i + j) * 32 + lane, list[j], same);
+                if (i + j < run1) what((i + j) * 32 + lane, list[j], same[j]);
                 __syncwarp();
             }
         }
     };
-    walk([&](int64_t, int list, uint32_t same) {
-        if (list >= 0 && lane == __ffs(same) - 1) own[list] += __popc(same);
+    walk(false, [&](int64_t, int in, uint32_t with) {
+        if (in >= 0 && lane == __ffs(with) - 1) own[in] += __popc(with);
     });
     __syncthreads();
-    // each thread a run of lists: what the warps before a warp have, the list's tokens; sums over the lists
+    // what the warps before a warp have of a list, and the list's tokens: a warp a list, or, for few warps, a thread
+    if (warps > 8) {
+        for (int a = warp; a < lists; a += static_cast<int>(blockDim.x) / 32) {
+            const int32_t of_warp = lane < warps ? counts[lane * lists + a] : 0;
+            int32_t upto = of_warp;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (lane < warps) counts[lane * lists + a] = upto - of_warp;
+            if (lane == 31) first_of[a] = upto;
+        }
+    } else {
+        for (int a = threadIdx.x; a < lists; a += blockDim.x) {
+            int32_t all = 0;
+            for (int w = 0; w < warps; w++) {
+                const int32_t of_warp = counts[w * lists + a];
+                counts[w * lists + a] = all;
+                all += of_warp;
+            }
+            first_of[a] = all;
+        }
+    }
+    __syncthreads();
+    // sums over the lists, a run of them a thread
     const int per = (lists + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
     const int a0 = min(lists, static_cast<int>(threadIdx.x) * per), a1 = min(lists, a0 + per);
     auto many_of = [&](int a, int32_t tokens) {
@@ -112,13 +141,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
     };
     int32_t n[3] = {0, 0, 0}, upto[3];  // tokens, chunks of many, chunks of few
     for (int a = a0; a < a1; a++) {
-        int32_t all = 0;
-        for (int w = 0; w < warps; w++) {
-            const int32_t of_warp = counts[w * lists + a];
-            counts[w * lists + a] = all;
-            all += of_warp;
-        }
-        first_of[a] = all;
+        const int32_t all = first_of[a];
         n[0] += all, n[1] += many_of(a, all), n[2] += few_of(a, all);
     }
 #pragma unroll
@@ -146,7 +169,6 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
         many_at[a] = upto[1];
         if (few_of(a, tokens))
             out[many + upto[2]] = make_int4(a, upto[0] + tokens / kChunk * kChunk, tokens % kChunk, 0);
-        for (int w = 0; w < warps; w++) counts[w * lists + a] += upto[0];
         upto[0] += tokens, upto[1] += many_of(a, tokens), upto[2] += few_of(a, tokens);
     }
     __syncthreads();
@@ -166,15 +188,16 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const int32_t* __restri
         reinterpret_cast<int4*>(plan)[0] = make_int4(static_cast<int32_t>(T), adapters, many, few);
         reinterpret_cast<int4*>(plan)[1] = make_int4(first_of[adapters], 0, 0, 0);
     }
-    walk([&](int64_t t, int list, uint32_t same) {
-        const int leader = __ffs(same) - 1;
+    walk(true, [&](int64_t t, int in, uint32_t with) {
+        const int leader = __ffs(with) - 1;
         int32_t at = 0;
-        if (list >= 0 && lane == leader) {
-            at = own[list];
-            own[list] = at + __popc(same);
+        if (in >= 0 && lane == leader) {
+            at = own[in];
+            own[in] = at + __popc(with);
+            at += first_of[in];
         }
-        at = __shfl_sync(0xFFFFFFFFu, at, leader) + __popc(same & ((1u << lane) - 1));
-        if (list >= 0) order[at] = static_cast<int32_t>(t);
+        at = __shfl_sync(0xFFFFFFFFu, at, leader) + __popc(with & ((1u << lane) - 1));
+        if (in >= 0) order[at] = static_cast<int32_t>(t);
     });
     if (bad) atomicCAS(&g_lora_error, 0, 46);
 }

@@ -30,7 +30,7 @@ def plan(lib, **change):
 
 @pytest.mark.parametrize("change,want", [
     (dict(batch=-1), SHAPE), (dict(batch=8193), SHAPE), (dict(t=-1), SHAPE), (dict(t=1 << 31), SHAPE),
-    (dict(pages=-1), SHAPE), (dict(pages=1 << 31), SHAPE), (dict(page_size=8), SHAPE), (dict(page_size=24), SHAPE),
+    (dict(pages=-1), SHAPE), (dict(pages=1 << 31), SHAPE), (dict(pages=(1 << 31) - 1), SHAPE), (dict(page_size=8), SHAPE), (dict(page_size=24), SHAPE),
     (dict(page_size=131072), SHAPE), (dict(page_size=0), SHAPE), (dict(max_pages=-1), SHAPE),
     (dict(batch=8192, max_pages=(1 << 31) - 1), SHAPE),
     (dict(lengths=0), NULL), (dict(new_tokens=0), NULL), (dict(table=0), NULL), (dict(ring=0), NULL),
