@@ -577,14 +577,15 @@ __device__ __forceinline__ Block block_of(const LoraArgs& a, int block) {
     return r;
 }
 
-// v * s as the sum of two bf16 numbers each.
+// v * s as the sum of two bf16 numbers each; an infinity as itself and zero, so that it stays one.
+__device__ __forceinline__ float rest_of(float f, float hi) { return fabsf(hi) == INFINITY ? 0.0f : f - hi; }
 __device__ __forceinline__ void split_h(const float4& v, float s, uint16_t* hi, uint16_t* lo) {
     const float f[4] = {v.x * s, v.y * s, v.z * s, v.w * s};
     const uint32_t h01 = f32x2_to_bf16x2(f[0], f[1]), h23 = f32x2_to_bf16x2(f[2], f[3]);
     const float2 r01 = bf16x2_to_f32x2(h01), r23 = bf16x2_to_f32x2(h23);
     *reinterpret_cast<uint2*>(hi) = make_uint2(h01, h23);
-    *reinterpret_cast<uint2*>(lo) =
-        make_uint2(f32x2_to_bf16x2(f[0] - r01.x, f[1] - r01.y), f32x2_to_bf16x2(f[2] - r23.x, f[3] - r23.y));
+    *reinterpret_cast<uint2*>(lo) = make_uint2(f32x2_to_bf16x2(rest_of(f[0], r01.x), rest_of(f[1], r01.y)),
+                                               f32x2_to_bf16x2(rest_of(f[2], r23.x), rest_of(f[3], r23.y)));
 }
 
 // h of a chunk for one projection: its slices from `h` on, `step` floats apart, summed in order, times s, as the sum of

@@ -255,3 +255,41 @@ def test_one_workspace_serves_smaller_calls():
         big.run()
         c.check()
         big.check()
+
+
+@pytest.mark.parametrize("ns,in_place", [([520, 136], True), ([256], False), ([8], True), ([24, 1000], False), ([57, 64], True)])
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
+def test_long_prompts(ns, in_place, rank):
+    """Calls with many tokens: rows that 16-byte copies reach and rows that they do not, last blocks of eight columns,
+    chunks of 64 and of less beside rows without an adapter."""
+    t = 1700
+    ids = ([0] * 700 + [-1] * 61 + [2] * 337 + [1] * 90 + [2] * 64 + [4] * 5 + [0] * 300)
+    ids += [-1] * (t - len(ids))
+    c = Case(t, 320, ns, rank, 5, ids, seed=rank + len(ns), in_place=in_place)
+    c.run()
+    first = [y.t.clone() for y in c.ys]
+    c.check()
+    if not in_place:
+        c.run()
+        assert all(torch.equal(y.t, f) for y, f in zip(c.ys, first))
+
+
+@pytest.mark.parametrize("t", [5, 40])
+@pytest.mark.parametrize("rank", [8, 16, 64])
+def test_infinities(t, rank):
+    """An infinite input, and products past the range of fp32, give what they give in the formula, in their row alone."""
+    c = Case(t, 128, [40], rank, 1, [0] * t, seed=t)
+    c.a[0].zero_()
+    c.a[0][0, :, 3] = 1.0  # h_r = x[3], and y = base + s x[3] (the sum of B's row)
+    c.b[0].copy_(c.b[0].abs() + 1)
+    c.b[0][0, 1::2] *= -1
+    c.scales.fill_(0.5)
+    for row, value in [(0, float("inf")), (t - 1, -float("inf")), (2, float("nan"))]:
+        c.x[row, 3] = value
+    c.run()
+    y = c.ys[0].t.float()
+    up = torch.tensor([1.0, -1.0] * 20, device=DEV) * float("inf")
+    assert torch.equal(y[0], up) and torch.equal(y[t - 1], -up) and bool(y[2].isnan().all())
+    keep = [r for r in range(t) if r not in (0, 2, t - 1)]
+    assert bool(y[keep].isfinite().all())
+    c.check(sample=keep)
