@@ -31,7 +31,7 @@
  *     M, N and K must each be at most 2^31 - 1.
  *   - Non-finite inputs are outside the contract: results are unspecified, but no call faults.
  *   - The same inputs give the same output bytes on every call (fixed reduction order; atomics only
- *     hand out the attention's work).
+ *     hand out the attention's work, add integers, and list candidates whose order is then settled).
  *   - Every call may be captured into a CUDA graph (the kernels build their constant tables in
  *     shared memory at launch; no call needs one-time device work), except the first call of
  *     nf4_linear_host_noalloc on a device (see there).
@@ -473,8 +473,9 @@ nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, i
  *   tokens       out  int32 [B]
  *   logprobs     out  float [B] or NULL: log softmax(l) of the token, before temperature and cuts
  * V in 1 .. 262144, stride >= V, B at most 2^24; everything is aligned to its elements (rows may start anywhere).
- * Logits of -inf (masked) and NaN have no weight; a row with nothing else gives token -1 and logprob -inf.  Weights
- * are whole multiples of 2^-40 (each within 2^-37), so sums are exact and the drawn token does not depend on their order.
+ * Logits of -inf (masked) and NaN have no weight; a row with nothing else gives token -1 and logprob -inf, one with
+ * +inf the first of n such and logprob -log n.  Weights are whole multiples of 2^-40 (each within 2^-30 of its size, or half a multiple), so
+ * sums are exact and the drawn token does not depend on their order; what weighs less than half a multiple is never drawn.
  */
 nf4_status nf4_sample(const void* logits, int logits_bf16, int64_t B, int64_t V, int64_t stride, const float* temperature,
                       const int32_t* top_k, const float* top_p, const float* min_p, const float* random, int32_t* tokens,
@@ -488,8 +489,7 @@ nf4_status nf4_sample(const void* logits, int logits_bf16, int64_t B, int64_t V,
  * unspecified.  nf4_embed records 41 for an id outside the table, the cache calls 42 for a slot
  * outside the cache, nf4_attention_decode 43 for a page or length outside its bounds (44: a
  * shared-memory layout that its kernel does not know; nothing is computed then), nf4_plan_step 45,
- * nf4_lora_plan 46 and nf4_lora 47 (see there).  *code receives the
- * first recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
+ * nf4_lora_plan 46 and nf4_lora 47 (see there).  *code receives the first recorded code (0 = none).  This call waits for the device (it is not meant for the hot path).
  */
 nf4_status nf4_check_device_error(int* code);
 

@@ -10,6 +10,12 @@
 // Both use mma.sync m16n8k16 with tokens as the 16 rows and weights as the 8 columns.  A product's k axis may
 // be permuted at will if both operands are permuted alike: a lane takes eight consecutive k (16 bytes) of its
 // row or column, which is two k steps of the instruction, and needs neither shared memory nor shuffles.
+//
+// Times with the plan, calls queued, and those of the bytes alone at the measured copy rate (us): q|k|v of one token, rank
+// 16: 11.0 / 0.04; gate|up of 64 tokens with 48 adapters: 28.9 / 9.9; q|k|v of 256 tokens, rank 64: 41.5 / 11.8; down of
+// 5, rank 128: 21.5 / 6.4; o of 8191, rank 16: 76 / 37; gate|up of 4099, rank 64: 194 / 91.  Few tokens are bound by three
+// launches and the chains of loads inside them, many by the latency of the base's loads at 16 warps an SM (second kernel:
+// issue slots 34-36%, L1 53-56%, tensor pipe 11-33%, long-scoreboard stalls 3.9 an issue).
 #include <mutex>
 
 #include "nf4_kv.cuh"
@@ -18,10 +24,12 @@ namespace nf4 {
 namespace {
 
 constexpr int kChunk = 64;      // tokens of a chunk at most
-constexpr int kFew = 16;        // of a chunk of few
+constexpr int kFew = 16;        // of a chunk of few (8: q|k|v of 256 tokens 42 -> 45 us, o of 8191 76 -> 74)
 constexpr int kHeader = 8;      // int32 before the chunks: T, adapters, chunks of many, of few, tokens with an adapter
 constexpr int kThreads = 256;
-constexpr int kUnits = 304;     // of the first product: two CTAs for each of 152 SMs
+// Of the first product: two CTAs for each of 152 SMs.  (152: down of 5 tokens 23 -> 26 us, o of 8191 85 -> 95, q|k|v of 256
+// 43 -> 41; 608: 26, 87 and 44.)
+constexpr int kUnits = 304;
 constexpr int kMaxSlices = 32;
 
 __device__ int g_lora_error;  // 46: an adapter or a row outside its list; 47: a plan of other sizes
@@ -250,12 +258,14 @@ __device__ __forceinline__ bool chunk_ok(const LoraArgs& a, const Plan& p, const
 __device__ __forceinline__ int64_t token_at(const LoraArgs& a, const Plan& p, int at) {
     return min(static_cast<uint32_t>(p.order[at]), static_cast<uint32_t>(a.T - 1));
 }
-constexpr int kFewTiles = 4;    // rank columns of a unit with few tokens, in eights
-constexpr int kManyTiles = 16;  // and with many
+// Rank columns of a unit with few tokens, in eights (4 make fewer, longer units: down of 5 tokens 22 -> 23 us, gate|up of 64
+// 29 -> 30), and with many (all that the stage and the accumulators hold, so that x is read once).
+constexpr int kFewTiles = 2, kManyTiles = 16;
 
 // How the first product is cut: rank-column groups, slices of K (in units of 64), and the rows of the workspace that a
 // chunk's slice takes (64 or 16, the chunks of many first).  As many slices as fill the GPU in one round, each with at
-// least one step of 32 for every warp; but eight at most with many tokens, whose sums the second product waits for.
+// least one step of 32 for every warp; but eight at most with many tokens, whose sums the second product waits for (q|k|v of
+// 256 tokens: 43.3 us; 44.6 with four, 46.6 with sixteen).
 struct Cut {
     int many_groups, few_groups, many_slices, few_slices;
     __device__ __forceinline__ int64_t many_row(int chunk, int slice) const {
@@ -493,6 +503,8 @@ template <int W>
 struct Weights {
     uint4 w[4][W];
     static constexpr int kLane = 8, kCols = W * 32;  // values of a row that a lane takes at a time, that fit
+    // of h's rows in shared memory, so that the eight lanes of a 128-bit read (two rows) hit all banks
+    static constexpr int kStride = W == 1 ? kCols : kCols + 32;
     // Rows `from`, from + 2, ... behind p, all there and of kCols values: every address is a constant away.
     __device__ __forceinline__ void load_whole(const uint16_t* p, int from) {
 #pragma unroll
@@ -536,7 +548,7 @@ struct Weights {
 template <>
 struct Weights<0> {
     uint2 w[4];
-    static constexpr int kLane = 4, kCols = 16;
+    static constexpr int kLane = 4, kCols = 16, kStride = 16;  // (sixteen lanes, four rows)
     __device__ __forceinline__ void load_whole(const uint16_t* p, int from) {
 #pragma unroll
         for (int j = 0; j < 4; j++) w[j] = __ldg(reinterpret_cast<const uint2*>(p + (from + 2 * j) * kCols));
@@ -652,12 +664,14 @@ __device__ __forceinline__ void add_row(const uint16_t* base, uint16_t* y, const
     }
 }
 
-// A unit is a chunk and 256 rows of one projection, 32 a warp.  Units u0 .. u1 of the chunks of many: bound by the bytes
-// of y, so the base of 32 or 64 tokens is on its way before anything is multiplied.
+// A unit is a chunk and 256 rows of one projection, 32 a warp.  Units u0 .. u1 of the chunks of many: bound by the base and
+// y, so the base of several tiles is on its way at once.
 template <int W, bool EXACT>
 __device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, const Cut& cut, int blocks, int64_t u0,
                                             int64_t u1, uint16_t* hi, uint16_t* lo, int32_t* rows) {
-    constexpr int kCols = Weights<W>::kCols, kStride = kCols + 8;
+    constexpr int kCols = Weights<W>::kCols, kStride = Weights<W>::kStride;
+    // tiles of 16 tokens whose base is on its way (gate|up of 4099 tokens, rank 64: 194 us; 207 with one, 210 with four)
+    constexpr int kTiles = W >= 4 ? 1 : W >= 1 ? 2 : 4;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4, warp_row = threadIdx.x / 32 * 32;
     const int rank = EXACT ? kCols : a.rank, R = a.count * rank;
     int held = -1, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
@@ -689,22 +703,23 @@ __device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, co
             w.load_whole(b, 0);
         else
             w.load(b, 0, N - 1 - first_row, rank, t);
-        constexpr int kTiles = W >= 2 ? 2 : 4;  // tiles of 16 tokens whose base is on its way
 #pragma unroll 1
-        for (int r0 = g; r0 - g < chunk.z; r0 += 16 * kTiles) {
+        for (int r0 = 0; r0 < chunk.z; r0 += 16 * kTiles) {
             uint4 in[2 * kTiles];
 #pragma unroll
-            for (int m = 0; m < 2 * kTiles; m++)
-                if (vec && in_row && r0 + 8 * m < chunk.z)
-                    in[m] = *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(rows[r0 + 8 * m]) * N);
+            for (int m = 0; m < 2 * kTiles; m++) {
+                const int r = r0 + g + 8 * m;
+                if (vec && in_row && r < chunk.z)
+                    in[m] = *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(rows[r]) * N);
+            }
 #pragma unroll
             for (int m = 0; m < 2 * kTiles; m += 2) {
-                if (r0 - g + 8 * m >= chunk.z) continue;
+                if (r0 + 8 * m >= chunk.z) continue;
                 float acc[4][4];
-                w.multiply(acc, hi, lo, r0 + 8 * m, kStride, t);
+                w.multiply(acc, hi, lo, r0 + g + 8 * m, kStride, t);
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    const int r = r0 + 8 * (m + h);
+                    const int r = r0 + g + 8 * (m + h);
                     if (r >= chunk.z || !in_row) continue;
                     const int64_t at = static_cast<int64_t>(rows[r]) * N;
                     add_row(base + at, y + at, in[m + h], acc, h, vec, n, N);
@@ -756,7 +771,7 @@ __device__ __forceinline__ void copy_idle(const LoraArgs& a, const Plan& p, int 
 template <int W, int D, bool EXACT>
 __device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, const Cut& cut, int blocks, int64_t u0,
                                            int64_t u1, uint16_t* hi, uint16_t* lo) {
-    constexpr int kCols = Weights<W>::kCols, kStride = kCols + 8;
+    constexpr int kCols = Weights<W>::kCols, kStride = Weights<W>::kStride;
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4, warp_row = threadIdx.x / 32 * 32;
     const int rank = EXACT ? kCols : a.rank, R = a.count * rank;
     int held = -1, held_chunk = -1, batch = 0, c = static_cast<int>(u0 / blocks), at_block = static_cast<int>(u0 % blocks);
@@ -833,10 +848,11 @@ __device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, con
 }
 
 // The units of all kinds on one line, each as long as it weighs (what it moves, roughly), cut into equal parts for the
-// CTAs: a unit belongs to the one in whose part it begins.
+// CTAs: a unit belongs to the one in whose part it begins.  (All weights 1: q|k|v of 256 tokens 42 -> 50 us; many against
+// few 4 : 1 or 2 instead of 2 : 1: 44.)
 template <int W, int D, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, int blocks, bool copy) {
-    constexpr int kStride = Weights<W>::kCols + 8;
+    constexpr int kStride = Weights<W>::kStride;
     __shared__ __align__(16) uint16_t hi[kChunk * kStride], lo[kChunk * kStride];
     __shared__ int32_t rows[kChunk];
     pdl_launch_dependents();
@@ -844,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 2) expand_kernel(const LoraArgs a, i
     Plan p;
     if (!read_plan(a, &p)) return;
     const Cut cut = cut_of(a, p);
-    constexpr int kMany = 4, kFewWeight = W >= 2 ? 2 : 1;
+    constexpr int kMany = 2, kFewWeight = 1;
     const int64_t idle = copy ? (a.T - p.n_tokens + kChunk - 1) / kChunk * blocks : 0;
     const int idle_weight = a.T - p.n_tokens >= kChunk ? kMany : 1;
     const int64_t to_few = static_cast<int64_t>(p.n_many) * blocks * kMany;
@@ -935,10 +951,11 @@ cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
         e = cudaLaunchKernelEx(&cfg, shrink_kernel, a);
         if (e != cudaSuccess) return e;
     }
-    // (ranks of exactly 16, 32, 64 and 128 have constants for addresses)
+    // Ranks of exactly 16, 32, 64 and 128 have constants for addresses (o of 8191 tokens 89 -> 85 us).  D is what registers
+    // allow (rank 16, gate|up of 64 tokens: 30.3 us with 2, 34 with 1, 32 with 4, which spills).
 #define NF4_EXPAND(W, D) \
     return a.rank == Weights<W>::kCols ? expand<W, D, true>(a, num_sms, stream) : expand<W, D, false>(a, num_sms, stream)
-    if (a.rank <= 16) NF4_EXPAND(0, 4);
+    if (a.rank <= 16) NF4_EXPAND(0, 2);
     if (a.rank <= 32) NF4_EXPAND(1, 2);
     if (a.rank <= 64) NF4_EXPAND(2, 1);
     NF4_EXPAND(4, 1);

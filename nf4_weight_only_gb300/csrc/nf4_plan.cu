@@ -5,9 +5,9 @@
 // of free pages that it takes; both are integers, so every order of addition gives the same.
 //
 // What bounds it: the latency of one launch, of two dependent reads and of two block scans (8 sequences of one
-// token: PLAN_SMALL), and for long prompts the instructions that find a token's sequence and page and the 16 bytes that its
-// place, position and sequence take (32768 tokens of 512 sequences: PLAN_LARGE).  Every CTA reads all B counts and scans
-// them for itself (a few kilobytes from L2), which spares a second launch; the rows are shared out among the CTAs.
+// token: 3.4 us replayed in a graph, 5.1 us a call, the host's), and for long prompts the search for a token's sequence
+// and page (32768 tokens of 512 sequences: 5.7 us, 0.08 of it their 16 bytes each).  Every CTA reads all B counts and
+// scans them for itself (a few kilobytes from L2), which spares a second launch; the rows are shared out among the CTAs.
 // Where `lengths` or the ring's state are updated in place, the CTAs are one cluster: its barrier stands between the
 // last read and the first write.
 #include <mutex>
@@ -196,9 +196,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a, ui
 }  // namespace
 
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream) {
-    // A row or two a thread; in place no more CTAs than a cluster has.
+    // A row or two a thread; in place no more CTAs than a cluster has (32768 tokens: 6.5 us with 32 CTAs, 8.3 with 8, 33
+    // with one).  Small CTAs start sooner (5.7 us with 64 of 256 threads); large ones scan many sequences, or share out the
+    // rows of a cluster.
     const int64_t rows = a.T > a.B ? a.T : a.B;
-    const int threads = rows <= 256 ? 256 : kPlanThreads;
+    const int threads = rows <= 256 || (!a.in_place && a.B <= 1024) ? 256 : kPlanThreads;
     int ctas = 1;
     while (ctas < (a.in_place ? 8 : num_sms / 2) && rows > 2 * threads * ctas) ctas *= 2;
     const int bytes = 5 * (a.B + 1) * static_cast<int>(sizeof(int32_t));

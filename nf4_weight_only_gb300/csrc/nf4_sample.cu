@@ -12,6 +12,11 @@
 // A row is held by the CTAs of one cluster, a slice of it in the shared memory of each, so the logits are read once
 // from memory; what a row needs next (its maximum, where the order is cut, which slice the token is in)
 // is exchanged through distributed shared memory.
+//
+// What bounds it: for few rows the chain of steps between barriers (one row of 151936 bf16 logits, top-k 50: 9.9 us, 0.05 of
+// it the bytes); for many the instructions of the passes over a slice and those steps, of two CTAs an SM (256 such rows
+// 55.6 us, 11.7 of it the bytes: issue slots 36%; 128 rows in fp32 without cuts, a weight for each of their 19 million logits,
+// 88 us: issue slots 43%, and the CTAs' waits for one another).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,7 +35,7 @@ constexpr int kBins = 1024;  // two a thread
 constexpr int kMaxCluster = 8;
 constexpr int kList = 2048;            // candidates that a row's cut is found among
 constexpr int kFewBins = 256;          // eight a lane
-constexpr int kFewest = 128;           // top_k up to this may take the short way
+constexpr int kFewest = 128;           // top_k up to this may take the short way (256 rows of top-k 50: 198 -> 56 us)
 constexpr int kSliceBytes = 80 * 1024; // of a slice, for two CTAs an SM
 constexpr int kOne = 40;               // a weight of 1 is 2^40
 constexpr float kFarthest = 41.0f;     // in powers of 2: what lies further from the top has no weight
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     // one thread; the others have seen sh.log_sum written
     auto finish = [&](int token, float logit) {
         a.tokens[b] = token;
-        if (a.logprobs) a.logprobs[b] = token < 0 ? minus_inf() : (logit - top) - sh.log_sum;
+        if (a.logprobs) a.logprobs[b] = token < 0 ? minus_inf() : (logit == top ? 0.0f : logit - top) - sh.log_sum;
     };
     if (top == minus_inf() || cold) {  // no token, or the first of the largest
         if (rank == 0 && tid == 0) {
@@ -464,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         cluster.sync();
         if (rank == 0 && tid == 0) {
             for (int r = 0; r < ranks; r++) at = min(at, sh.notes[1][r].at);
-            sh.log_sum = 0.0f;
+            if (a.logprobs) sh.log_sum = log_of_sum();
             finish(at, top);
         }
         return;
@@ -871,9 +876,9 @@ cudaError_t sample(const SampleArgs& a, int num_sms, cudaStream_t stream) {
         e = cudaFuncSetAttribute(sample_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     });
     if (e != cudaSuccess) return e;
-    // Eight CTAs a row for a few rows, where the row's own steps count (one row of 151936 bf16 logits, top-k 50: 13.6 us
-    // with 8, 15.0 with 4); for many rows as few as leave an SM room for two CTAs, since each has the same
-    // overhead whatever its slice (256 such rows: 93 us with 8, 68 with 4, 74 with 2).
+    // Eight CTAs a row for a few rows, where the row's own steps count (one row of 151936 bf16 logits, top-k 50: 9.9 us
+    // with 8, 10.9 with 4; 16 rows of 50001: 32.4 with 8, 44 with 2); for many rows as few as leave an SM room for two CTAs,
+    // since each has the same overhead whatever its slice (256 rows of 151936: 76 us with 8, 56 with 4).
     int ranks = 1;
     while (ranks < kMaxCluster && a.V > 4096 * ranks &&
            (a.B * ranks < num_sms || (a.V + ranks - 1) / ranks * E > kSliceBytes))

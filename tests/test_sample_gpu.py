@@ -248,3 +248,15 @@ def test_captured_calls_and_several_streams():
     torch.cuda.synchronize()
     for g in got:
         assert torch.equal(g[0], again[0]) and torch.equal(g[1], again[1])
+
+
+@pytest.mark.parametrize("v", [9, 700, 30011])
+@pytest.mark.parametrize("settings", [{}, dict(top_k=[5] * 3), dict(temperature=[0.0] * 3), dict(top_p=[0.5] * 3)])
+def test_infinite_logits_have_equal_shares(v, settings):
+    """log softmax of a row with n infinite logits is -log n at each; one row's infinities are in two slices."""
+    l, u = rows(3, v, 4)
+    l[0, v // 2] = l[1, v - 1] = l[1, 2] = l[2, 0] = float("inf")
+    l[2, 1::2] = -float("inf")
+    tokens, logs = call(l, u, **settings)
+    assert tokens == [v // 2, 2, 0]
+    assert logs[0] == 0.0 and abs(logs[1] + np.log(2.0)) <= 2.0 ** -24 and logs[2] == 0.0
