@@ -13,7 +13,7 @@
 //
 // Times with the plan, calls queued, and those of the bytes alone at the measured copy rate (us): q|k|v of one token, rank
 // 16: 11.0 / 0.04; gate|up of 64 tokens with 48 adapters: 28.9 / 9.9; q|k|v of 256 tokens, rank 64: 41.5 / 11.8; down of
-// 5, rank 128: 21.5 / 6.4; o of 8191, rank 16: 76 / 37; gate|up of 4099, rank 64: 194 / 91.  Few tokens are bound by three
+// 5, rank 128: 21.5 / 6.4; o of 8191, rank 16: 75 / 37; gate|up of 4099, rank 64: 194 / 91.  Few tokens are bound by three
 // launches and the chains of loads inside them, many by the latency of the base's loads at 16 warps an SM (second kernel:
 // issue slots 34-36%, L1 53-56%, tensor pipe 11-33%, long-scoreboard stalls 3.9 an issue).
 #include <mutex>
@@ -375,7 +375,8 @@ __device__ __forceinline__ void shrink_few(const LoraArgs& a, const Plan& p, con
 }
 
 // A unit with many tokens, up to 64 by 128 columns: bound by the bytes of x, so x is read once for all columns.  Stages
-// of 128 k, of x and of A, are copied into shared memory while the last one is multiplied; a row is 16 pieces of 16
+// of 128 k, of x and of A, are copied into shared memory while one is multiplied, two of 128 columns or up to four of
+// fewer (o of 8191 tokens, rank 16: 76.3 -> 74.8 us); a row is 16 pieces of 16
 // bytes, and the odd rows' pieces change places by four, so that the eight lanes of a 128-bit read (two rows) hit
 // all banks.  Eight warps: two halves of the tokens, and column groups of up to four tiles; with few columns the
 // warps of a half share out the stage's k instead.
@@ -394,6 +395,7 @@ __device__ __forceinline__ void shrink_many(const LoraArgs& a, const Plan& p, co
     const int each = (tiles + col_groups - 1) / col_groups, first_tile = col_group * each;
     const int own_tiles = max(0, min(each, tiles - first_tile));
     const int64_t steps = a.K / 64, k0 = 64 * (steps * slice / n_slices), k1 = 64 * (steps * (slice + 1) / n_slices);
+    const int stage_bytes = (kChunk + tiles * 8) * kStageK * 2, stages = min(4, 2 * kStageBytes / stage_bytes);
     // what this thread copies: piece `piece` of rows first, first + 16, ...
     const int piece = threadIdx.x % 16, first = threadIdx.x / 16;
     const uint16_t* src[12];
@@ -418,16 +420,26 @@ __device__ __forceinline__ void shrink_many(const LoraArgs& a, const Plan& p, co
     };
     float acc[2][4][4] = {};
     __syncthreads();  // the last unit's sums are read
-    copy(k0, ring);
-    int at = 0;
-    for (int64_t k = k0; k < k1; k += kStageK, at ^= 1) {
-        if (k + kStageK < k1)
-            copy(k + kStageK, ring + (at ^ 1) * kStageBytes);
+    for (int i = 0; i < stages - 1; i++) {
+        if (k0 + i * kStageK < k1)
+            copy(k0 + i * kStageK, ring + i * stage_bytes);
         else
             cp_async_commit();
-        cp_async_wait<1>();
+    }
+    int at = 0;
+    for (int64_t k = k0; k < k1; k += kStageK, at = at + 1 == stages ? 0 : at + 1) {
+        if (k + (stages - 1) * kStageK < k1)
+            copy(k + (stages - 1) * kStageK, ring + (at ? at - 1 : stages - 1) * stage_bytes);
+        else
+            cp_async_commit();
+        if (stages == 2)
+            cp_async_wait<1>();
+        else if (stages == 3)
+            cp_async_wait<2>();
+        else
+            cp_async_wait<3>();
         __syncthreads();
-        const uint8_t* stage = ring + at * kStageBytes;
+        const uint8_t* stage = ring + at * stage_bytes;
 #pragma unroll
         for (int s = 0; s < kStageK / 32; s++) {
             if (s % k_groups != k_group) continue;
@@ -644,23 +656,31 @@ __device__ __forceinline__ void stage_h(const float* h, int R, int rank, int tok
     }
 }
 
-// Adds a lane's eight results (row h * 8 + g of a tile) to the base, at `base` and `y`: columns col .. col + 7 of N.
-__device__ __forceinline__ void add_row(const uint16_t* base, uint16_t* y, const uint4& v, const float (&acc)[4][4], int h,
-                                        bool vec, int col, int N) {
-    if (vec) {
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t out[4];
+// Eight values of the base from column col on, in rows that begin anywhere: read one by one, and before anything is
+// stored (a load stays behind a store that may be to its place: one by one, 778 tokens beside 328 + 73 columns took 32 us,
+// not 22).
+__device__ __forceinline__ uint4 odd_row(const uint16_t* base, int col, int N) {
+    uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = bf16x2_to_f32x2(in[j]);
-            out[j] = f32x2_to_bf16x2(f.x + acc[j][2 * h], f.y + acc[j][2 * h + 1]);
-        }
+    for (int j = 0; j < 8; j++) v[j] = col + j < N ? base[j] : 0;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+
+// Adds a lane's eight results (row h * 8 + g of a tile) to the base `v`, to `y`: columns col .. col + 7 of N.
+__device__ __forceinline__ void add_row(uint16_t* y, const uint4& v, const float (&acc)[4][4], int h, bool vec, int col, int N) {
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const float2 f = bf16x2_to_f32x2(in[j]);
+        out[j] = f32x2_to_bf16x2(f.x + acc[j][2 * h], f.y + acc[j][2 * h + 1]);
+    }
+    if (vec) {
         *reinterpret_cast<uint4*>(y) = make_uint4(out[0], out[1], out[2], out[3]);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++)
-            if (col + j < N)
-                y[j] = bf16_bits(__uint_as_float(static_cast<uint32_t>(base[j]) << 16) + acc[j / 2][2 * h + j % 2]);
+            if (col + j < N) y[j] = static_cast<uint16_t>(out[j / 2] >> (16 * (j % 2)));
     }
 }
 
@@ -715,6 +735,12 @@ __device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, co
 #pragma unroll
             for (int m = 0; m < 2 * kTiles; m += 2) {
                 if (r0 + 8 * m >= chunk.z) continue;
+                if (!vec)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int r = r0 + g + 8 * (m + h);
+                        if (r < chunk.z) in[m + h] = odd_row(base + static_cast<int64_t>(rows[r]) * N, n, N);
+                    }
                 float acc[4][4];
                 w.multiply(acc, hi, lo, r0 + g + 8 * m, kStride, t);
 #pragma unroll
@@ -722,7 +748,7 @@ __device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, co
                     const int r = r0 + g + 8 * (m + h);
                     if (r >= chunk.z || !in_row) continue;
                     const int64_t at = static_cast<int64_t>(rows[r]) * N;
-                    add_row(base + at, y + at, in[m + h], acc, h, vec, n, N);
+                    add_row(y + at, in[m + h], acc, h, vec, n, N);
                 }
             }
         }
@@ -757,10 +783,17 @@ __device__ __forceinline__ void copy_idle(const LoraArgs& a, const Plan& p, int 
             for (int q = 0; q < 8; q++)
                 if (at[q] >= 0) *reinterpret_cast<uint4*>(y + at[q]) = v[q];
         } else {
-            for (int r = 0; r < tokens; r++)
-                for (int col = n0 + lane; col < N && col < n0 + batch * 256; col += 256) {
-                    const int64_t at = token_at(a, p, first + r) * N + col;
-                    y[at] = base[at];
+            for (int col = n0 + lane; col < N && col < n0 + batch * 256; col += 256)
+                for (int r = 0; r < tokens; r += 8) {  // loads before stores, which may not pass each other
+                    uint16_t v[8];
+                    int64_t at[8];
+#pragma unroll
+                    for (int q = 0; q < 8; q++) {
+                        at[q] = token_at(a, p, first + min(r + q, tokens - 1)) * N + col;
+                        v[q] = base[at[q]];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; q++) y[at[q]] = v[q];  // (the last row may be written twice, alike)
                 }
         }
     }
@@ -837,12 +870,16 @@ __device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, con
 #pragma unroll
         for (int d = 0; d < D; d++) {
             if (d >= batch) continue;
+            if (!vec)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    if (real[h]) in[d][h] = odd_row(base + at[h] + 256 * d, n + 256 * d, N);
             float acc[4][4];
             w[d].multiply(acc, hi, lo, g, kStride, t);
             if (n + 256 * d >= N) continue;
             const int64_t more = 256 * d;
-            if (real[0]) add_row(base + at[0] + more, y + at[0] + more, in[d][0], acc, 0, vec, n + 256 * d, N);
-            if (both && real[1]) add_row(base + at[1] + more, y + at[1] + more, in[d][1], acc, 1, vec, n + 256 * d, N);
+            if (real[0]) add_row(y + at[0] + more, in[d][0], acc, 0, vec, n + 256 * d, N);
+            if (both && real[1]) add_row(y + at[1] + more, in[d][1], acc, 1, vec, n + 256 * d, N);
         }
     }
 }
