@@ -293,3 +293,13 @@ def test_infinities(t, rank):
     keep = [r for r in range(t) if r not in (0, 2, t - 1)]
     assert bool(y[keep].isfinite().all())
     c.check(sample=keep)
+
+
+@pytest.mark.parametrize("ns", [[57, 320], [1, 259], [41]])
+@pytest.mark.parametrize("rank,in_place", [(16, False), (24, True), (64, False), (128, True), (128, False)])
+def test_rows_that_begin_anywhere(ns, rank, in_place):
+    """Odd heights with chunks of 64, of less and of few, and whole and broken runs of rows without an adapter."""
+    ids = [-1] * 71 + [0] * 150 + [-1] * 9 + [1] * 13 + [2] * 64 + [3] + [-1] * 64
+    c = Case(len(ids), 192, ns, rank, 4, ids, seed=rank + len(ns), in_place=in_place)
+    c.run()
+    c.check()
