@@ -264,8 +264,9 @@ constexpr int kFewTiles = 2, kManyTiles = 16;
 
 // How the first product is cut: rank-column groups, slices of K (in units of 64), and the rows of the workspace that a
 // chunk's slice takes (64 or 16, the chunks of many first).  As many slices as fill the GPU in one round, each with at
-// least one step of 32 for every warp; but eight at most with many tokens, whose sums the second product waits for (q|k|v of
-// 256 tokens: 43.3 us; 44.6 with four, 46.6 with sixteen).
+// least one step of 32 for every warp; but with many tokens, whose sums the second product waits for, no more than eight
+// (q|k|v of 256 tokens: 43.3 us; 44.6 with four, 46.6 with sixteen) or slices of 512 (649 tokens, K 16064, rank 64: 66 us
+// with eight, 56 with 23).
 struct Cut {
     int many_groups, few_groups, many_slices, few_slices;
     __device__ __forceinline__ int64_t many_row(int chunk, int slice) const {
@@ -281,7 +282,7 @@ __device__ __forceinline__ Cut cut_of(const LoraArgs& a, const Plan& p) {
     c.many_groups = (tiles + kManyTiles - 1) / kManyTiles;
     c.few_groups = (tiles + kFewTiles - 1) / kFewTiles;
     const int many = max(1, p.n_many * c.many_groups), few = max(1, p.n_few * c.few_groups);
-    c.many_slices = max(1, min(min(most, 8), kUnits / many));
+    c.many_slices = max(1, min(min(most, max(8, K / 512)), kUnits / many));
     c.few_slices = max(1, min(most, kUnits / few));
     return c;
 }
@@ -613,46 +614,34 @@ __device__ __forceinline__ void split_h(const float4& v, float s, uint16_t* hi, 
 }
 
 // h of a chunk for one projection: its slices from `h` on, `step` floats apart, summed in order, times s, as the sum of
-// two bf16 numbers (2^-16 of it), rows of kStride; zeros up to whole tiles.  A thread takes four columns of a row, ITEMS
-// such and AHEAD slices at a time.
+// two bf16 numbers (2^-16 of it), rows of kStride; zeros up to whole tiles.  A thread takes four columns of a row, and
+// four slices at a time.
 // (The thread's number is hidden from the compiler: it would work the places out ahead of the loop that stages now and
 // then, and keep them in registers that the loop needs.)
-template <int kCols, int kStride, int ITEMS, int AHEAD>
+template <int kCols, int kStride>
 __device__ __forceinline__ void stage_h(const float* h, int R, int rank, int tokens, int n_slices, int step, float s,
                                         uint16_t* hi, uint16_t* lo) {
+    constexpr int kAhead = 4;
     const int items = (tokens + 15) / 16 * 16 * (kCols / 4);
     int thread = threadIdx.x;
     asm volatile("" : "+r"(thread));
-    for (int e0 = thread; e0 < items; e0 += ITEMS * kThreads) {
-        float4 v[ITEMS];
-        int at[ITEMS];
-#pragma unroll
-        for (int j = 0; j < ITEMS; j++) {
-            const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
-            v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            at[j] = row < tokens && col < rank ? row * R + col : -1;
-        }
+    for (int e = thread; e < items; e += kThreads) {
+        const int row = e / (kCols / 4), col = e % (kCols / 4) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (row < tokens && col < rank) {
+            const float* from = h + row * R + col;
 #pragma unroll 1
-        for (int q0 = 0; q0 < n_slices; q0 += AHEAD) {
-            float4 o[ITEMS][AHEAD];
+            for (int q0 = 0; q0 < n_slices; q0 += kAhead) {
+                float4 o[kAhead];
 #pragma unroll
-            for (int q = 0; q < AHEAD; q++)
+                for (int q = 0; q < kAhead; q++)
+                    if (q0 + q < n_slices) o[q] = *reinterpret_cast<const float4*>(from + (q0 + q) * step);
 #pragma unroll
-                for (int j = 0; j < ITEMS; j++)
-                    if (at[j] >= 0 && q0 + q < n_slices)
-                        o[j][q] = *reinterpret_cast<const float4*>(h + (q0 + q) * step + at[j]);
-#pragma unroll
-            for (int q = 0; q < AHEAD; q++)
-#pragma unroll
-                for (int j = 0; j < ITEMS; j++)
-                    if (at[j] >= 0 && q0 + q < n_slices)
-                        v[j].x += o[j][q].x, v[j].y += o[j][q].y, v[j].z += o[j][q].z, v[j].w += o[j][q].w;
+                for (int q = 0; q < kAhead; q++)
+                    if (q0 + q < n_slices) v.x += o[q].x, v.y += o[q].y, v.z += o[q].z, v.w += o[q].w;
+            }
         }
-#pragma unroll
-        for (int j = 0; j < ITEMS; j++) {
-            const int e = e0 + j * kThreads, row = e / (kCols / 4), col = e % (kCols / 4) * 4;
-            if (e < items) split_h(v[j], s, hi + row * kStride + col, lo + row * kStride + col);
-        }
+        split_h(v, s, hi + row * kStride + col, lo + row * kStride + col);
     }
 }
 
@@ -667,7 +656,8 @@ __device__ __forceinline__ uint4 odd_row(const uint16_t* base, int col, int N) {
 }
 
 // Adds a lane's eight results (row h * 8 + g of a tile) to the base `v`, to `y`: columns col .. col + 7 of N.
-__device__ __forceinline__ void add_row(uint16_t* y, const uint4& v, const float (&acc)[4][4], int h, bool vec, int col, int N) {
+__device__ __forceinline__ void add_row(uint16_t* y, const uint4& v, const float (&acc)[4][4], int h, bool vec, int col,
+                                        int N) {
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t out[4];
 #pragma unroll
@@ -705,8 +695,8 @@ __device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, co
         if (held != c * a.count + i) {
             held = c * a.count + i;
             __syncthreads();
-            stage_h<kCols, kStride, 2, 2>(a.h + cut.many_row(c, 0) * R + i * rank, R, rank, chunk.z, cut.many_slices, kChunk * R,
-                                    a.scales[chunk.x], hi, lo);
+            stage_h<kCols, kStride>(a.h + cut.many_row(c, 0) * R + i * rank, R, rank, chunk.z, cut.many_slices,
+                                    kChunk * R, a.scales[chunk.x], hi, lo);
             if (threadIdx.x < kChunk)
                 rows[threadIdx.x] =
                     static_cast<int32_t>(token_at(a, p, chunk.y + min(static_cast<int>(threadIdx.x), chunk.z - 1)));
@@ -840,7 +830,7 @@ __device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, con
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(b + static_cast<int64_t>(row) * rank));
             }
             __syncthreads();
-            stage_h<kCols, kStride, 1, 4>(a.h + cut.few_row(p.n_many, c, 0) * R + i * rank, R, rank, chunk.z, cut.few_slices,
+            stage_h<kCols, kStride>(a.h + cut.few_row(p.n_many, c, 0) * R + i * rank, R, rank, chunk.z, cut.few_slices,
                                     kFew * R, a.scales[chunk.x], hi, lo);
             __syncthreads();
         }
