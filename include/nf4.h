@@ -474,8 +474,10 @@ nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, i
  *   logprobs     out  float [B] or NULL: log softmax(l) of the token, before temperature and cuts
  * V in 1 .. 262144, stride >= V, B at most 2^24; everything is aligned to its elements (rows may start anywhere).
  * Logits of -inf (masked) and NaN have no weight; a row with nothing else gives token -1 and logprob -inf, one with
- * +inf the first of n such and logprob -log n.  Weights are whole multiples of 2^-40 (each within 2^-30 of its size, or half a multiple), so
- * sums are exact and the drawn token does not depend on their order; what weighs less than half a multiple is never drawn.
+ * +inf the first of n such and logprob -log n.  Weights are whole multiples of 2^-40 (each within 1.1 * 2^-30 of its size,
+ * or half a multiple), so sums are exact and the drawn token does not depend on their order; what weighs less than half a
+ * multiple is never drawn.  So the borders between tokens lie within 2^-30 of the whole of where the formula has them, plus
+ * V * 2^-41 where many tokens weigh only a few multiples.
  */
 nf4_status nf4_sample(const void* logits, int logits_bf16, int64_t B, int64_t V, int64_t stride, const float* temperature,
                       const int32_t* top_k, const float* top_p, const float* min_p, const float* random, int32_t* tokens,

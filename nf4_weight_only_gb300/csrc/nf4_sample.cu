@@ -4,7 +4,7 @@
 // beginning of the tokens ordered by logit (ties: the lower index first); the token drawn is the first index i, in
 // index order, at which the sum of the kept weights up to i passes u times their whole sum.
 //
-// Sums are exact: a weight is a whole number of 2^-40 (within 2^-30 of its own size of the exponential, or half
+// Sums are exact: a weight is a whole number of 2^-40 (within 1.1 * 2^-30 of its own size of the exponential, or half
 // a unit), and sums of up to 2^18 of them fit 64 bits.  So no order of addition, number of CTAs or atomic changes a
 // result, and since the weights' errors do not add up (each is rounded by itself), the border between two of 150,000
 // equal tokens is within some 10^-5 of a token of where the formula has it; sums in fp32 move it by hundredths.
@@ -92,7 +92,8 @@ struct Row {
 };
 
 // 2^40 exp((l - top) / T) of two logits.  y = log2(e) (top - l) / T, in two floats, is k / 1024 + r; 2^(-k / 1024)
-// is a table's entry and a shift, 2^-r = 1 - p + p^2 / 2 with p = r ln 2 < 2^-11 (the next term is below 2^-37).
+// is a table's entry and a shift, 2^-r = 1 - p + p^2 / 2 with p = r ln 2 < 2^-11.5 (the next term is below 2^-37).  The
+// entry and the correction are rounded to 31 bits, half of 2^-30 each, and fp32 adds a tenth: 1.1 * 2^-30.
 __device__ __forceinline__ void weights_of(float l0, float l1, const Row& row, const uint32_t* table, uint64_t (&w)[2]) {
     const Pair l(l0, l1), top(row.top), minus(-1.0f), c_hi(row.c_hi);
     const Pair s = fma2(l, minus, top), b = s + Pair(-row.top);
@@ -107,7 +108,8 @@ __device__ __forceinline__ void weights_of(float l0, float l1, const Row& row, c
     for (int j = 0; j < 2; j++) {
         const uint32_t k = __float_as_uint(j ? zs.y : zs.x), n = (k >> 10) & 63u;  // (1.5 * 2^23 adds no bit to either)
         const uint32_t t = table[k & 1023u];
-        const uint32_t m = t - (__mulhi(static_cast<int>(t >> 1), __float2int_rn(j ? q.y : q.x)) >> 8);
+        // (rounded: cut, the weights were too large by 0.35 * 2^-30 on average, and by up to 1.5 * 2^-30)
+        const uint32_t m = t - ((__mulhi(static_cast<int>(t >> 1), __float2int_rn(j ? q.y : q.x)) + 128) >> 8);
         uint64_t v;
         if (n >= 10)
             v = (static_cast<uint64_t>(m) * (1u << ((41u - n) & 31u)) + 0x80000000u) >> 32;
