@@ -19,6 +19,7 @@
 #include <mutex>
 
 #include "nf4_kv.cuh"
+#include "nf4_lora_index.h"
 
 namespace nf4 {
 namespace {
@@ -824,10 +825,12 @@ __device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, con
         if (held != c * a.count + i) {
             held = c * a.count + i;
             // B starts on its way to L2 meanwhile
+            if (lane_in_row(Weights<W>::kLane, t, rank)) {
 #pragma unroll
-            for (int j = 0; j < 4 * D; j++) {
-                const int row = min(j / 4 * 256 + j % 4 * 2, last_row);
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(b + static_cast<int64_t>(row) * rank));
+                for (int j = 0; j < 4 * D; j++) {
+                    const int row = min(j / 4 * 256 + j % 4 * 2, last_row);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(b + static_cast<int64_t>(row) * rank));
+                }
             }
             __syncthreads();
             stage_h<kCols, kStride>(a.h + cut.few_row(p.n_many, c, 0) * R + i * rank, R, rank, chunk.z, cut.few_slices,

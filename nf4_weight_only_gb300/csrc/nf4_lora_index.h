@@ -1,0 +1,17 @@
+// Index rules of the adapters' kernels that keep their accesses inside the caller's arrays, apart from the kernels so that
+// a host program can check them over all sizes.
+#pragma once
+
+#ifdef __CUDACC__
+#define NF4_INDEX __host__ __device__ __forceinline__
+#else
+#define NF4_INDEX inline
+#endif
+
+namespace nf4 {
+
+// Four lanes share a row of B, lane t from value values * t on: whether the row has that value.  (At rank 8 lanes 2 and 3,
+// at rank 24 lane 3, have none; behind the last row of the last adapter their place is past the end of B.)
+NF4_INDEX bool lane_in_row(int values, int t, int rank) { return values * t < rank; }
+
+}  // namespace nf4
