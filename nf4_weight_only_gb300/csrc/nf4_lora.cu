@@ -710,7 +710,7 @@ __device__ __forceinline__ void expand_many(const LoraArgs& a, const Plan& p, co
         uint16_t* y = a.y[i] + n;
         const uint16_t* b = a.b[i] + (static_cast<int64_t>(chunk.x) * N + first_row) * rank + Weights<W>::kLane * t;
         Weights<W> w;
-        if (EXACT && block.first + 256 <= N)
+        if (EXACT && whole_blocks(block.first, N, 1))
             w.load_whole(b, 0);
         else
             w.load(b, 0, N - 1 - first_row, rank, t);
@@ -766,21 +766,23 @@ __device__ __forceinline__ void copy_idle(const LoraArgs& a, const Plan& p, int 
             int64_t at[8];
 #pragma unroll
             for (int q = 0; q < 8; q++) {
-                const int r = q % rounds * 8 + g, col = n + q / rounds * 256;
-                at[q] = q < batch * rounds && r < tokens && col < N ? token_at(a, p, first + r) * N + col : -1;
+                const int r = q % rounds * 8 + g, more = q / rounds * 256;
+                at[q] = q < batch * rounds && r < tokens && column_there(n, more, N)
+                            ? token_at(a, p, first + r) * N + n + more
+                            : -1;
                 if (at[q] >= 0) v[q] = *reinterpret_cast<const uint4*>(base + at[q]);
             }
 #pragma unroll
             for (int q = 0; q < 8; q++)
                 if (at[q] >= 0) *reinterpret_cast<uint4*>(y + at[q]) = v[q];
         } else {
-            for (int col = n0 + lane; col < N && col < n0 + batch * 256; col += 256)
+            for (int more = 0; more < batch * 256 && column_there(n0 + lane, more, N); more += 256)
                 for (int r = 0; r < tokens; r += 8) {  // loads before stores, which may not pass each other
                     uint16_t v[8];
                     int64_t at[8];
 #pragma unroll
                     for (int q = 0; q < 8; q++) {
-                        at[q] = token_at(a, p, first + min(r + q, tokens - 1)) * N + col;
+                        at[q] = token_at(a, p, first + min(r + q, tokens - 1)) * N + n0 + lane + more;
                         v[q] = base[at[q]];
                     }
 #pragma unroll
@@ -841,7 +843,7 @@ __device__ __forceinline__ void expand_few(const LoraArgs& a, const Plan& p, con
         const int64_t at[2] = {static_cast<int64_t>(token[0]) * N, static_cast<int64_t>(token[1]) * N};
         Weights<W> w[D];
         uint4 in[D][2];
-        if (EXACT && vec && block.first + 256 * D <= N && left >= D) {
+        if (EXACT && vec && whole_blocks(block.first, N, D) && left >= D) {
 #pragma unroll
             for (int d = 0; d < D; d++) w[d].load_whole(b, 256 * d);
 #pragma unroll

@@ -14,4 +14,10 @@ namespace nf4 {
 // at rank 24 lane 3, have none; behind the last row of the last adapter their place is past the end of B.)
 NF4_INDEX bool lane_in_row(int values, int t, int rank) { return values * t < rank; }
 
+// Columns of a projection, of which there are up to 2^31 - 1: a sum of two could pass that, their difference cannot.
+// Whether so many blocks of 256 from column `first` on (below N) are whole; whether column from + more (from at most N + 255)
+// is there.
+NF4_INDEX bool whole_blocks(int first, int N, int blocks) { return N - first >= 256 * blocks; }
+NF4_INDEX bool column_there(int from, int more, int N) { return more < N - from; }
+
 }  // namespace nf4

@@ -12,6 +12,8 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PROGRAM = r"""
 #include "nf4_lora_index.h"
 extern "C" int lane_in_row(int values, int t, int rank) { return nf4::lane_in_row(values, t, rank); }
+extern "C" int whole_blocks(int first, int N, int blocks) { return nf4::whole_blocks(first, N, blocks); }
+extern "C" int column_there(int from, int more, int N) { return nf4::column_there(from, more, N); }
 """
 
 
@@ -22,7 +24,7 @@ def rules(tmp_path_factory):
     source.write_text(PROGRAM)
     compiler = shutil.which(os.environ.get("CXX", "g++"))
     assert compiler, "no C++ compiler"
-    subprocess.run([compiler, "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
+    subprocess.run([compiler, "-std=c++17", "-O1", "-Wall", "-Werror", "-ftrapv", "-shared", "-fPIC", "-I",
                     os.path.join(ROOT, "nf4_weight_only_gb300", "csrc"), str(source), "-o", str(out)], check=True)
     return ctypes.CDLL(str(out))
 
@@ -37,3 +39,18 @@ def test_lanes_that_start_in_a_row(rules):
         covered = {s + step + i for s in starts for step in range(0, rank, 4 * values) for i in range(values)
                    if s + step < rank}
         assert covered == set(range(rank))
+
+
+@pytest.mark.parametrize("n", [1, 8, 255, 256, 257, 511, 512, 513, 5000, (1 << 31) - 513, (1 << 31) - 512, (1 << 31) - 257,
+                               (1 << 31) - 256, (1 << 31) - 255, (1 << 31) - 8, (1 << 31) - 1])
+def test_blocks_and_columns_up_to_the_widest(rules, n):
+    """Python's integers do not overflow; the last blocks of the widest projections end past 2^31."""
+    last = (n + 255) // 256 * 256 - 256
+    for first in range(max(0, last - 2048), last + 1, 256):
+        for blocks in (1, 2):
+            assert rules.whole_blocks(first, n, blocks) == (first + 256 * blocks <= n)
+        for inside in range(0, 256, 8):
+            for more in range(0, 8 * 256, 256):
+                assert rules.column_there(first + inside, more, n) == (first + inside + more < n)
+    # a lane's column in a block that the row ends inside, as far as 2^31 - 1 reaches
+    assert not rules.column_there(min(n + 255, (1 << 31) - 1), 0, n)
