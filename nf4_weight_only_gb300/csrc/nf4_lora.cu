@@ -254,7 +254,7 @@ __device__ __forceinline__ bool read_plan(const LoraArgs& a, Plan* p) {
     return true;
 }
 __device__ __forceinline__ bool chunk_ok(const LoraArgs& a, const Plan& p, const int4& c, int most) {
-    return c.x >= 0 && c.x < a.adapters && c.y >= 0 && c.z > 0 && c.z <= most && c.y + c.z <= p.n_tokens;
+    return chunk_in_lists(c.x, c.y, c.z, most, a.adapters, p.n_tokens);
 }
 __device__ __forceinline__ int64_t token_at(const LoraArgs& a, const Plan& p, int at) {
     return min(static_cast<uint32_t>(p.order[at]), static_cast<uint32_t>(a.T - 1));

@@ -20,4 +20,9 @@ NF4_INDEX bool lane_in_row(int values, int t, int rank) { return values * t < ra
 NF4_INDEX bool whole_blocks(int first, int N, int blocks) { return N - first >= 256 * blocks; }
 NF4_INDEX bool column_there(int from, int more, int N) { return more < N - from; }
 
+// Whether a chunk of the plan (an adapter, its first place in the order, its tokens) is inside the lists, whatever its words say.
+NF4_INDEX bool chunk_in_lists(int adapter, int first, int tokens, int most, long long adapters, int listed) {
+    return adapter >= 0 && adapter < adapters && tokens > 0 && tokens <= most && first >= 0 && first <= listed - tokens;
+}
+
 }  // namespace nf4

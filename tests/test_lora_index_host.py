@@ -14,6 +14,9 @@ PROGRAM = r"""
 extern "C" int lane_in_row(int values, int t, int rank) { return nf4::lane_in_row(values, t, rank); }
 extern "C" int whole_blocks(int first, int N, int blocks) { return nf4::whole_blocks(first, N, blocks); }
 extern "C" int column_there(int from, int more, int N) { return nf4::column_there(from, more, N); }
+extern "C" int chunk_in_lists(int adapter, int first, int tokens, int most, long long adapters, int listed) {
+    return nf4::chunk_in_lists(adapter, first, tokens, most, adapters, listed);
+}
 """
 
 
@@ -54,3 +57,16 @@ def test_blocks_and_columns_up_to_the_widest(rules, n):
                 assert rules.column_there(first + inside, more, n) == (first + inside + more < n)
     # a lane's column in a block that the row ends inside, as far as 2^31 - 1 reaches
     assert not rules.column_there(min(n + 255, (1 << 31) - 1), 0, n)
+
+
+def test_chunks_of_any_words(rules):
+    """A plan's words may be anything: what passes is inside the order's tokens and the loaded adapters."""
+    words = [0, 1, 2, 16, 17, 63, 64, 65, 100, 1 << 24, (1 << 31) - 65, (1 << 31) - 64, (1 << 31) - 2, (1 << 31) - 1, -1, -64,
+             -(1 << 31)]
+    for adapter in (0, 2, 3, (1 << 31) - 1, -1):
+        for first in words:
+            for tokens in words:
+                for most, listed in ((16, 0), (16, 100), (64, 100), (64, 1 << 24)):
+                    inside = 0 <= adapter < 3 and first >= 0 and 1 <= tokens <= most and first + tokens <= listed
+                    got = rules.chunk_in_lists(adapter, first, tokens, most, ctypes.c_longlong(3), listed)
+                    assert bool(got) == inside, (adapter, first, tokens, most, listed)
