@@ -402,7 +402,7 @@ nf4_status nf4_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16
  *   free_in      in   int64 [2]
  *   free_out     out  int64 [2]; may be free_in
  *   lengths_out  out  int32 [B]; may be lengths
- *   starts       out  int32 [B + 1]; starts[B] is the number of new tokens (sums stop at 2^31-1)
+ *   starts       out  int32 [B + 1]; starts[B] is the number of new tokens (sums stop at 2^31-1, which counts as past row T)
  *   slots        out  int64 [T], what nf4_kv_append takes: page * page_size + offset; -1 for the tokens of a
  *                     refused sequence and for rows from starts[B] on
  *   positions    out  int32 [T], lengths[b] + i for token i of sequence b; 0 from row starts[B] on
@@ -447,8 +447,10 @@ nf4_status nf4_lora_plan(const int32_t* ids, const int32_t* sequences, int64_t S
  *   ys         host array; ys[i]: bf16 bits [T][Ns[i]]; may be its own base, no other overlap
  *   workspace  nf4_lora_workspace_bytes(T, adapters, rank, count) bytes on the device; needs no set-up.  Calls that
  *              may overlap on the GPU need one each
- * Sums are fp32; scales[a] * h_r goes into the second product as the sum of two bf16 numbers (2^-16 of it).  The
- * host arrays are read before the call returns.  A plan of other sizes records code 47, and nothing is computed.
+ * Sums are fp32; scales[a] * h_r goes into the second product as the sum of two bf16 numbers (2^-16 of it; past bf16's range,
+ * 3.39e38, as an infinity).  The order of the sums follows from the call's sizes and from how its tokens share the adapters:
+ * the same call gives the same bytes, a token beside other tokens the same within rounding.  The host arrays are read before
+ * the call returns.  A plan of other sizes records code 47, and nothing is computed.
  */
 int64_t nf4_lora_workspace_bytes(int64_t T, int64_t adapters, int64_t rank, int64_t count);
 nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, int64_t plan_bytes, int64_t adapters,
@@ -471,7 +473,8 @@ nf4_status nf4_lora(const uint16_t* x, int64_t T, int64_t K, const void* plan, i
  *   min_p        in   float [B]; 0 or less: all.  NULL: all
  *   random       in   float [B] in [0, 1)
  *   tokens       out  int32 [B]
- *   logprobs     out  float [B] or NULL: log softmax(l) of the token, before temperature and cuts
+ *   logprobs     out  float [B] or NULL: log softmax(l) of the token, before temperature and cuts, its sum in fp32 by the
+ *                     hardware's exp2: off by 2^-17 + 2^-22 of its size at most, by some 4e-8 on a model's logits
  * V in 1 .. 262144, stride >= V, B at most 2^24; everything is aligned to its elements (rows may start anywhere).
  * Logits of -inf (masked) and NaN have no weight; a row with nothing else gives token -1 and logprob -inf, one with
  * +inf the first of n such and logprob -log n.  Weights are whole multiples of 2^-40 (each within 1.1 * 2^-30 of its size,

@@ -984,7 +984,8 @@ cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     // Ranks of exactly 16, 32, 64 and 128 have constants for addresses (o of 8191 tokens 89 -> 85 us).  D is what registers
-    // allow (rank 16, gate|up of 64 tokens: 30.3 us with 2, 34 with 1, 32 with 4, which spills).
+    // allow (rank 16, gate|up of 64 tokens: 30.3 us with 2, 34 with 1, 32 with 4, which spills).  At two CTAs an SM the higher
+    // ranks spill all the same: 32 bytes at 32, 12 at 64, 204 to 224 at 128.
 #define NF4_EXPAND(W, D) \
     return a.rank == Weights<W>::kCols ? expand<W, D, true>(a, num_sms, stream) : expand<W, D, false>(a, num_sms, stream)
     if (a.rank <= 16) NF4_EXPAND(0, 2);
